@@ -258,6 +258,66 @@ int externd_matvec(const uint8_t* Bt, const float* D, const uint8_t* C, int64_t 
 int externd_pack_mask_sign(const uint8_t* T, int64_t rows, int64_t len, uint8_t* mask_out, uint32_t* sign_out,
                            int64_t sign_words, int64_t* sign_offsets_out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 4-bit weights with group scales, and the gated feed-forward block.
+ *
+ * The uniform 4-bit format is what the pages compare the ternary factors with, and the gated
+ * block is where a model's MLP matrices are used.  All pointers are DEVICE pointers of the
+ * current device (EXTERND_EINVAL otherwise).  Matrices are row-major with an explicit leading
+ * dimension in ELEMENTS (at least the number of columns); element types are EXTERND_F32,
+ * EXTERND_F16 or EXTERND_BF16.  Calls are stream-ordered and asynchronous unless noted; they
+ * allocate nothing and keep nothing between calls, so they can be captured into CUDA graphs.
+ * Outputs must not overlap inputs.  Sums are held in fp32.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { EXTERND_F32 = 0, EXTERND_F16 = 1, EXTERND_BF16 = 2 } externd_dtype;
+
+/* act(g): silu g / (1 + e^-g); gelu g Phi(g) (Phi the normal distribution function); gelu_tanh
+ * 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))); relu2 max(g, 0)^2. */
+typedef enum {
+    EXTERND_ACT_SILU = 0,
+    EXTERND_ACT_GELU = 1,
+    EXTERND_ACT_GELU_TANH = 2,
+    EXTERND_ACT_RELU2 = 3
+} externd_act;
+
+/* Bytes of one row of n 4-bit codes: 64 ceil(n / 128).  0 for n < 1. */
+size_t externd_int4_row_bytes(int64_t n);
+
+/* Quantise A (m x n) to w = s (q - 8) + b, q in 0..15, s and b fp16 per row and group of `group`
+ * columns (32, 64 or 128; the last group may be shorter).
+ *   offset_out NULL: symmetric, s = max |A| / 7, b = 0.  Otherwise affine: s = (max - min) / 15,
+ *              b = min + 8 s.  s and b are computed in fp64 and rounded to fp32, then to fp16;
+ *              q = clamp(round_to_even((A - b) / s) + 8, 0, 15), decided as in fp64; 8 where s = 0.
+ *   q_out      [out] m rows of externd_int4_row_bytes(n), 16-byte aligned.  A row is blocks of 128
+ *              columns and 64 bytes; column 128 B + 32 i + 8 c + t (i, c < 4, t < 8) is nibble
+ *              4 (t % 2) + t / 2 of 32-bit word 4 c + i of block B.  Padding columns hold 8.
+ *   scale_out, offset_out [out] ceil(n / group) rows of m fp16 values: one row per group.
+ *   async_status  NULL: the call is synchronous and returns the status.  Otherwise a device int
+ *              that receives it when the stream gets there (as for the factorizations).
+ * EXTERND_ENONFINITE if A holds NaN or Inf, EXTERND_ELIMIT if a scale or offset leaves the fp16
+ * range (max |A| about 65504); the outputs of the groups concerned are then unspecified. */
+int externd_int4_quantize(const void* A, int dtype, int64_t m, int64_t n, int64_t lda, int group, uint8_t* q_out,
+                          void* scale_out, void* offset_out, int* async_status, void* stream);
+
+/* out (m x n, type dtype) = s (q - 8) + b, rounded once.  offset NULL: b = 0. */
+int externd_int4_dequantize(const uint8_t* q, const void* scale, const void* offset, int64_t m, int64_t n, int group,
+                            void* out, int dtype, int64_t ldo, void* stream);
+
+/* Y = X W^T: Y[t] = W X[t] for t < batch (X batch x n, Y batch x m, both of type dtype; batch 0
+ * does nothing).  q as externd_int4_quantize lays it out, 16-byte aligned; offset NULL: b = 0.
+ * The codes enter the products exactly and each group's sum is scaled in fp32; fp32 inputs are
+ * split without loss.  |X| up to 2^115: beyond that, and for infinite entries, a sum may become
+ * inf or NaN before it is scaled.  Rows of X do not influence one another. */
+int externd_int4_matvec(const uint8_t* q, const void* scale, const void* offset, int64_t m, int64_t n, int group,
+                        const void* X, int dtype, int64_t ldx, int64_t batch, void* Y, int64_t ldy, void* stream);
+
+/* H = act(X Wg^T) * (X Wu^T), elementwise product, both matrices m x n in 4 bits with one group
+ * size; otherwise as externd_int4_matvec. */
+int externd_int4_gated(const uint8_t* qg, const void* scale_g, const void* offset_g, const uint8_t* qu,
+                       const void* scale_u, const void* offset_u, int64_t m, int64_t n, int group, int act,
+                       const void* X, int dtype, int64_t ldx, int64_t batch, void* H, int64_t ldh, void* stream);
+
 /* Human-readable message for a status code (static storage). */
 const char* externd_strerror(int status);
 

@@ -31,6 +31,11 @@ EXPORTS = (
     "externd_transpose_trits",
     "externd_matvec",
     "externd_pack_mask_sign",
+    "externd_int4_row_bytes",
+    "externd_int4_quantize",
+    "externd_int4_dequantize",
+    "externd_int4_matvec",
+    "externd_int4_gated",
 )
 
 
@@ -161,5 +166,15 @@ def load():
     L.externd_matvec.restype = c_int
     L.externd_pack_mask_sign.argtypes = [vp, i64, i64, vp, vp, i64, vp, vp]
     L.externd_pack_mask_sign.restype = c_int
+    L.externd_int4_row_bytes.argtypes = [i64]
+    L.externd_int4_row_bytes.restype = ctypes.c_size_t
+    L.externd_int4_quantize.argtypes = [vp, c_int, i64, i64, i64, c_int, vp, vp, vp, vp, vp]
+    L.externd_int4_quantize.restype = c_int
+    L.externd_int4_dequantize.argtypes = [vp, vp, vp, i64, i64, c_int, vp, c_int, i64, vp]
+    L.externd_int4_dequantize.restype = c_int
+    L.externd_int4_matvec.argtypes = [vp, vp, vp, i64, i64, c_int, vp, c_int, i64, i64, vp, i64, vp]
+    L.externd_int4_matvec.restype = c_int
+    L.externd_int4_gated.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, c_int, c_int, vp, c_int, i64, i64, vp, i64, vp]
+    L.externd_int4_gated.restype = c_int
     _lib = L
     return L

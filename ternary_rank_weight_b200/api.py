@@ -7,6 +7,7 @@ library stages them through device memory inside the call).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass, field
 from typing import Optional, Sequence
@@ -543,3 +544,200 @@ def pack_mask_sign(T: torch.Tensor, rows: int, length: int, *, stream=None):
     _check(rc, "externd_pack_mask_sign")
     total = int(offs[-1].item())
     return mask, signs[: (total + 31) // 32], offs
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights with group scales
+# ---------------------------------------------------------------------------
+
+_DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu2": 3}
+
+
+def _on_stream(stream, device):
+    """Temporaries and outputs come from the stream the kernels run on: torch's allocator may hand
+    their memory to later work of that stream only."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _rows_in(t, cols: int, name: str, like: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A 2-D CUDA tensor with `cols` columns of unit stride (copied otherwise) and one of the element
+    types; rows may be strided."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda or t.dtype not in _DTYPE:
+        raise ValueError(f"{name} must be a 2-D float32, float16 or bfloat16 CUDA tensor")
+    if t.shape[1] != cols:
+        raise ValueError(f"{name} must have {cols} columns, not {t.shape[1]}")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have the element type and device of the other tensors")
+    if t.shape[0] > 0 and (t.stride(1) != 1 and cols > 1 or t.shape[0] > 1 and t.stride(0) < cols):
+        t = t.contiguous()
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Leading dimension (rows of at most one element's worth may carry any stride)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _result(out, rows: int, cols: int, like: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty((rows, cols), dtype=like.dtype, device=like.device)
+    if (not isinstance(out, torch.Tensor) or tuple(out.shape) != (rows, cols) or out.dtype != like.dtype
+            or out.device != like.device or (cols > 1 and out.stride(1) != 1)
+            or (rows > 1 and out.stride(0) < cols)):
+        raise ValueError(f"out must be a {rows} x {cols} {like.dtype} tensor on {like.device} with unit column stride")
+    return out
+
+
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}")
+    return ACTS[act]
+
+
+def int4_row_bytes(n: int) -> int:
+    return int(_lib.load().externd_int4_row_bytes(int(n)))
+
+
+@dataclass
+class Int4Weights:
+    """An m x n matrix in 4 bits: w = scale (q - 8) + offset."""
+    q: torch.Tensor                  # uint8 [m, int4_row_bytes(n)] (pack_int4 gives the layout)
+    scale: torch.Tensor              # float16 [ceil(n / group), m]
+    offset: Optional[torch.Tensor]   # float16 [ceil(n / group), m]; None: symmetric
+    m: int
+    n: int
+    group: int                       # 32, 64 or 128 columns
+
+    def codes(self) -> np.ndarray:
+        """q on the host, m x n uint8."""
+        return unpack_int4(self.q.cpu().numpy(), self.n)
+
+
+def _check_int4(w: Int4Weights, device: Optional[torch.device] = None):
+    if not isinstance(w, Int4Weights) or w.m < 1 or w.n < 1 or w.group not in (32, 64, 128):
+        raise ValueError("w must be Int4Weights with m, n >= 1 and groups of 32, 64 or 128 columns")
+    groups = (w.n + w.group - 1) // w.group
+    want = [("q", w.q, (w.m, int4_row_bytes(w.n)), torch.uint8), ("scale", w.scale, (groups, w.m), torch.float16)]
+    if w.offset is not None:
+        want.append(("offset", w.offset, (groups, w.m), torch.float16))
+    for name, t, shape, dtype in want:
+        if (not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda
+                or not t.is_contiguous() or (device is not None and t.device != device)):
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape} on the vectors' device")
+
+
+def int4_quantize(A: torch.Tensor, group: int = 128, *, affine: bool = True, async_status=None,
+                  stream=None) -> Int4Weights:
+    """Round a matrix to 4 bits with fp16 scales (and, affine, offsets) per row and group of columns
+    (externd_int4_quantize).  A: 2-D float32, float16 or bfloat16 CUDA tensor.
+
+    async_status: a one-element int32 CUDA tensor: the call queues its work and returns at once; the
+    tensor receives the status when the stream gets there.  A must then need no copy (unit column
+    stride) and stay alive and unchanged until then."""
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a 2-D float32, float16 or bfloat16 CUDA tensor")
+    with _on_stream(stream, A.device):
+        A2 = _rows_in(A, A.shape[1], "A")
+        if async_status is not None:
+            if A2 is not A:
+                raise ValueError("an asynchronous call needs A with unit column stride")
+            if not (isinstance(async_status, torch.Tensor) and async_status.device == A.device
+                    and async_status.dtype == torch.int32 and async_status.numel() >= 1):
+                raise ValueError("async_status must be an int32 CUDA tensor")
+        m, n = A2.shape
+        if m < 1 or n < 1 or group not in (32, 64, 128):
+            raise ValueError("A must not be empty and group must be 32, 64 or 128")
+        groups = (n + group - 1) // group
+        q = torch.empty((m, int4_row_bytes(n)), dtype=torch.uint8, device=A2.device)
+        scale = torch.empty((groups, m), dtype=torch.float16, device=A2.device)
+        offset = torch.empty_like(scale) if affine else None
+        with _on_device(A2):
+            rc = _lib.load().externd_int4_quantize(_ptr(A2), _DTYPE[A2.dtype], m, n, _ld(A2), int(group), _ptr(q),
+                                                   _ptr(scale), _ptr(offset), _ptr(async_status),
+                                                   _stream(stream, A2.device))
+    _check(rc, "externd_int4_quantize")
+    return Int4Weights(q=q, scale=scale, offset=offset, m=m, n=n, group=int(group))
+
+
+def int4_dequantize(w: Int4Weights, dtype: torch.dtype = torch.float32, *, stream=None) -> torch.Tensor:
+    """The m x n matrix that the 4 bits stand for, rounded once to dtype (externd_int4_dequantize)."""
+    _check_int4(w)
+    if dtype not in _DTYPE:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
+    with _on_stream(stream, w.q.device):
+        out = torch.empty((w.m, w.n), dtype=dtype, device=w.q.device)
+        with _on_device(out):
+            rc = _lib.load().externd_int4_dequantize(_ptr(w.q), _ptr(w.scale), _ptr(w.offset), w.m, w.n, w.group,
+                                                     _ptr(out), _DTYPE[dtype], w.n, _stream(stream, out.device))
+    _check(rc, "externd_int4_dequantize")
+    return out
+
+
+def int4_matvec(w: Int4Weights, X: torch.Tensor, *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y = X W^T for X of shape (batch, n) or (n,), in X's element type (externd_int4_matvec)."""
+    return _int4_products((w,), X, 0, out, stream)
+
+
+def int4_gated(wg: Int4Weights, wu: Int4Weights, X: torch.Tensor, act: str = "silu", *,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """H = act(X Wg^T) * (X Wu^T) for X of shape (batch, n) or (n,), in X's element type
+    (externd_int4_gated); act: "silu", "gelu", "gelu_tanh" or "relu2"."""
+    if isinstance(wg, Int4Weights) and isinstance(wu, Int4Weights) and (wg.m, wg.n, wg.group) != (wu.m, wu.n, wu.group):
+        raise ValueError("both matrices must have the same shape and group")
+    return _int4_products((wg, wu), X, _act(act), out, stream)
+
+
+def _int4_products(ws, X, act: int, out, stream) -> torch.Tensor:
+    if not isinstance(X, torch.Tensor):
+        raise ValueError("X must be a CUDA tensor")
+    for w in ws:
+        _check_int4(w, X.device)
+    m, n = ws[0].m, ws[0].n
+    squeeze = X.dim() == 1
+    with _on_stream(stream, X.device):
+        X2 = _rows_in(X.unsqueeze(0) if squeeze else X, n, "X")
+        if out is not None and squeeze:
+            out = out.unsqueeze(0)
+        Y = _result(out, X2.shape[0], m, X2)
+        mats = [_ptr(t) for w in ws for t in (w.q, w.scale, w.offset)]
+        tail = [_ptr(X2), _DTYPE[X2.dtype], _ld(X2), X2.shape[0], _ptr(Y), _ld(Y), _stream(stream, X2.device)]
+        with _on_device(X2):
+            if len(ws) == 1:
+                rc = _lib.load().externd_int4_matvec(*mats, m, n, ws[0].group, *tail)
+            else:
+                rc = _lib.load().externd_int4_gated(*mats, m, n, ws[0].group, act, *tail)
+    _check(rc, "externd_int4_matvec" if len(ws) == 1 else "externd_int4_gated")
+    return Y[0] if squeeze else Y
+
+
+def _int4_places(n: int):
+    """Byte and shift of each column's nibble within a row."""
+    j = np.arange(n)
+    t, c, i, blk = j % 8, j // 8 % 4, j // 32 % 4, j // 128
+    nib = 4 * (t % 2) + t // 2
+    return 64 * blk + 4 * (4 * c + i) + nib // 2, (4 * (nib % 2)).astype(np.uint8)
+
+
+def unpack_int4(packed: np.ndarray, n: int) -> np.ndarray:
+    """uint8 rows (..., int4_row_bytes(n)) -> uint8 codes (..., n), 0..15."""
+    byte, shift = _int4_places(n)
+    return (np.asarray(packed, dtype=np.uint8)[..., byte] >> shift) & 15
+
+
+def pack_int4(codes: np.ndarray) -> np.ndarray:
+    """Codes 0..15 (..., n) -> uint8 (..., int4_row_bytes(n)); padding columns hold 8."""
+    codes = np.asarray(codes, dtype=np.uint8)
+    n = codes.shape[-1]
+    full = np.full((*codes.shape[:-1], (n + 127) // 128 * 128), 8, dtype=np.uint8)
+    full[..., :n] = codes
+    byte, shift = _int4_places(full.shape[-1])
+    out = np.zeros((*codes.shape[:-1], int4_row_bytes(n)), dtype=np.uint8)
+    low = shift == 0
+    out[..., byte[low]] = full[..., low]
+    out[..., byte[~low]] |= full[..., ~low] << np.uint8(4)
+    return out

@@ -1,0 +1,219 @@
+// Shared pieces of the 4-bit weight and gated feed-forward operators (sm_100a): element types,
+// activations with their derivatives, argument checks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "externd.h"
+
+namespace externd_llm {
+
+constexpr unsigned FULL = 0xffffffffu;
+
+// ---- element types -------------------------------------------------------------------------------
+
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// two fp32 values -> one register of two 16-bit values (lo in the low half)
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t v);
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+// ---- activations ---------------------------------------------------------------------------------
+//
+// silu       g s(g),                     s(g) = 1 / (1 + e^-g);     derivative s + g s (1 - s)
+// gelu       g P(g),                     P the normal distribution; derivative P + g e^{-g^2/2} / sqrt(2 pi)
+// gelu_tanh  g s(2y), y = sqrt(2/pi) (g + 0.044715 g^3);            derivative s + g s (1 - s) 2 y'
+// relu2      max(g, 0)^2;                                           derivative 2 max(g, 0)
+// e^-g overflows to +inf for g < -88: s is then 0 and g s is -0, the limit.
+//
+// PRECISE takes the full-precision exponential and division (fp32 results); the others are rounded to
+// 16 bits, which hides the few ulp (growing with |g|) of the hardware exponential.  P is taken as
+// erfc(-g / sqrt 2) / 2, which keeps its relative accuracy where P is small.
+
+template <bool PRECISE>
+__device__ __forceinline__ float sigmoid(float v) {
+    if constexpr (PRECISE) return 1.0f / (1.0f + expf(-v));
+    // 1 / y as computed here is 0 for y in 2^126..2^128 too (v below -87): the value there is below 1e-37
+    return __fdividef(1.0f, 1.0f + __expf(-v));
+}
+
+template <int ACT, bool PRECISE>
+__device__ __forceinline__ float act_fn(float g) {
+    if constexpr (ACT == EXTERND_ACT_SILU) {
+        return g * sigmoid<PRECISE>(g);
+    } else if constexpr (ACT == EXTERND_ACT_GELU) {
+        return 0.5f * g * erfcf(-0.70710678118654752f * g);
+    } else if constexpr (ACT == EXTERND_ACT_GELU_TANH) {
+        return g * sigmoid<PRECISE>(1.5957691216057308f * g * fmaf(0.044715f * g, g, 1.0f));
+    } else {
+        const float r = g > 0.0f ? g : g * 0.0f;   // 0 for g <= 0, NaN stays
+        return r * r;
+    }
+}
+
+// activation and derivative together
+template <int ACT, bool PRECISE>
+__device__ __forceinline__ float2 act_both(float g) {
+    if constexpr (ACT == EXTERND_ACT_SILU) {
+        const float s = sigmoid<PRECISE>(g), a = g * s;
+        return make_float2(a, fmaf(a, 1.0f - s, s));
+    } else if constexpr (ACT == EXTERND_ACT_GELU) {
+        const float p = 0.5f * erfcf(-0.70710678118654752f * g);
+        return make_float2(g * p, fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), p));
+    } else if constexpr (ACT == EXTERND_ACT_GELU_TANH) {
+        const float c = 0.044715f * g * g;
+        const float s = sigmoid<PRECISE>(1.5957691216057308f * g * (1.0f + c)), a = g * s;
+        return make_float2(a, fmaf(a * (1.0f - s), 1.5957691216057308f * fmaf(3.0f, c, 1.0f), s));
+    } else {
+        const float r = g > 0.0f ? g : g * 0.0f;
+        return make_float2(r * r, 2.0f * r);
+    }
+}
+
+template <bool PRECISE>
+__device__ __forceinline__ float act_rt(int act, float g) {
+    switch (act) {   // uniform over the launch
+        case EXTERND_ACT_SILU: return act_fn<EXTERND_ACT_SILU, PRECISE>(g);
+        case EXTERND_ACT_GELU: return act_fn<EXTERND_ACT_GELU, PRECISE>(g);
+        case EXTERND_ACT_GELU_TANH: return act_fn<EXTERND_ACT_GELU_TANH, PRECISE>(g);
+        default: return act_fn<EXTERND_ACT_RELU2, PRECISE>(g);
+    }
+}
+
+// ---- argument checks -----------------------------------------------------------------------------
+
+inline bool valid_dtype(int t) { return t == EXTERND_F32 || t == EXTERND_F16 || t == EXTERND_BF16; }
+inline size_t dtype_bytes(int t) { return t == EXTERND_F32 ? 4 : 2; }
+inline bool valid_act(int a) { return a >= EXTERND_ACT_SILU && a <= EXTERND_ACT_RELU2; }
+inline bool valid_group(int g) { return g == 32 || g == 64 || g == 128; }
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// memory that kernels on the current device may use
+inline bool on_device(const void* p) {
+    cudaPointerAttributes a;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    if (a.type == cudaMemoryTypeManaged) return true;
+    return a.type == cudaMemoryTypeDevice && a.device == dev;
+}
+
+inline int sm_count() {
+    int dev = 0, v = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+    cudaGetLastError();
+    return v;
+}
+
+// ---- warp-level matrix product ---------------------------------------------------------------------
+//
+// d += a b for a 16 x 16 and b 16 x 8, fp32 accumulation.  Lane 4 r + c holds a's rows r and r + 8 and b's
+// column r; the order of the 16 inner indices is free as long as a and b agree, so a lane takes
+// consecutive elements of its row.
+template <typename T> __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                               uint32_t a3, uint32_t b0, uint32_t b1);
+template <> __device__ __forceinline__ void mma16816<__half>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <> __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// ---- vectors as product operands -------------------------------------------------------------------
+
+// x = hi + mid + lo with bf16 terms; infinities and NaN stay in hi
+__device__ __forceinline__ void split3(float x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    const uint32_t u = __float_as_uint(x);
+    hi = u >> 16;
+    const bool special = (u & 0x7f800000u) == 0x7f800000u;
+    if (special && (u & 0x007fffffu)) hi |= 0x0040u;          // a NaN whose payload sits in the low half
+    const float r = special ? 0.0f : x - __uint_as_float(u & 0xffff0000u);
+    mid = __float_as_uint(r) >> 16;
+    const float r2 = r - __uint_as_float(__float_as_uint(r) & 0xffff0000u);
+    lo = __float_as_uint(r2) >> 16;
+}
+
+// eight consecutive entries of one vector as product operands
+template <typename T, int PLANES>
+struct XFrag { uint32_t v[PLANES][4]; };
+
+// X is the vector's row; entries from n on (and whole vectors, x == nullptr) are 0
+template <typename X, typename T, int PLANES, bool VEC>
+__device__ __forceinline__ void load_x(const X* __restrict__ x, int64_t k, int64_t n, XFrag<T, PLANES>& f) {
+    if (x == nullptr || k >= n) {
+        #pragma unroll
+        for (int p = 0; p < PLANES; ++p)
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) f.v[p][i] = 0;
+        return;
+    }
+    if constexpr (PLANES == 1) {
+        if (VEC && k + 8 <= n) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + k));
+            f.v[0][0] = v.x; f.v[0][1] = v.y; f.v[0][2] = v.z; f.v[0][3] = v.w;
+        } else {
+            const unsigned short* xs = reinterpret_cast<const unsigned short*>(x);
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a = k + 2 * i < n ? __ldg(xs + k + 2 * i) : 0;
+                const uint32_t b = k + 2 * i + 1 < n ? __ldg(xs + k + 2 * i + 1) : 0;
+                f.v[0][i] = a | (b << 16);
+            }
+        }
+    } else {
+        float e[8];
+        if (VEC && k + 8 <= n) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(x + k)), b = __ldg(reinterpret_cast<const float4*>(x + k) + 1);
+            e[0] = a.x; e[1] = a.y; e[2] = a.z; e[3] = a.w; e[4] = b.x; e[5] = b.y; e[6] = b.z; e[7] = b.w;
+        } else {
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = k + i < n ? __ldg(x + k + i) : 0.0f;
+        }
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t h0, m0, l0, h1, m1, l1;
+            split3(e[2 * i], h0, m0, l0);
+            split3(e[2 * i + 1], h1, m1, l1);
+            f.v[0][i] = h0 | (h1 << 16);
+            f.v[1][i] = m0 | (m1 << 16);
+            f.v[2][i] = l0 | (l1 << 16);
+        }
+    }
+}
+
+}  // namespace externd_llm

@@ -1,0 +1,60 @@
+"""Host-side checks of the 4-bit and gated feed-forward entry points: layouts, and refusals before any device
+work."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import ternary_rank_weight_b200 as ext
+from ternary_rank_weight_b200 import _lib
+
+EINVAL = ext.STATUS["EINVAL"]
+
+
+def test_int4_layout_follows_its_rule():
+    assert [ext.int4_row_bytes(n) for n in (0, 1, 128, 129, 6912)] == [0, 64, 64, 128, 3456]
+    n = 300
+    codes = np.random.default_rng(1).integers(0, 16, size=(5, n)).astype(np.uint8)
+    packed = ext.pack_int4(codes)
+    assert packed.shape == (5, ext.int4_row_bytes(n))
+    assert np.array_equal(ext.unpack_int4(packed, n), codes)
+    words = packed.view("<u4")
+    for j in range(384):                                   # column 128 B + 32 i + 8 c + t, padding 8
+        blk, i, c, t = j // 128, j // 32 % 4, j // 8 % 4, j % 8
+        got = (words[:, 16 * blk + 4 * c + i] >> (4 * (4 * (t % 2) + t // 2))) & 15
+        assert np.array_equal(got, codes[:, j] if j < n else np.full(5, 8)), j
+
+
+def test_int4_entry_points_reject_bad_arguments_before_device_work():
+    L = _lib.load()
+    host = (ctypes.c_uint8 * 256)()
+    p = (ctypes.addressof(host) + 15) // 16 * 16
+    assert L.externd_int4_quantize(None, 0, 1, 1, 1, 32, p, p, None, None, None) == EINVAL
+    assert L.externd_int4_quantize(p, 0, 1, 1, 1, 32, p, p, None, None, None) == EINVAL        # host memory
+    assert L.externd_int4_quantize(p, 0, 0, 1, 1, 32, p, p, None, None, None) == EINVAL
+    assert L.externd_int4_quantize(p, 0, 1, 4, 3, 32, p, p, None, None, None) == EINVAL        # lda < n
+    assert L.externd_int4_quantize(p, 3, 1, 1, 1, 32, p, p, None, None, None) == EINVAL
+    assert L.externd_int4_quantize(p, 0, 1, 1, 1, 48, p, p, None, None, None) == EINVAL
+    assert L.externd_int4_dequantize(p, p, None, 1, 1, 32, p, 0, 1, None) == EINVAL            # host memory
+    assert L.externd_int4_dequantize(p, p, None, 1, 1, 32, None, 0, 1, None) == EINVAL
+    assert L.externd_int4_matvec(p, p, None, 1, 1, 32, p, 0, 1, 1, p, 1, None) == EINVAL       # host memory
+    assert L.externd_int4_matvec(p, p, None, 1, 1, 32, p, 0, 1, -1, p, 1, None) == EINVAL
+    assert L.externd_int4_gated(p, p, None, p, p, None, 1, 1, 32, 4, p, 0, 1, 1, p, 1, None) == EINVAL   # activation
+
+
+def test_int4_binding_rejects_bad_tensors():
+    cpu = torch.zeros(4, 128)
+    with pytest.raises(ValueError):
+        ext.int4_quantize(cpu)                                       # not on the GPU
+    with pytest.raises(ValueError):
+        ext.int4_quantize(np.zeros((4, 128), dtype=np.float32))
+    w = ext.Int4Weights(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(1, 4, dtype=torch.float16), None, 4, 128, 128)
+    with pytest.raises(ValueError):
+        ext.int4_dequantize(w)
+    with pytest.raises(ValueError):
+        ext.int4_matvec(w, cpu)
+    with pytest.raises(ValueError):
+        ext.int4_gated(w, w, cpu, "swish")
+    with pytest.raises(ValueError):
+        ext.int4_matvec(w, None)
