@@ -741,3 +741,112 @@ def pack_int4(codes: np.ndarray) -> np.ndarray:
     out[..., byte[low]] = full[..., low]
     out[..., byte[~low]] |= full[..., ~low] << np.uint8(4)
     return out
+
+
+# ---------------------------------------------------------------------------
+# gated feed-forward block with dense weights
+# ---------------------------------------------------------------------------
+
+def _dense_in(t, cols: int, name: str, like: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A 2-D float16 or bfloat16 CUDA tensor that the tile kernel can read: unit column stride, rows on 16-byte
+    boundaries (copied into such rows otherwise)."""
+    if isinstance(t, torch.Tensor) and t.dtype == torch.float32:
+        raise ValueError(f"{name} must be float16 or bfloat16")
+    t = _rows_in(t, cols, name, like)
+    if t.data_ptr() % 16 == 0 and (t.shape[0] < 2 or t.stride(0) % 8 == 0):
+        return t
+    padded = torch.empty((t.shape[0], (cols + 7) // 8 * 8), dtype=t.dtype, device=t.device)[:, :cols]
+    padded.copy_(t)
+    return padded
+
+
+def _ld8(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+def _check_status(async_status, device):
+    if async_status is not None and not (isinstance(async_status, torch.Tensor) and async_status.device == device
+                                         and async_status.dtype == torch.int32 and async_status.numel() >= 1):
+        raise ValueError("async_status must be an int32 CUDA tensor")
+
+
+def _gated_inputs(X, Wg, Wu):
+    if not isinstance(Wg, torch.Tensor) or Wg.dim() != 2 or Wg.shape[0] < 1 or Wg.shape[1] < 1:
+        raise ValueError("Wg must be a 2-D float16 or bfloat16 CUDA tensor")
+    m, n = Wg.shape
+    if not isinstance(X, torch.Tensor) or X.dim() < 1 or X.shape[-1] != n:
+        raise ValueError(f"X must be a CUDA tensor whose last dimension is {n}")
+    if not isinstance(Wu, torch.Tensor) or tuple(Wu.shape) != (m, n):
+        raise ValueError("Wg and Wu must have the same shape")
+    return m, n
+
+
+def _gated(X, Wg, Wu, act, save, out, async_status, stream):
+    m, n = _gated_inputs(X, Wg, Wu)
+    code = _act(act)
+    _check_status(async_status, X.device)
+    lead = X.shape[:-1]
+    with _on_stream(stream, X.device):
+        X2 = _dense_in(X.reshape(-1, n), n, "X")
+        Wg, Wu = _dense_in(Wg, n, "Wg", X2), _dense_in(Wu, n, "Wu", X2)
+        t = X2.shape[0]
+        if out is not None:
+            if not isinstance(out, torch.Tensor) or tuple(out.shape) != (*lead, m):
+                raise ValueError(f"out must have shape {(*lead, m)}")
+            out = out.view(-1, m)
+        H = _result(out, t, m, X2)
+        G = torch.empty((t, m), dtype=X2.dtype, device=X2.device) if save else None
+        U = torch.empty((t, m), dtype=X2.dtype, device=X2.device) if save else None
+        with _on_device(X2):
+            rc = _lib.load().externd_gated(_ptr(X2), _ld8(X2), _ptr(Wg), _ld8(Wg), _ptr(Wu), _ld8(Wu), _DTYPE[X2.dtype], m, n,
+                                           t, code, _ptr(H), _ld(H), _ptr(G) if t else None, _ptr(U) if t else None, m,
+                                           _ptr(async_status), _stream(stream, X2.device))
+    _check(rc, "externd_gated")
+    shape = (*lead, m)
+    return H.view(shape), G.view(shape) if save else None, U.view(shape) if save else None
+
+
+def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", *, out: Optional[torch.Tensor] = None,
+          async_status=None, stream=None) -> torch.Tensor:
+    """H = act(X Wg^T) * (X Wu^T) for X of shape (..., n) and Wg, Wu of shape (m, n), float16 or bfloat16
+    (externd_gated); act: "silu", "gelu", "gelu_tanh" or "relu2".  Rows that do not start on 16-byte boundaries
+    are copied first.  The call is asynchronous; autograd does not record it (gated_forward and
+    gated_backward are the training pair).  async_status: an int32 CUDA tensor that receives the status."""
+    return _gated(X, Wg, Wu, act, False, out, async_status, stream)[0]
+
+
+def gated_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", *, async_status=None, stream=None):
+    """(H, G, U): gated() with the projections G = X Wg^T and U = X Wu^T that gated_backward needs."""
+    return _gated(X, Wg, Wu, act, True, None, async_status, stream)
+
+
+def gated_backward(dH: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, G: torch.Tensor, U: torch.Tensor,
+                   act: str = "silu", *, need=(True, True, True), async_status=None, stream=None):
+    """(dX, dWg, dWu) from the gradient dH of gated_forward's H and the G and U it returned
+    (externd_gated_backward); need: which of the three to compute (None in place of the others)."""
+    m, n = _gated_inputs(X, Wg, Wu)
+    code = _act(act)
+    _check_status(async_status, X.device)
+    lead = X.shape[:-1]
+    for name, t in (("dH", dH), ("G", G), ("U", U)):
+        if not isinstance(t, torch.Tensor) or tuple(t.shape) != (*lead, m):
+            raise ValueError(f"{name} must have shape {(*lead, m)}")
+    with _on_stream(stream, X.device):
+        X2 = _dense_in(X.reshape(-1, n), n, "X")
+        Wg, Wu = _dense_in(Wg, n, "Wg", X2), _dense_in(Wu, n, "Wu", X2)
+        dH2, G2, U2 = (_rows_in(t.reshape(-1, m), m, name, X2) for name, t in (("dH", dH), ("G", G), ("U", U)))
+        if _ld(G2) != _ld(U2):
+            G2, U2 = G2.contiguous(), U2.contiguous()
+        t = X2.shape[0]
+        dX = torch.empty((t, n), dtype=X2.dtype, device=X2.device) if need[0] else None
+        dWg = torch.empty((m, n), dtype=X2.dtype, device=X2.device) if need[1] else None
+        dWu = torch.empty((m, n), dtype=X2.dtype, device=X2.device) if need[2] else None
+        nbytes = int(_lib.load().externd_gated_backward_work(m, t))
+        work = torch.empty((max(nbytes, 256),), dtype=torch.uint8, device=X2.device)
+        with _on_device(X2):
+            rc = _lib.load().externd_gated_backward(
+                _ptr(dH2), _ld(dH2), _ptr(X2), _ld8(X2), _ptr(Wg), _ld8(Wg), _ptr(Wu), _ld8(Wu), _ptr(G2), _ptr(U2), _ld(G2),
+                _DTYPE[X2.dtype], m, n, t, code, _ptr(dX), n, _ptr(dWg), _ptr(dWu), n, _ptr(work), nbytes, _ptr(async_status),
+                _stream(stream, X2.device))
+    _check(rc, "externd_gated_backward")
+    return dX.view(*lead, n) if need[0] else None, dWg, dWu

@@ -11,9 +11,15 @@
 //   DW   dG^T X and dU^T X as one list of tiles (both operands read along their columns, as stored).
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "llm_ops.cuh"
 
-namespace externd_gated {
+#ifndef GATED_CG
+#define GATED_CG 1
+#endif
+
+namespace externd_ffn {
 
 using namespace externd_llm;
 
@@ -67,17 +73,17 @@ constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;   // per wait, as for the fact
 
 // Wait for a phase.  Gives up after WAIT_LIMIT_NS, or when another warp of the CTA gave up: the CTA then
 // leaves its loops and the launch reports EXTERND_ETIMEOUT.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* quit) {
     if (mbar_try(bar, parity)) return true;
     uint64_t t0 = 0;
     for (;;) {
         #pragma unroll 1
         for (int i = 0; i < 32; ++i)
             if (mbar_try(bar, parity)) return true;
-        if (*abort) return false;
+        if (*quit) return false;
         const uint64_t t = timer_ns();
         if (t0 == 0) t0 = t;
-        else if (t - t0 > WAIT_LIMIT_NS) { *abort = 1; return false; }
+        else if (t - t0 > WAIT_LIMIT_NS) { *quit = 1; return false; }
     }
 }
 
@@ -147,6 +153,7 @@ struct GemmArgs {
     int rows, cols;          // outputs: FWD tokens x m; DX tokens x n; DW 2 x (m x n), rows = m
     int depth;               // FWD n; DX m (per half); DW tokens
     int tiles_r, tiles_c;    // tile grid (DW: tiles_r counts both matrices)
+    int half_r;              // DW: row tiles of one matrix
     int act;
     void* out0; int64_t ld0; // FWD H, DX dX, DW dWg
     void* out1; int64_t ld1; // FWD G, DW dWu (FWD: may be null)
@@ -218,14 +225,14 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t bars[2 * C::STAGES + 5];
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
+    __shared__ int quit_flag;
     const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;          // swizzle atoms are 1024-byte aligned
     unsigned char* const stg_base = raw + (base - smem_u32(raw)) + C::STAGES * C::STAGE;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 1 ? 0 : cluster_rank();
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::STAGES, tfull0 = empty0 + 8 * C::STAGES, tempty0 = tfull0 + 16,
                    drain = tempty0 + 16;
-    volatile int* const abort = &abort_flag;
+    volatile int* const quit = &quit_flag;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
             mbar_init(tempty0 + 8 * i, 4 * CG);                      // one arrival per epilogue warp of the pair
         }
         mbar_init(drain, 1);
-        abort_flag = 0;
+        quit_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -259,7 +266,6 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
     const int kbs = MODE == DX ? 2 * kb_half : kb_half;
     const int tiles = g.tiles_r * g.tiles_c;
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
-    const int half_r = g.tiles_r / 2;                                  // DW: row tiles of one matrix
 
     if (warp == 0 && lane == 0) {
         // ---- loads: each CTA fetches its 128 rows of A and its share of B; both complete on the leader's barrier
@@ -270,11 +276,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
             tile_at(t, g.tiles_r, g.tiles_c, tr, tc);
             const CUtensorMap *ma = &a0, *mb = MODE == FWD && CG == 2 && rank == 1 ? &b1 : &b0;
             int rr = tr;
-            if (MODE == DW && tr >= half_r) { ma = &a1; rr -= half_r; }
+            if (MODE == DW && tr >= g.half_r) { ma = &a1; rr -= g.half_r; }
             const int ar = rr * C::BM + 128 * (int)rank;               // first A row (FWD, DX: token; DW: row of the matrix)
             for (int kb = 0; kb < kbs; ++kb, ++it) {
                 const int s = it % C::STAGES;
-                if (!mbar_wait(empty0 + 8 * s, ((it / C::STAGES) & 1) ^ 1, abort)) { ok = false; break; }
+                if (!mbar_wait(empty0 + 8 * s, ((it / C::STAGES) & 1) ^ 1, quit)) { ok = false; break; }
                 const uint32_t sa = base + s * C::STAGE, sb = sa + 128 * BK * 2;
                 uint32_t bar = full0 + 8 * s;
                 if (rank == 0) mbar_expect(bar, CG * C::STAGE);
@@ -321,11 +327,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         bool ok = true;
         for (int t = first; t < tiles && ok; t += step, ++n) {
             const uint32_t acc = tmem + (n & 1) * ACC;
-            if (!mbar_wait(tempty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, abort)) break;
+            if (!mbar_wait(tempty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, quit)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             for (int kb = 0; kb < kbs; ++kb, ++it) {
                 const int s = it % C::STAGES;
-                if (!mbar_wait(full0 + 8 * s, (it / C::STAGES) & 1, abort)) { ok = false; break; }
+                if (!mbar_wait(full0 + 8 * s, (it / C::STAGES) & 1, quit)) { ok = false; break; }
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t sa = base + s * C::STAGE, sb = sa + 128 * BK * 2;
                 const uint64_t da = A_MN ? smem_desc(sa, box, 1024) : smem_desc(sa, 16, 1024);
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
             }
             if (ok) mma_commit<CG>(tfull0 + 8 * (n & 1));
         }
-        if (*abort) {
+        if (*quit) {
             // issued products end before the tensor memory is freed
             mma_commit<CG>(drain);
             const uint64_t t0 = timer_ns();
@@ -353,13 +359,13 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         for (int t = first; t < tiles; t += step, ++n) {
             int tr, tc;
             tile_at(t, g.tiles_r, g.tiles_c, tr, tc);
-            if (!mbar_wait(tfull0 + 8 * (n & 1), (n >> 1) & 1, abort)) break;
+            if (!mbar_wait(tfull0 + 8 * (n & 1), (n >> 1) & 1, quit)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + (n & 1) * ACC + ((uint32_t)(32 * w) << 16);
             T* out = (T*)g.out0;
             int64_t ld = g.ld0;
             int rr = tr;
-            if (MODE == DW && tr >= half_r) { out = (T*)g.out1; ld = g.ld1; rr -= half_r; }
+            if (MODE == DW && tr >= g.half_r) { out = (T*)g.out1; ld = g.ld1; rr -= g.half_r; }
             const int row0 = rr * C::BM + 128 * (int)rank + 32 * w;
             if constexpr (MODE == FWD) {
                 #pragma unroll 1
@@ -406,7 +412,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0 && abort_flag && g.status) atomicExch(g.status, EXTERND_ETIMEOUT);
+    if (threadIdx.x == 0 && quit_flag && g.status) atomicExch(g.status, EXTERND_ETIMEOUT);
     if constexpr (CG == 2) cluster_sync();
     if (warp == 1) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -414,3 +420,336 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
 }
+
+// ---------------------------------------------------------------------------------------------------
+// dG and dU from the saved projections
+// ---------------------------------------------------------------------------------------------------
+
+// Bound by memory: reads dH, G, U and writes dG, dU, 10 bytes per entry.  dG and dU are rounded to the
+// operands' type, which the tensor cores need (as the forward pass rounds G and U where it saves them).
+template <typename T, int ACT, bool VEC>
+__global__ void __launch_bounds__(256) gate_grad_kernel(const T* __restrict__ dh, int64_t lddh, const T* __restrict__ gs,
+                                                        const T* __restrict__ us, int64_t ldgu, int64_t rows, int64_t m,
+                                                        T* __restrict__ dg, T* __restrict__ du, int64_t ldw) {
+    const int64_t per = VEC ? (m + 7) / 8 : m;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / per, c = i - r * per;
+        if (VEC) {
+            const uint4 h4 = __ldg(reinterpret_cast<const uint4*>(dh + r * lddh) + c);
+            const uint4 g4 = __ldg(reinterpret_cast<const uint4*>(gs + r * ldgu) + c);
+            const uint4 u4 = __ldg(reinterpret_cast<const uint4*>(us + r * ldgu) + c);
+            const uint32_t hv[4] = {h4.x, h4.y, h4.z, h4.w}, gv[4] = {g4.x, g4.y, g4.z, g4.w}, uv[4] = {u4.x, u4.y, u4.z, u4.w};
+            uint32_t og[4], ou[4];
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 h = unpack2<T>(hv[e]), g = unpack2<T>(gv[e]), u = unpack2<T>(uv[e]);
+                const float2 a = act_both<ACT, false>(g.x), b = act_both<ACT, false>(g.y);
+                og[e] = pack2<T>(h.x * u.x * a.y, h.y * u.y * b.y);
+                ou[e] = pack2<T>(h.x * a.x, h.y * b.x);
+            }
+            *(reinterpret_cast<uint4*>(dg + r * ldw) + c) = make_uint4(og[0], og[1], og[2], og[3]);
+            *(reinterpret_cast<uint4*>(du + r * ldw) + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+        } else {
+            const float h = to_f32(dh[r * lddh + c]), g = to_f32(gs[r * ldgu + c]), u = to_f32(us[r * ldgu + c]);
+            const float2 a = act_both<ACT, false>(g);
+            dg[r * ldw + c] = from_f32<T>(h * u * a.y);
+            du[r * ldw + c] = from_f32<T>(h * a.x);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------
+// few tokens: stream the weights once
+// ---------------------------------------------------------------------------------------------------
+
+// A CTA takes 16 rows of both matrices and 8 NT tokens; its warps split the columns and meet in shared memory
+// in a fixed order.  Bound by the weights' bytes.  A tile of the tile kernel would leave most of its 128
+// token rows empty, and half of the SMs without a tile.
+template <typename T, int NT, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) dense_stream_kernel(const T* __restrict__ wg, int64_t ldg, const T* __restrict__ wu,
+                                                                 int64_t ldu, int64_t m, int64_t n, int act,
+                                                                 const T* __restrict__ x, int64_t ldx, int64_t tokens,
+                                                                 T* __restrict__ hout, int64_t ldh, T* __restrict__ gout,
+                                                                 T* __restrict__ uout, int64_t ldgu) {
+    constexpr int COLS = 8 * NT;
+    __shared__ float part[2][WARPS][16][COLS + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = lane >> 2, c = lane & 3;
+    const int64_t row0 = (int64_t)blockIdx.x * 16;
+    const int64_t ra = min(row0 + r, m - 1), rb = min(row0 + r + 8, m - 1);
+    const T* rows[4] = {wg + ra * ldg, wg + rb * ldg, wu + ra * ldu, wu + rb * ldu};
+    const T* xr[NT];
+    #pragma unroll
+    for (int t = 0; t < NT; ++t) xr[t] = 8 * t + r < tokens ? x + (8 * t + r) * ldx : nullptr;
+    float acc[2][NT][4] = {};
+    const int64_t blocks = (n + 63) / 64;
+    for (int64_t blk = warp; blk < blocks; blk += WARPS) {
+        XFrag<T, 1> w[2][4], xf[2][NT];
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t k = blk * 64 + 32 * i + 8 * c;
+            #pragma unroll
+            for (int j = 0; j < 4; ++j) load_x<T, T, 1, true>(rows[j], k, n, w[i][j]);
+            #pragma unroll
+            for (int t = 0; t < NT; ++t) load_x<T, T, 1, true>(xr[t], k, n, xf[i][t]);
+        }
+        #pragma unroll
+        for (int i = 0; i < 2; ++i)
+            #pragma unroll
+            for (int j = 0; j < 2; ++j)
+                #pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint32_t(&a)[4] = w[i][2 * j].v[0];
+                    const uint32_t(&b)[4] = w[i][2 * j + 1].v[0];
+                    const uint32_t(&v)[4] = xf[i][t].v[0];
+                    mma16816<T>(acc[j][t], a[0], b[0], a[1], b[1], v[0], v[1]);
+                    mma16816<T>(acc[j][t], a[2], b[2], a[3], b[3], v[2], v[3]);
+                }
+    }
+    #pragma unroll
+    for (int j = 0; j < 2; ++j)
+        #pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            part[j][warp][r][8 * t + 2 * c] = acc[j][t][0];
+            part[j][warp][r][8 * t + 2 * c + 1] = acc[j][t][1];
+            part[j][warp][r + 8][8 * t + 2 * c] = acc[j][t][2];
+            part[j][warp][r + 8][8 * t + 2 * c + 1] = acc[j][t][3];
+        }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 16 * COLS; e += WARPS * 32) {
+        const int rr = e & 15, cc = e >> 4;
+        if (row0 + rr >= m || cc >= tokens) continue;
+        float g = 0.0f, u = 0.0f;
+        #pragma unroll
+        for (int p = 0; p < WARPS; ++p) {
+            g += part[0][p][rr][cc];
+            u += part[1][p][rr][cc];
+        }
+        hout[cc * ldh + row0 + rr] = from_f32<T>(act_rt<false>(act, g) * u);
+        if (gout) {
+            gout[cc * ldgu + row0 + rr] = from_f32<T>(g);
+            uout[cc * ldgu + row0 + rr] = from_f32<T>(u);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------------------------------
+
+constexpr int64_t STREAM_TOKENS = 16;
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+    static const EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return (EncodeFn)p;
+    }();
+    return fn;
+}
+
+// rows x cols matrix, boxes of 64 columns (128 bytes) x box_rows; reads past the edges give 0
+bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows, int dtype) {
+    const EncodeFn fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, es[2] = {1, 1};
+    return fn(map, dtype == EXTERND_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p),
+              dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int MODE, int CG>
+cudaError_t launch_gemm(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1, const GemmArgs& g,
+                        cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(gemm_kernel<T, MODE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<CG>::SMEM);
+    if (e != cudaSuccess) return e;
+    const int tiles = g.tiles_r * g.tiles_c, slots = sm_count() / CG;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((tiles < slots ? tiles : slots) * CG));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = Cfg<CG>::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = CG > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, gemm_kernel<T, MODE, CG>, a0, a1, b0, b1, g);
+}
+
+bool good_matrix(const void* p, int64_t ld, int64_t cols) { return p && aligned(p, 16) && ld >= cols && ld % 8 == 0 && on_device(p); }
+
+template <typename T, int CG>
+int forward_tiles(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu, int dtype, int64_t m, int64_t n,
+                  int64_t tokens, int act, void* H, int64_t ldh, void* G, void* U, int64_t ldgu, int* status, cudaStream_t s) {
+    CUtensorMap a, bg, bu;
+    if (!make_map(&a, X, tokens, n, ldx, 128, dtype) || !make_map(&bg, Wg, m, n, ldg, 128, dtype) || !make_map(&bu, Wu, m, n, ldu, 128, dtype))
+        return EXTERND_ECUDA;
+    GemmArgs g = {};
+    g.rows = (int)tokens; g.cols = (int)m; g.depth = (int)n;
+    g.tiles_r = (int)((tokens + Cfg<CG>::BM - 1) / Cfg<CG>::BM);
+    g.tiles_c = (int)((m + 127) / 128);
+    g.act = act;
+    g.out0 = H; g.ld0 = ldh; g.out1 = G; g.out2 = U; g.ld1 = ldgu; g.status = status;
+    return launch_gemm<T, FWD, CG>(a, a, bg, bu, g, s) == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
+}
+
+template <typename T>
+int forward(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu, int dtype, int64_t m, int64_t n,
+            int64_t tokens, int act, void* H, int64_t ldh, void* G, void* U, int64_t ldgu, int* status, cudaStream_t s) {
+    if (tokens <= STREAM_TOKENS) {
+        const unsigned grid = (unsigned)((m + 15) / 16);
+        if (tokens <= 8)
+            dense_stream_kernel<T, 1, 8><<<grid, 256, 0, s>>>((const T*)Wg, ldg, (const T*)Wu, ldu, m, n, act, (const T*)X, ldx, tokens,
+                                                              (T*)H, ldh, (T*)G, (T*)U, ldgu);
+        else
+            dense_stream_kernel<T, 2, 8><<<grid, 256, 0, s>>>((const T*)Wg, ldg, (const T*)Wu, ldu, m, n, act, (const T*)X, ldx, tokens,
+                                                              (T*)H, ldh, (T*)G, (T*)U, ldgu);
+        return cudaGetLastError() == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
+    }
+    return forward_tiles<T, GATED_CG>(X, ldx, Wg, ldg, Wu, ldu, dtype, m, n, tokens, act, H, ldh, G, U, ldgu, status, s);
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_gate_grad(int act, const void* dH, int64_t lddh, const void* G, const void* U, int64_t ldgu, int64_t tokens, int64_t m,
+                             T* dg, T* du, int64_t ldw, cudaStream_t s) {
+    const int64_t items = tokens * (VEC ? (m + 7) / 8 : m), cap = (int64_t)sm_count() * 32;
+    const unsigned grid = (unsigned)((items + 255) / 256 < cap ? (items + 255) / 256 : cap);
+    const T *h = (const T*)dH, *g = (const T*)G, *u = (const T*)U;
+    switch (act) {
+        case EXTERND_ACT_SILU: gate_grad_kernel<T, EXTERND_ACT_SILU, VEC><<<grid, 256, 0, s>>>(h, lddh, g, u, ldgu, tokens, m, dg, du, ldw); break;
+        case EXTERND_ACT_GELU: gate_grad_kernel<T, EXTERND_ACT_GELU, VEC><<<grid, 256, 0, s>>>(h, lddh, g, u, ldgu, tokens, m, dg, du, ldw); break;
+        case EXTERND_ACT_GELU_TANH: gate_grad_kernel<T, EXTERND_ACT_GELU_TANH, VEC><<<grid, 256, 0, s>>>(h, lddh, g, u, ldgu, tokens, m, dg, du, ldw); break;
+        default: gate_grad_kernel<T, EXTERND_ACT_RELU2, VEC><<<grid, 256, 0, s>>>(h, lddh, g, u, ldgu, tokens, m, dg, du, ldw); break;
+    }
+    return cudaGetLastError();
+}
+
+int64_t work_ld(int64_t m) { return (m + 7) / 8 * 8; }
+size_t work_plane(int64_t tokens, int64_t m) { return ((size_t)tokens * (size_t)work_ld(m) * 2 + 255) / 256 * 256; }
+
+template <typename T, int CG>
+int backward(const void* dH, int64_t lddh, const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu,
+             const void* G, const void* U, int64_t ldgu, int dtype, int64_t m, int64_t n, int64_t tokens, int act, void* dX, int64_t lddx,
+             void* dWg, void* dWu, int64_t lddw, void* work, int* status, cudaStream_t s) {
+    const int64_t ldw = work_ld(m);
+    T* dg = (T*)work;
+    T* du = (T*)((char*)work + work_plane(tokens, m));
+    // whole vectors of 8 only where the rows' tails are inside the rows
+    const bool vec = m % 8 == 0 && lddh % 8 == 0 && ldgu % 8 == 0 && aligned(dH, 16) && aligned(G, 16) && aligned(U, 16);
+    const cudaError_t e = vec ? launch_gate_grad<T, true>(act, dH, lddh, G, U, ldgu, tokens, m, dg, du, ldw, s)
+                              : launch_gate_grad<T, false>(act, dH, lddh, G, U, ldgu, tokens, m, dg, du, ldw, s);
+    if (e != cudaSuccess) return EXTERND_ECUDA;
+    constexpr int BM = Cfg<CG>::BM;
+    GemmArgs g = {};
+    g.act = act;
+    g.status = status;
+    if (dX) {
+        CUtensorMap a0, a1, b0, b1;
+        if (!make_map(&a0, dg, tokens, m, ldw, 128, dtype) || !make_map(&a1, du, tokens, m, ldw, 128, dtype) ||
+            !make_map(&b0, Wg, m, n, ldg, BK, dtype) || !make_map(&b1, Wu, m, n, ldu, BK, dtype))
+            return EXTERND_ECUDA;
+        g.rows = (int)tokens; g.cols = (int)n; g.depth = (int)m;
+        g.tiles_r = (int)((tokens + BM - 1) / BM);
+        g.tiles_c = (int)((n + 255) / 256);
+        g.out0 = dX; g.ld0 = lddx;
+        if (launch_gemm<T, DX, CG>(a0, a1, b0, b1, g, s) != cudaSuccess) return EXTERND_ECUDA;
+    }
+    if (dWg || dWu) {
+        // with one gradient only, both halves of the tile list would be the same: the list is that half
+        CUtensorMap a0, a1, b0;
+        if (!make_map(&a0, dWg ? dg : du, tokens, m, ldw, BK, dtype) || !make_map(&a1, du, tokens, m, ldw, BK, dtype) ||
+            !make_map(&b0, X, tokens, n, ldx, BK, dtype))
+            return EXTERND_ECUDA;
+        g.rows = (int)m; g.cols = (int)n; g.depth = (int)tokens;
+        g.half_r = (int)((m + BM - 1) / BM);
+        g.tiles_r = (dWg && dWu ? 2 : 1) * g.half_r;
+        g.tiles_c = (int)((n + 255) / 256);
+        g.out0 = dWg ? dWg : dWu; g.ld0 = lddw;
+        g.out1 = dWu; g.ld1 = lddw;
+        if (launch_gemm<T, DW, CG>(a0, a1, b0, b0, g, s) != cudaSuccess) return EXTERND_ECUDA;
+    }
+    return EXTERND_OK;
+}
+
+bool too_large(int64_t m, int64_t n, int64_t tokens) {
+    const int64_t lim = 0x7fffffff - 1024;
+    if (m > lim || n > lim || tokens > lim) return true;
+    return (tokens / 128 + 1) * (m / 128 + 1) > lim || (tokens / 128 + 1) * (n / 128 + 1) > lim || 2 * (m / 128 + 1) * (n / 128 + 1) > lim;
+}
+
+}  // namespace externd_ffn
+
+using namespace externd_ffn;
+
+extern "C" {
+
+int externd_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu, int dtype, int64_t m, int64_t n,
+                  int64_t tokens, int act, void* H, int64_t ldh, void* G, void* U, int64_t ldgu, int* async_status, void* stream) {
+    if (m < 1 || n < 1 || tokens < 0 || (dtype != EXTERND_F16 && dtype != EXTERND_BF16) || !valid_act(act)) return EXTERND_EINVAL;
+    if (!good_matrix(Wg, ldg, n) || !good_matrix(Wu, ldu, n) || !G != !U) return EXTERND_EINVAL;
+    if (async_status && (!aligned(async_status, 4) || !on_device(async_status))) return EXTERND_EINVAL;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (tokens > 0) {
+        if (!good_matrix(X, ldx, n) || !H || !aligned(H, 2) || ldh < m || !on_device(H)) return EXTERND_EINVAL;
+        if (G && (!aligned(G, 2) || !aligned(U, 2) || ldgu < m || !on_device(G) || !on_device(U))) return EXTERND_EINVAL;
+        if (too_large(m, n, tokens)) return EXTERND_ELIMIT;
+    }
+    if (async_status && cudaMemsetAsync(async_status, 0, sizeof(int), s) != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
+    if (tokens == 0) return EXTERND_OK;
+    const int rc = dtype == EXTERND_F16
+                       ? forward<__half>(X, ldx, Wg, ldg, Wu, ldu, dtype, m, n, tokens, act, H, ldh, G, U, ldgu, async_status, s)
+                       : forward<__nv_bfloat16>(X, ldx, Wg, ldg, Wu, ldu, dtype, m, n, tokens, act, H, ldh, G, U, ldgu, async_status, s);
+    if (rc != EXTERND_OK) cudaGetLastError();
+    return rc;
+}
+
+size_t externd_gated_backward_work(int64_t m, int64_t tokens) { return m < 1 || tokens < 1 ? 0 : 2 * work_plane(tokens, m); }
+
+int externd_gated_backward(const void* dH, int64_t lddh, const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu,
+                           int64_t ldu, const void* G, const void* U, int64_t ldgu, int dtype, int64_t m, int64_t n, int64_t tokens,
+                           int act, void* dX, int64_t lddx, void* dWg, void* dWu, int64_t lddw, void* work, size_t work_bytes,
+                           int* async_status, void* stream) {
+    if (m < 1 || n < 1 || tokens < 0 || (dtype != EXTERND_F16 && dtype != EXTERND_BF16) || !valid_act(act)) return EXTERND_EINVAL;
+    if (async_status && (!aligned(async_status, 4) || !on_device(async_status))) return EXTERND_EINVAL;
+    void* dw[2] = {dWg, dWu};
+    for (void* p : dw)
+        if (p && (!aligned(p, 2) || lddw < n || !on_device(p))) return EXTERND_EINVAL;
+    if (tokens > 0) {
+        if (!dH || !G || !U || !aligned(dH, 2) || !aligned(G, 2) || !aligned(U, 2) || lddh < m || ldgu < m || !on_device(dH) ||
+            !on_device(G) || !on_device(U))
+            return EXTERND_EINVAL;
+        if (dX && (!aligned(dX, 2) || lddx < n || !on_device(dX) || !good_matrix(Wg, ldg, n) || !good_matrix(Wu, ldu, n))) return EXTERND_EINVAL;
+        if ((dWg || dWu) && !good_matrix(X, ldx, n)) return EXTERND_EINVAL;
+        if (!work || !aligned(work, 256) || work_bytes < externd_gated_backward_work(m, tokens) || !on_device(work)) return EXTERND_EINVAL;
+        if (too_large(m, n, tokens)) return EXTERND_ELIMIT;
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (async_status && cudaMemsetAsync(async_status, 0, sizeof(int), s) != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
+    if (tokens == 0) {
+        for (void* p : dw)   // a sum of no terms
+            if (p && cudaMemset2DAsync(p, (size_t)lddw * 2, 0, (size_t)n * 2, (size_t)m, s) != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
+        return EXTERND_OK;
+    }
+    if (!dX && !dWg && !dWu) return EXTERND_OK;
+    const int rc = dtype == EXTERND_F16
+                       ? backward<__half, GATED_CG>(dH, lddh, X, ldx, Wg, ldg, Wu, ldu, G, U, ldgu, dtype, m, n, tokens, act, dX, lddx, dWg,
+                                                    dWu, lddw, work, async_status, s)
+                       : backward<__nv_bfloat16, GATED_CG>(dH, lddh, X, ldx, Wg, ldg, Wu, ldu, G, U, ldgu, dtype, m, n, tokens, act, dX,
+                                                           lddx, dWg, dWu, lddw, work, async_status, s);
+    if (rc != EXTERND_OK) cudaGetLastError();
+    return rc;
+}
+
+}  // extern "C"

@@ -88,7 +88,7 @@ __device__ __forceinline__ float2 act_both(float g) {
         const float p = 0.5f * erfcf(-0.70710678118654752f * g);
         return make_float2(g * p, fmaf(g * 0.39894228040143268f, __expf(-0.5f * g * g), p));
     } else if constexpr (ACT == EXTERND_ACT_GELU_TANH) {
-        const float c = 0.044715f * g * g;
+        const float c = fminf(0.044715f * g * g, 1e4f);   // far past the sigmoid's end: keeps 0 * inf away
         const float s = sigmoid<PRECISE>(1.5957691216057308f * g * (1.0f + c)), a = g * s;
         return make_float2(a, fmaf(a * (1.0f - s), 1.5957691216057308f * fmaf(3.0f, c, 1.0f), s));
     } else {

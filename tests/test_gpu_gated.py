@@ -1,0 +1,331 @@
+"""The dense gated feed-forward block on the GPU: forward, saved projections and gradients, against the formulas
+in 64 bits (tests/_llm_ref.py states what the arithmetic may lose)."""
+import pytest
+import torch
+
+import ternary_rank_weight_b200 as ext
+from _llm_ref import ACTS, U, act64, act_eps, act_slope, act_slope2, gated_bound, half_step
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+def _make(t, m, n, dtype, seed=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed + 7 * t + 11 * m + 13 * n)
+    X = torch.randn(t, n, generator=g, device="cuda").to(dtype)
+    Wg = (torch.randn(m, n, generator=g, device="cuda") * n ** -0.5).to(dtype)
+    Wu = (torch.randn(m, n, generator=g, device="cuda") * n ** -0.5).to(dtype)
+    dH = (0.1 * torch.randn(t, m, generator=g, device="cuda")).to(dtype)
+    return X, Wg, Wu, dH
+
+
+def _proj(X, W):
+    """A projection in 64 bits and what n fp32 terms may lose."""
+    x, w = X.double(), W.double()
+    return x @ w.t(), (W.shape[1] + 24) * U * (x.abs() @ w.abs().t())
+
+
+def _check_forward(X, Wg, Wu, act, H, G=None, Up=None):
+    (g, dg), (u, du) = _proj(X, Wg), _proj(X, Wu)
+    h = act64(act, g)[0] * u
+    bound = gated_bound(act, g, u, dg, du)
+    assert H.dtype == X.dtype and H.shape == h.shape
+    assert torch.all((H.double() - h).abs() <= bound * (1 + 2.0 ** -8) + half_step(X.dtype, h))
+    if G is not None:
+        assert torch.all((G.double() - g).abs() <= dg * (1 + 2.0 ** -8) + half_step(X.dtype, g))
+        assert torch.all((Up.double() - u).abs() <= du * (1 + 2.0 ** -8) + half_step(X.dtype, u))
+
+
+def _check_backward(X, Wg, Wu, dH, act, G, Up, got):
+    """The gradients' own arithmetic, from the saved (rounded) projections: dG and dU carry the activation's
+    error, two or three fp32 products and one rounding to the operands' type; the sums add theirs."""
+    g, u, r, x = G.double(), Up.double(), dH.double(), X.double()
+    f, df = act64(act, g)
+    # the derivative's parts s, g s, (1 - s) ... carry act_eps each; their magnitudes stay below 1 + slope
+    edf = act_eps(g) * (df.abs() + 1 + f.abs()) * 4
+    dg, du = r * u * df, r * f
+    eg = (r * u).abs() * edf + 4 * U * dg.abs()
+    eu = r.abs() * act_eps(g) * f.abs() + 4 * U * du.abs()
+    eg = eg + half_step(X.dtype, dg) * (1 + 2.0 ** -8) + eg * 2.0 ** -8
+    eu = eu + half_step(X.dtype, du) * (1 + 2.0 ** -8) + eu * 2.0 ** -8
+    t, m = g.shape
+    wg, wu = Wg.double(), Wu.double()
+    dX, dWg, dWu = got
+    if dX is not None:
+        v = dg @ wg + du @ wu
+        e = eg @ wg.abs() + eu @ wu.abs() + (2 * m + 24) * U * ((dg.abs() + eg) @ wg.abs() + (du.abs() + eu) @ wu.abs())
+        assert dX.shape == v.shape and torch.all((dX.double() - v).abs() <= e * (1 + 2.0 ** -8) + half_step(X.dtype, v))
+    for d, ed, dW in ((dg, eg, dWg), (du, eu, dWu)):
+        if dW is not None:
+            v = d.t() @ x
+            e = ed.t() @ x.abs() + (t + 24) * U * ((d.abs() + ed).t() @ x.abs())
+            assert dW.shape == v.shape and torch.all((dW.double() - v).abs() <= e * (1 + 2.0 ** -8) + half_step(X.dtype, v))
+
+
+SHAPES = [(1, 1, 1), (1, 64, 64), (2, 17, 33), (5, 100, 72), (8, 33, 1000), (9, 40, 64), (16, 130, 777), (17, 16, 16), (31, 129, 200),
+          (64, 128, 64), (127, 250, 130), (128, 128, 128), (129, 257, 65), (200, 1000, 300), (300, 1111, 777), (513, 300, 520),
+          (1000, 640, 256)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("t,m,n", SHAPES)
+def test_forward_matches_64_bits(t, m, n, dtype):
+    for act in ACTS:
+        X, Wg, Wu, _ = _make(t, m, n, dtype)
+        H, G, Up = ext.gated_forward(X, Wg, Wu, act)
+        _check_forward(X, Wg, Wu, act, H, G, Up)
+        assert torch.equal(ext.gated(X, Wg, Wu, act), H)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("t,m,n", SHAPES)
+def test_backward_matches_64_bits(t, m, n, dtype):
+    for act in ACTS:
+        X, Wg, Wu, dH = _make(t, m, n, dtype, seed=1)
+        _, G, Up = ext.gated_forward(X, Wg, Wu, act)
+        got = ext.gated_backward(dH, X, Wg, Wu, G, Up, act)
+        _check_backward(X, Wg, Wu, dH, act, G, Up, got)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_small_integers_are_exact(dtype):
+    """Integers whose sums stay below 2^8: every product, sum and rounding of the projections and of relu2's
+    gradients' sums is exact, so a lost or doubled term anywhere shows."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    t, m, n = 333, 210, 392
+    X = (torch.rand(t, n, generator=g, device="cuda") < 0.06).to(dtype)
+    Wg = torch.randint(-1, 2, (m, n), generator=g, device="cuda").to(dtype)
+    Wu = torch.randint(-1, 2, (m, n), generator=g, device="cuda").to(dtype)
+    H, G, Up = ext.gated_forward(X, Wg, Wu, "relu2")
+    g64, u64 = X.double() @ Wg.double().t(), X.double() @ Wu.double().t()
+    assert g64.abs().max() < 128 and torch.equal(G.double(), g64) and torch.equal(Up.double(), u64)
+    assert torch.equal(H, (g64.clamp(min=0) ** 2 * u64).float().to(dtype))
+    # gradients with G in {-1, 0, 1}, U in {-1, 0, 1} and sparse dH in {0, 1}: dG, dU small integers
+    Gs = torch.randint(-1, 2, (t, m), generator=g, device="cuda").to(dtype)
+    Us = torch.randint(-1, 2, (t, m), generator=g, device="cuda").to(dtype)
+    dH = (torch.rand(t, m, generator=g, device="cuda") < 0.1).to(dtype)
+    dX, dWg, dWu = ext.gated_backward(dH, X, Wg, Wu, Gs, Us, "relu2")
+    dg, du = dH.double() * Us.double() * 2 * Gs.double().clamp(min=0), dH.double() * Gs.double().clamp(min=0) ** 2
+    for got, want in ((dX, dg @ Wg.double() + du @ Wu.double()), (dWg, dg.t() @ X.double()), (dWu, du.t() @ X.double())):
+        assert want.abs().max() < 256 and torch.equal(got.double(), want)
+
+
+def test_gradients_match_differences():
+    """d/ds of sum(dH H(X + s V)) in 64 bits, by central differences of the formula, against the kernels'
+    gradients contracted with V: the gradients' bound of one rounding chain (4 roundings of fp16, 2^-11 each,
+    of the sum of the terms' magnitudes) and a difference error below 1e-6 of it."""
+    t, m, n, act = 40, 96, 72, "gelu"
+    X, Wg, Wu, dH = _make(t, m, n, F16, seed=2)
+    _, G, Up = ext.gated_forward(X, Wg, Wu, act)
+    grads = ext.gated_backward(dH, X, Wg, Wu, G, Up, act)
+    x = [X.double(), Wg.double(), Wu.double()]
+
+    def f(a, b, c):
+        return (dH.double() * act64(act, a @ b.t())[0] * (a @ c.t())).sum()
+
+    for i in range(3):
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(i)
+        V = torch.randn(x[i].shape, generator=gen, device="cuda", dtype=torch.float64)
+        h = 1e-5
+        hi, lo = [v.clone() for v in x], [v.clone() for v in x]
+        hi[i] += h * V
+        lo[i] -= h * V
+        diff = (f(*hi) - f(*lo)) / (2 * h)
+        r = dH.double().abs()
+        g, u = x[0] @ x[1].t(), x[0] @ x[2].t()
+        a, b = r * u.abs() * 1.13, r * 1.13 * g.abs()
+        mags = [a @ x[1].abs() + b @ x[2].abs(), a.t() @ x[0].abs(), b.t() @ x[0].abs()][i]
+        # G and U rounded once each and act', act of a rounded G (slopes 0.8 and 1.13 of 2^-11 |G|), dG, the result
+        bound = 8 * 2.0 ** -11 * (mags * (1 + g.abs().max()) * V.abs()).sum()
+        assert (diff - (grads[i].double() * V).sum()).abs() <= bound
+
+
+def test_large_magnitudes_of_the_gate():
+    """Gates far out on both sides: silu and its gradient reach their limits without NaN."""
+    n = 64
+    X = torch.eye(n, device="cuda", dtype=BF16)
+    vals = torch.tensor([-3e38, -1e30, -200.0, -90.0, -88.0, -20.0, -1.0, 0.0, 1.0, 20.0, 88.0, 90.0, 200.0, 1e18], device="cuda")
+    Wg = torch.zeros(n, n, device="cuda")
+    Wg[:, :14] = vals
+    Wg, Wu = Wg.to(BF16), torch.ones(n, n, device="cuda").to(BF16)
+    for act in ("silu", "gelu", "gelu_tanh"):
+        H, G, Up = ext.gated_forward(X, Wg, Wu, act)
+        want = act64(act, Wg.double().t())[0].to(torch.float32).to(BF16)
+        assert torch.isfinite(H).all()
+        assert torch.all((H.double() - want.double()).abs() <= 2.0 ** -7 * want.double().abs() + 1e-9)
+        for g in ext.gated_backward(torch.ones_like(H), X, Wg, Wu, G, Up, act):
+            assert not torch.isnan(g).any()
+
+
+def test_shapes_strides_and_partial_gradients():
+    t, m, n = 60, 130, 100
+    X, Wg, Wu, dH = _make(t, m, n, BF16)
+    H, G, Up = ext.gated_forward(X, Wg, Wu)
+    for lead in ((3, 20), (2, 5, 6)):
+        H2, G2, U2 = ext.gated_forward(X.view(*lead, n), Wg, Wu)
+        assert H2.shape == (*lead, m) and torch.equal(H2.view(t, m), H) and torch.equal(G2.view(t, m), G)
+        dX, dWg, dWu = ext.gated_backward(dH.view(*lead, m), X.view(*lead, n), Wg, Wu, G2, U2)
+        assert dX.shape == (*lead, n)
+    ref = ext.gated_backward(dH, X, Wg, Wu, G, Up)
+    assert torch.equal(dX.view(t, n), ref[0]) and torch.equal(dWg, ref[1]) and torch.equal(dWu, ref[2])
+    for need in ((True, False, False), (False, True, False), (False, False, True), (True, False, True), (False, False, False)):
+        got = ext.gated_backward(dH, X, Wg, Wu, G, Up, need=need)
+        for want, a, b in zip(need, got, ref):
+            assert (a is None) == (not want) and (a is None or torch.equal(a, b))
+    one = ext.gated(X[0], Wg, Wu)
+    assert one.shape == (m,) and torch.equal(one, ext.gated(X[:1], Wg, Wu)[0])
+    # rows off the 16-byte boundaries, strided rows, transposed storage
+    bigX, bigW, bigd = torch.zeros(t, n + 9, dtype=BF16, device="cuda"), torch.zeros(m, n + 16, dtype=BF16, device="cuda"), \
+        torch.zeros(t, m + 3, dtype=BF16, device="cuda")
+    bigX[:, 5:5 + n], bigW[:, 8:8 + n], bigd[:, 1:1 + m] = X, Wg, dH
+    Xv, Wv, dv, Wt = bigX[:, 5:5 + n], bigW[:, 8:8 + n], bigd[:, 1:1 + m], Wu.t().contiguous().t()
+    H3, G3, U3 = ext.gated_forward(Xv, Wv, Wt)
+    assert torch.equal(H3, H) and torch.equal(G3, G) and torch.equal(U3, Up)
+    for a, b in zip(ext.gated_backward(dv, Xv, Wv, Wt, bigd.new_zeros(t, m + 3)[:, :m].copy_(G3), U3), ref):
+        assert torch.equal(a, b)
+    out = torch.full((t + 2, m + 7), 5.0, dtype=BF16, device="cuda")
+    got = ext.gated(X, Wg, Wu, out=out[1:-1, 3:3 + m])
+    assert torch.equal(got, H)
+    out[1:-1, 3:3 + m] = 5.0
+    assert torch.all(out == 5.0)
+
+
+def test_no_tokens():
+    X, Wg, Wu, dH = _make(4, 40, 24, F16)
+    H, G, Up = ext.gated_forward(X[:0], Wg, Wu)
+    assert H.shape == (0, 40) and G.shape == (0, 40)
+    dX, dWg, dWu = ext.gated_backward(dH[:0], X[:0], Wg, Wu, G, Up)
+    assert dX.shape == (0, 24) and not dWg.any() and not dWu.any() and dWg.shape == (40, 24)
+
+
+def test_nan_stays_in_its_token():
+    X, Wg, Wu, dH = _make(140, 70, 200, BF16)
+    ref = ext.gated(X, Wg, Wu)
+    X[3, 5] = float("nan")
+    got = ext.gated(X, Wg, Wu)
+    keep = [i for i in range(140) if i != 3]
+    assert torch.equal(got[keep], ref[keep]) and torch.isnan(got[3]).all()
+
+
+def test_columns_beside_the_inputs_are_not_read():
+    """Padding columns and neighbouring rows hold NaN; none of it may enter a sum."""
+    for t in (3, 150):
+        X, Wg, Wu, dH = _make(t, 75, 100, BF16)
+        ref = ext.gated_forward(X, Wg, Wu)
+        gref = ext.gated_backward(dH, X, Wg, Wu, *ref[1:])
+
+        def surround(a):
+            b = torch.full((a.shape[0] + 8, a.shape[1] + 20), float("nan"), dtype=a.dtype, device="cuda")
+            b = b[:, :b.shape[1] // 8 * 8].contiguous()
+            v = b[4:4 + a.shape[0], 8:8 + a.shape[1]]
+            v.copy_(a)
+            return v
+
+        Xs, Gs, Us = surround(X), surround(Wg), surround(Wu)
+        got = ext.gated_forward(Xs, Gs, Us)
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        got = ext.gated_backward(surround(dH), Xs, Gs, Us, surround(ref[1]), surround(ref[2]))
+        assert all(torch.equal(a, b) for a, b in zip(got, gref))
+
+
+def test_repeats_bit_for_bit_on_streams_and_in_graphs():
+    for t in (5, 300):
+        X, Wg, Wu, dH = _make(t, 520, 260, BF16)
+        fw = ext.gated_forward(X, Wg, Wu, "gelu_tanh")
+        ref = (*fw, *ext.gated_backward(dH, X, Wg, Wu, fw[1], fw[2], "gelu_tanh"))
+        torch.cuda.synchronize()
+        st = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+        s = torch.cuda.Stream()
+        for _ in range(3):
+            a = ext.gated_forward(X, Wg, Wu, "gelu_tanh", stream=s, async_status=st)
+            b = ext.gated_backward(dH, X, Wg, Wu, a[1], a[2], "gelu_tanh", stream=s.cuda_stream)
+            s.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip((*a, *b), ref)) and int(st.item()) == 0
+        graphs = []
+        for _ in range(2):                      # two graphs alive at once
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr):
+                a = ext.gated_forward(X, Wg, Wu, "gelu_tanh")
+                b = ext.gated_backward(dH, X, Wg, Wu, a[1], a[2], "gelu_tanh", async_status=st)
+            graphs.append((gr, (*a, *b)))
+        for gr, outs in graphs + graphs:
+            for o in outs:
+                o.zero_()
+            gr.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(outs, ref)) and int(st.item()) == 0
+
+
+def test_block_in_4_bits_follows_the_dense_block():
+    """A converted MLP as it is used: quantise gate, up and down, run tokens through the 4-bit block and the
+    4-bit down projection, and through the dense block over the values the 4 bits stand for (rounded to
+    fp16, 2^-11 of each weight)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    m, n = 700, 256
+    Wg, Wu, Wd = (torch.randn(*s, generator=g, device="cuda") * s[1] ** -0.5 for s in ((m, n), (m, n), (n, m)))
+    wg, wu, wd = (ext.int4_quantize(w, 64) for w in (Wg, Wu, Wd))
+    dg, du, dd = (ext.int4_dequantize(w, F16) for w in (wg, wu, wd))
+    for t in (1, 12, 90):
+        X = torch.randn(t, n, generator=g, device="cuda").to(F16)
+        h4 = ext.int4_gated(wg, wu, X)
+        y4 = ext.int4_matvec(wd, h4)
+        h16 = ext.gated(X, dg, du)
+        x = X.double()
+        G, Up = x @ dg.double().t(), x @ du.double().t()
+        eg, eu = (2.0 ** -10 * (x.abs() @ w.double().abs().t()) for w in (dg, du))
+        bound = gated_bound("silu", G, Up, eg, eu)
+        assert torch.all((h4.double() - h16.double()).abs() <= 2 * bound + 3 * half_step(F16, h16.double()))
+        y = h4.double() @ ext.int4_dequantize(wd).double().t()
+        mag = h4.double().abs() @ (dd.double().abs() + 2 * wd.scale.double().max() * 8).t()
+        assert torch.all((y4.double() - y).abs() <= (64 + 2 * 11 + 20) * U * 4 * mag + half_step(F16, y))
+
+
+def test_library_refuses_bad_arguments():
+    L, einval = ext._lib.load(), ext.STATUS["EINVAL"]
+    t, m, n = 20, 24, 32
+    X, Wg, Wu, dH = _make(t, m, n, BF16)
+    H, G, Up = ext.gated_forward(X, Wg, Wu)
+    out = [torch.zeros(s, dtype=BF16, device="cuda") for s in ((t, n), (m, n), (m, n))]
+    work = torch.zeros(L.externd_gated_backward_work(m, t), dtype=torch.uint8, device="cuda")
+    host = torch.zeros(1 << 16, dtype=torch.uint8)
+    st = torch.cuda.current_stream().cuda_stream
+    base = dict(x=X.data_ptr(), ldx=n, wg=Wg.data_ptr(), ldg=n, wu=Wu.data_ptr(), ldu=n, dt=2, m=m, n=n, t=t, act=0, h=H.data_ptr(),
+                ldh=m, g=G.data_ptr(), u=Up.data_ptr(), ldgu=m, status=None, dh=dH.data_ptr(), lddh=m, dx=out[0].data_ptr(), lddx=n,
+                dwg=out[1].data_ptr(), dwu=out[2].data_ptr(), lddw=n, work=work.data_ptr(), wb=work.numel())
+
+    def fwd(**kw):
+        a = dict(base, **kw)
+        return L.externd_gated(*(a[k] for k in "x ldx wg ldg wu ldu dt m n t act h ldh g u ldgu status".split()), st)
+
+    def bwd(**kw):
+        a = dict(base, **kw)
+        return L.externd_gated_backward(*(a[k] for k in "dh lddh x ldx wg ldg wu ldu g u ldgu dt m n t act dx lddx dwg dwu lddw work "
+                                          "wb status".split()), st)
+
+    assert fwd() == 0 and bwd() == 0 and fwd(g=None, u=None) == 0
+    common = [dict(x=None), dict(wg=None), dict(wu=None), dict(dt=0), dict(dt=5), dict(m=0), dict(n=0), dict(t=-1), dict(act=4),
+              dict(act=-1), dict(ldx=n + 1), dict(ldx=n - 8), dict(ldg=n + 4), dict(ldu=n - 8), dict(x=X.data_ptr() + 2),
+              dict(wg=Wg.data_ptr() + 8), dict(x=host.data_ptr()), dict(wu=host.data_ptr()), dict(status=host.data_ptr()),
+              dict(u=None), dict(ldgu=m - 1), dict(g=G.data_ptr() + 1)]
+    for kw in common:
+        assert fwd(**kw) == einval, kw
+        assert bwd(**kw) == einval, kw
+    for kw in (dict(h=None), dict(ldh=m - 1), dict(h=host.data_ptr()), dict(g=None)):
+        assert fwd(**kw) == einval, kw
+    for kw in (dict(dh=None), dict(lddh=m - 1), dict(dx=host.data_ptr()), dict(lddx=n - 1), dict(lddw=n - 1), dict(work=None),
+               dict(wb=work.numel() - 1), dict(work=work.data_ptr() + 16), dict(dwg=host.data_ptr())):
+        assert bwd(**kw) == einval, kw
+    assert bwd(dx=None, wg=None, wu=None) == 0 and bwd(dwg=None, dwu=None, x=None) == 0
+    with pytest.raises(ValueError):
+        ext.gated(X.float(), Wg.float(), Wu.float())
+    with pytest.raises(ValueError):
+        ext.gated(X, Wg, Wu.half())
+    with pytest.raises(ValueError):
+        ext.gated(X, Wg, Wu[:-1])
+    with pytest.raises(ValueError):
+        ext.gated_backward(dH[:-1], X, Wg, Wu, G, Up)

@@ -58,3 +58,30 @@ def test_int4_binding_rejects_bad_tensors():
         ext.int4_gated(w, w, cpu, "swish")
     with pytest.raises(ValueError):
         ext.int4_matvec(w, None)
+
+
+def test_gated_entry_points_reject_bad_arguments_before_device_work():
+    L = _lib.load()
+    host = (ctypes.c_uint8 * 512)()
+    p = (ctypes.addressof(host) + 255) // 256 * 256
+    assert L.externd_gated(p, 8, p, 8, p, 8, 2, 1, 1, 1, 0, p, 1, None, None, 1, None, None) == EINVAL   # host memory
+    assert L.externd_gated(p, 8, None, 8, p, 8, 2, 1, 1, 1, 0, p, 1, None, None, 1, None, None) == EINVAL
+    assert L.externd_gated(p, 8, p, 8, p, 8, 0, 1, 1, 1, 0, p, 1, None, None, 1, None, None) == EINVAL   # fp32
+    assert L.externd_gated(p, 8, p, 8, p, 8, 2, 1, 1, 1, 9, p, 1, None, None, 1, None, None) == EINVAL   # activation
+    assert L.externd_gated(p, 8, p, 8, p, 8, 2, 0, 1, 1, 0, p, 1, None, None, 1, None, None) == EINVAL
+    assert L.externd_gated(p, 8, p, 8, p, 8, 2, 1, 1, -1, 0, p, 1, None, None, 1, None, None) == EINVAL
+    assert L.externd_gated_backward(p, 1, p, 8, p, 8, p, 8, p, p, 1, 2, 1, 1, 1, 0, p, 1, p, p, 1, p, 512, None, None) == EINVAL
+    assert L.externd_gated_backward_work(0, 5) == 0 and L.externd_gated_backward_work(5, 0) == 0
+    assert L.externd_gated_backward_work(1000, 300) == 2 * ((300 * 1000 * 2 + 255) // 256 * 256)
+    assert L.externd_gated_backward_work(3, 1) == 512                       # rows of 8 elements, planes on 256 bytes
+
+
+def test_gated_binding_rejects_bad_tensors():
+    x, w = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(8, 16, dtype=torch.bfloat16)
+    for args in ((x, w, w), (x[:, :8], w, w), (x, w, w[:4]), (None, w, w), (x, None, w), (x.float(), w.float(), w.float())):
+        with pytest.raises(ValueError):
+            ext.gated(*args)
+    with pytest.raises(ValueError):
+        ext.gated(x, w, w, "tanh")
+    with pytest.raises(ValueError):
+        ext.gated_backward(x, x, w, w, x, x)
