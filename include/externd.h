@@ -318,35 +318,38 @@ int externd_int4_gated(const uint8_t* qg, const void* scale_g, const void* offse
                        const void* scale_u, const void* offset_u, int64_t m, int64_t n, int group, int act,
                        const void* X, int dtype, int64_t ldx, int64_t batch, void* H, int64_t ldh, void* stream);
 
-/* The gated feed-forward block with dense fp16 or bf16 weights (m x n, as stored by a model's gate and
- * up projections): H = act(G) * U, G = X Wg^T, U = X Wu^T, for X tokens x n.  fp32 sums, one rounding
- * of each output.
- *   X, Wg, Wu  [in]  16-byte aligned with leading dimensions that are multiples of 8 (columns from n on
- *                    are not read).
+/* The gated feed-forward block with dense fp16 or bf16 weights (m x n, as a model stores its gate and up
+ * projections): H = act(G) * U, G = X Wg^T, U = X Wu^T, for X tokens x n.  fp32 sums, one rounding of each
+ * output.  Columns from n on are not read.
  *   H          [out] tokens x m.
- *   G, U       [out] both NULL, or both tokens x m with leading dimension ldgu: the projections, rounded
- *                    to dtype, which externd_gated_backward needs.
+ *   G, U       [out] both NULL, or both tokens x m with leading dimension ldgu: the projections, which
+ *                    externd_gated_backward needs, of type save_dtype: EXTERND_F32, or dtype.  (16-bit ones
+ *                    halve the memory held for the backward pass and add their rounding to its results.)
+ *   work       [tmp] 256-byte aligned, owned by the caller; NULL (work_bytes 0) where the rows of X, Wg and
+ *                    Wu start on 16-byte boundaries (pointer 16-byte aligned, leading dimension a multiple
+ *                    of 8, or one row).  Otherwise externd_gated_work(rows, n) bytes for each of the three
+ *                    that does not: it is copied there first.
  *   async_status  NULL, or a device int that receives EXTERND_OK, or EXTERND_ETIMEOUT if a device-side
  *                    wait gave up (2 s; the outputs are then unspecified), when the stream gets there.
- * tokens = 0 does nothing. */
+ * tokens = 0 computes nothing. */
+size_t externd_gated_work(int64_t rows, int64_t n);
 int externd_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu, int dtype,
-                  int64_t m, int64_t n, int64_t tokens, int act, void* H, int64_t ldh, void* G, void* U, int64_t ldgu,
-                  int* async_status, void* stream);
+                  int64_t m, int64_t n, int64_t tokens, int act, void* H, int64_t ldh, void* G, void* U, int save_dtype,
+                  int64_t ldgu, void* work, size_t work_bytes, int* async_status, void* stream);
 
-/* Bytes of `work` for externd_gated_backward. */
-size_t externd_gated_backward_work(int64_t m, int64_t tokens);
-
-/* Gradients of the gated block: with dG = dH * U * act'(G) and dU = dH * act(G) (rounded to dtype),
+/* Gradients of the gated block: with dG = dH * U * act'(G) and dU = dH * act(G) (rounded to dtype, for the
+ * tensor cores),
  *   dX = dG Wg + dU Wu (tokens x n),   dWg = dG^T X,   dWu = dU^T X (m x n, leading dimension lddw).
- *   dX, dWg, dWu  [out] any of them may be NULL: it is then not computed.  dH, X, Wg, Wu, G, U are only
- *                       needed (and checked) for what is computed.
- *   X, Wg, Wu     [in]  as for externd_gated.  dH, G, U, dX, dWg, dWu need only their element's alignment.
- *   work          [tmp] 256-byte aligned, externd_gated_backward_work(m, tokens) bytes, owned by the caller.
- * tokens = 0 sets dWg and dWu to 0.  Results do not change from call to call (no atomics). */
+ *   dX, dWg, dWu  [out] any of them may be NULL: it is then not computed.  The inputs are needed (and
+ *                       checked) only for what is computed: X for dWg and dWu, Wg and Wu for dX.
+ *   G, U, save_dtype, ldgu  as externd_gated returned them.
+ *   work          [tmp] as for externd_gated, with externd_gated_backward_work(m, tokens) bytes besides.
+ * tokens = 0 sets dWg and dWu to 0.  The same call gives the same bits (no atomics). */
+size_t externd_gated_backward_work(int64_t m, int64_t tokens);
 int externd_gated_backward(const void* dH, int64_t lddh, const void* X, int64_t ldx, const void* Wg, int64_t ldg,
-                           const void* Wu, int64_t ldu, const void* G, const void* U, int64_t ldgu, int dtype, int64_t m,
-                           int64_t n, int64_t tokens, int act, void* dX, int64_t lddx, void* dWg, void* dWu,
-                           int64_t lddw, void* work, size_t work_bytes, int* async_status, void* stream);
+                           const void* Wu, int64_t ldu, const void* G, const void* U, int save_dtype, int64_t ldgu,
+                           int dtype, int64_t m, int64_t n, int64_t tokens, int act, void* dX, int64_t lddx, void* dWg,
+                           void* dWu, int64_t lddw, void* work, size_t work_bytes, int* async_status, void* stream);
 
 /* Human-readable message for a status code (static storage). */
 const char* externd_strerror(int status);

@@ -554,14 +554,24 @@ _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu2": 3}
 
 
-def _on_stream(stream, device):
-    """Temporaries and outputs come from the stream the kernels run on: torch's allocator may hand
-    their memory to later work of that stream only."""
+_NOTHING = contextlib.nullcontext()
+
+
+def _guard(stream, device: torch.device):
+    """Make `device` current, and `stream` if one is given: torch's allocator may hand the memory of
+    temporaries and outputs to later work of the stream they were allocated on only."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    if stream.device != device:
+        raise ValueError("the stream and the tensors must belong to one device")
     return torch.cuda.stream(stream)
+
+
+def _raw_stream() -> int:
+    """The current stream, inside _guard."""
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _rows_in(t, cols: int, name: str, like: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -639,27 +649,22 @@ def int4_quantize(A: torch.Tensor, group: int = 128, *, affine: bool = True, asy
     async_status: a one-element int32 CUDA tensor: the call queues its work and returns at once; the
     tensor receives the status when the stream gets there.  A must then need no copy (unit column
     stride) and stay alive and unchanged until then."""
-    if not isinstance(A, torch.Tensor) or A.dim() != 2:
-        raise ValueError("A must be a 2-D float32, float16 or bfloat16 CUDA tensor")
-    with _on_stream(stream, A.device):
+    if not isinstance(A, torch.Tensor) or A.dim() != 2 or not A.is_cuda or A.numel() == 0:
+        raise ValueError("A must be a 2-D float32, float16 or bfloat16 CUDA tensor that is not empty")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    _check_status(async_status, A.device)
+    with _guard(stream, A.device):
         A2 = _rows_in(A, A.shape[1], "A")
-        if async_status is not None:
-            if A2 is not A:
-                raise ValueError("an asynchronous call needs A with unit column stride")
-            if not (isinstance(async_status, torch.Tensor) and async_status.device == A.device
-                    and async_status.dtype == torch.int32 and async_status.numel() >= 1):
-                raise ValueError("async_status must be an int32 CUDA tensor")
+        if async_status is not None and A2 is not A:
+            raise ValueError("an asynchronous call needs A with unit column stride")
         m, n = A2.shape
-        if m < 1 or n < 1 or group not in (32, 64, 128):
-            raise ValueError("A must not be empty and group must be 32, 64 or 128")
         groups = (n + group - 1) // group
-        q = torch.empty((m, int4_row_bytes(n)), dtype=torch.uint8, device=A2.device)
+        q = torch.empty((m, (n + 127) // 128 * 64), dtype=torch.uint8, device=A2.device)
         scale = torch.empty((groups, m), dtype=torch.float16, device=A2.device)
-        offset = torch.empty_like(scale) if affine else None
-        with _on_device(A2):
-            rc = _lib.load().externd_int4_quantize(_ptr(A2), _DTYPE[A2.dtype], m, n, _ld(A2), int(group), _ptr(q),
-                                                   _ptr(scale), _ptr(offset), _ptr(async_status),
-                                                   _stream(stream, A2.device))
+        offset = torch.empty((groups, m), dtype=torch.float16, device=A2.device) if affine else None
+        rc = _lib.load().externd_int4_quantize(A2.data_ptr(), _DTYPE[A2.dtype], m, n, _ld(A2), int(group), q.data_ptr(),
+                                               scale.data_ptr(), _ptr(offset), _ptr(async_status), _raw_stream())
     _check(rc, "externd_int4_quantize")
     return Int4Weights(q=q, scale=scale, offset=offset, m=m, n=n, group=int(group))
 
@@ -669,11 +674,10 @@ def int4_dequantize(w: Int4Weights, dtype: torch.dtype = torch.float32, *, strea
     _check_int4(w)
     if dtype not in _DTYPE:
         raise ValueError("dtype must be float32, float16 or bfloat16")
-    with _on_stream(stream, w.q.device):
+    with _guard(stream, w.q.device):
         out = torch.empty((w.m, w.n), dtype=dtype, device=w.q.device)
-        with _on_device(out):
-            rc = _lib.load().externd_int4_dequantize(_ptr(w.q), _ptr(w.scale), _ptr(w.offset), w.m, w.n, w.group,
-                                                     _ptr(out), _DTYPE[dtype], w.n, _stream(stream, out.device))
+        rc = _lib.load().externd_int4_dequantize(w.q.data_ptr(), w.scale.data_ptr(), _ptr(w.offset), w.m, w.n, w.group,
+                                                 out.data_ptr(), _DTYPE[dtype], w.n, _raw_stream())
     _check(rc, "externd_int4_dequantize")
     return out
 
@@ -693,24 +697,23 @@ def int4_gated(wg: Int4Weights, wu: Int4Weights, X: torch.Tensor, act: str = "si
 
 
 def _int4_products(ws, X, act: int, out, stream) -> torch.Tensor:
-    if not isinstance(X, torch.Tensor):
+    if not isinstance(X, torch.Tensor) or not X.is_cuda:
         raise ValueError("X must be a CUDA tensor")
     for w in ws:
         _check_int4(w, X.device)
-    m, n = ws[0].m, ws[0].n
+    w = ws[0]
     squeeze = X.dim() == 1
-    with _on_stream(stream, X.device):
-        X2 = _rows_in(X.unsqueeze(0) if squeeze else X, n, "X")
+    with _guard(stream, X.device):
+        X2 = _rows_in(X.unsqueeze(0) if squeeze else X, w.n, "X")
         if out is not None and squeeze:
             out = out.unsqueeze(0)
-        Y = _result(out, X2.shape[0], m, X2)
-        mats = [_ptr(t) for w in ws for t in (w.q, w.scale, w.offset)]
-        tail = [_ptr(X2), _DTYPE[X2.dtype], _ld(X2), X2.shape[0], _ptr(Y), _ld(Y), _stream(stream, X2.device)]
-        with _on_device(X2):
-            if len(ws) == 1:
-                rc = _lib.load().externd_int4_matvec(*mats, m, n, ws[0].group, *tail)
-            else:
-                rc = _lib.load().externd_int4_gated(*mats, m, n, ws[0].group, act, *tail)
+        Y = _result(out, X2.shape[0], w.m, X2)
+        mats = [p for v in ws for p in (v.q.data_ptr(), v.scale.data_ptr(), _ptr(v.offset))]
+        tail = (X2.data_ptr(), _DTYPE[X2.dtype], _ld(X2), X2.shape[0], Y.data_ptr(), _ld(Y), _raw_stream())
+        if len(ws) == 1:
+            rc = _lib.load().externd_int4_matvec(*mats, w.m, w.n, w.group, *tail)
+        else:
+            rc = _lib.load().externd_int4_gated(*mats, w.m, w.n, w.group, act, *tail)
     _check(rc, "externd_int4_matvec" if len(ws) == 1 else "externd_int4_gated")
     return Y[0] if squeeze else Y
 
@@ -747,77 +750,83 @@ def pack_int4(codes: np.ndarray) -> np.ndarray:
 # gated feed-forward block with dense weights
 # ---------------------------------------------------------------------------
 
-def _dense_in(t, cols: int, name: str, like: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """A 2-D float16 or bfloat16 CUDA tensor that the tile kernel can read: unit column stride, rows on 16-byte
-    boundaries (copied into such rows otherwise)."""
-    if isinstance(t, torch.Tensor) and t.dtype == torch.float32:
-        raise ValueError(f"{name} must be float16 or bfloat16")
-    t = _rows_in(t, cols, name, like)
-    if t.data_ptr() % 16 == 0 and (t.shape[0] < 2 or t.stride(0) % 8 == 0):
-        return t
-    padded = torch.empty((t.shape[0], (cols + 7) // 8 * 8), dtype=t.dtype, device=t.device)[:, :cols]
-    padded.copy_(t)
-    return padded
-
-
-def _ld8(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
-
-
 def _check_status(async_status, device):
     if async_status is not None and not (isinstance(async_status, torch.Tensor) and async_status.device == device
                                          and async_status.dtype == torch.int32 and async_status.numel() >= 1):
-        raise ValueError("async_status must be an int32 CUDA tensor")
+        raise ValueError("async_status must be an int32 CUDA tensor on the other tensors' device")
 
 
 def _gated_inputs(X, Wg, Wu):
-    if not isinstance(Wg, torch.Tensor) or Wg.dim() != 2 or Wg.shape[0] < 1 or Wg.shape[1] < 1:
+    if not isinstance(Wg, torch.Tensor) or Wg.dim() != 2 or Wg.numel() == 0:
         raise ValueError("Wg must be a 2-D float16 or bfloat16 CUDA tensor")
     m, n = Wg.shape
-    if not isinstance(X, torch.Tensor) or X.dim() < 1 or X.shape[-1] != n:
+    if not isinstance(X, torch.Tensor) or X.dim() < 1 or X.shape[-1] != n or not X.is_cuda:
         raise ValueError(f"X must be a CUDA tensor whose last dimension is {n}")
-    if not isinstance(Wu, torch.Tensor) or tuple(Wu.shape) != (m, n):
+    if X.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("X, Wg and Wu must be float16 or bfloat16")
+    if not isinstance(Wu, torch.Tensor) or Wu.shape != Wg.shape:
         raise ValueError("Wg and Wu must have the same shape")
     return m, n
+
+
+def _flat(t: torch.Tensor) -> torch.Tensor:
+    return t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
+
+
+def _align_bytes(*tensors) -> int:
+    """Workspace for the operands whose rows do not start on 16-byte boundaries (externd_gated_work each)."""
+    total = 0
+    for t in tensors:
+        rows, cols = t.shape
+        if rows > 0 and (t.data_ptr() % 16 or (rows > 1 and t.stride(0) % 8)):
+            total += (rows * ((cols + 7) // 8 * 8) * 2 + 255) // 256 * 256
+    return total
 
 
 def _gated(X, Wg, Wu, act, save, out, async_status, stream):
     m, n = _gated_inputs(X, Wg, Wu)
     code = _act(act)
-    _check_status(async_status, X.device)
-    lead = X.shape[:-1]
-    with _on_stream(stream, X.device):
-        X2 = _dense_in(X.reshape(-1, n), n, "X")
-        Wg, Wu = _dense_in(Wg, n, "Wg", X2), _dense_in(Wu, n, "Wu", X2)
+    dev = X.device
+    _check_status(async_status, dev)
+    shape = (*X.shape[:-1], m)
+    if out is not None and (not isinstance(out, torch.Tensor) or out.shape != shape):
+        raise ValueError(f"out must have shape {shape}")
+    if save is not None and save not in (torch.float32, X.dtype):
+        raise ValueError("the projections can be saved in float32 or in X's type")
+    with _guard(stream, dev):
+        X2 = _rows_in(_flat(X), n, "X")
+        Wg, Wu = _rows_in(Wg, n, "Wg", X2), _rows_in(Wu, n, "Wu", X2)
         t = X2.shape[0]
-        if out is not None:
-            if not isinstance(out, torch.Tensor) or tuple(out.shape) != (*lead, m):
-                raise ValueError(f"out must have shape {(*lead, m)}")
-            out = out.view(-1, m)
-        H = _result(out, t, m, X2)
-        G = torch.empty((t, m), dtype=X2.dtype, device=X2.device) if save else None
-        U = torch.empty((t, m), dtype=X2.dtype, device=X2.device) if save else None
-        with _on_device(X2):
-            rc = _lib.load().externd_gated(_ptr(X2), _ld8(X2), _ptr(Wg), _ld8(Wg), _ptr(Wu), _ld8(Wu), _DTYPE[X2.dtype], m, n,
-                                           t, code, _ptr(H), _ld(H), _ptr(G) if t else None, _ptr(U) if t else None, m,
-                                           _ptr(async_status), _stream(stream, X2.device))
+        H = _result(None if out is None else out.view(-1, m), t, m, X2)
+        G = U = None
+        if save is not None:
+            G, U = torch.empty(shape, dtype=save, device=dev), torch.empty(shape, dtype=save, device=dev)
+        nbytes = _align_bytes(X2, Wg, Wu)
+        work = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
+        rc = _lib.load().externd_gated(X2.data_ptr(), _ld(X2), Wg.data_ptr(), _ld(Wg), Wu.data_ptr(), _ld(Wu), _DTYPE[X2.dtype],
+                                       m, n, t, code, H.data_ptr(), _ld(H), G.data_ptr() if t and save else None,
+                                       U.data_ptr() if t and save else None, _DTYPE[save or X2.dtype], m, _ptr(work), nbytes,
+                                       _ptr(async_status), _raw_stream())
     _check(rc, "externd_gated")
-    shape = (*lead, m)
-    return H.view(shape), G.view(shape) if save else None, U.view(shape) if save else None
+    return (H if X.dim() == 2 else H.view(shape)), G, U
 
 
 def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", *, out: Optional[torch.Tensor] = None,
           async_status=None, stream=None) -> torch.Tensor:
     """H = act(X Wg^T) * (X Wu^T) for X of shape (..., n) and Wg, Wu of shape (m, n), float16 or bfloat16
-    (externd_gated); act: "silu", "gelu", "gelu_tanh" or "relu2".  Rows that do not start on 16-byte boundaries
-    are copied first.  The call is asynchronous; autograd does not record it (gated_forward and
+    (externd_gated); act: "silu", "gelu", "gelu_tanh" or "relu2".  Operands whose rows do not start on 16-byte
+    boundaries are copied first.  The call is asynchronous; autograd does not record it (gated_forward and
     gated_backward are the training pair).  async_status: an int32 CUDA tensor that receives the status."""
-    return _gated(X, Wg, Wu, act, False, out, async_status, stream)[0]
+    return _gated(X, Wg, Wu, act, None, out, async_status, stream)[0]
 
 
-def gated_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", *, async_status=None, stream=None):
-    """(H, G, U): gated() with the projections G = X Wg^T and U = X Wu^T that gated_backward needs."""
-    return _gated(X, Wg, Wu, act, True, None, async_status, stream)
+def gated_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", *,
+                  save_dtype: torch.dtype = torch.float32, async_status=None, stream=None):
+    """(H, G, U): gated() with the projections G = X Wg^T and U = X Wu^T that gated_backward needs, in
+    float32, or in X's type (half the memory; their rounding then adds to the gradients' errors)."""
+    if save_dtype is None:
+        raise ValueError("the projections can be saved in float32 or in X's type")
+    return _gated(X, Wg, Wu, act, save_dtype, None, async_status, stream)
 
 
 def gated_backward(dH: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, G: torch.Tensor, U: torch.Tensor,
@@ -826,27 +835,35 @@ def gated_backward(dH: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torc
     (externd_gated_backward); need: which of the three to compute (None in place of the others)."""
     m, n = _gated_inputs(X, Wg, Wu)
     code = _act(act)
-    _check_status(async_status, X.device)
-    lead = X.shape[:-1]
-    for name, t in (("dH", dH), ("G", G), ("U", U)):
-        if not isinstance(t, torch.Tensor) or tuple(t.shape) != (*lead, m):
-            raise ValueError(f"{name} must have shape {(*lead, m)}")
-    with _on_stream(stream, X.device):
-        X2 = _dense_in(X.reshape(-1, n), n, "X")
-        Wg, Wu = _dense_in(Wg, n, "Wg", X2), _dense_in(Wu, n, "Wu", X2)
-        dH2, G2, U2 = (_rows_in(t.reshape(-1, m), m, name, X2) for name, t in (("dH", dH), ("G", G), ("U", U)))
+    dev = X.device
+    _check_status(async_status, dev)
+    shape = (*X.shape[:-1], m)
+    for name, v in (("dH", dH), ("G", G), ("U", U)):
+        if not isinstance(v, torch.Tensor) or v.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}")
+    if G.dtype != U.dtype or G.dtype not in (torch.float32, X.dtype):
+        raise ValueError("G and U must both be float32 or both of X's type")
+    with _guard(stream, dev):
+        X2 = _rows_in(_flat(X), n, "X")
+        Wg, Wu = _rows_in(Wg, n, "Wg", X2), _rows_in(Wu, n, "Wu", X2)
+        dH2, G2 = _rows_in(_flat(dH), m, "dH", X2), _rows_in(_flat(G), m, "G")
+        U2 = _rows_in(_flat(U), m, "U", G2)
+        if G2.device != dev:
+            raise ValueError("G and U must be on X's device")
         if _ld(G2) != _ld(U2):
             G2, U2 = G2.contiguous(), U2.contiguous()
         t = X2.shape[0]
-        dX = torch.empty((t, n), dtype=X2.dtype, device=X2.device) if need[0] else None
-        dWg = torch.empty((m, n), dtype=X2.dtype, device=X2.device) if need[1] else None
-        dWu = torch.empty((m, n), dtype=X2.dtype, device=X2.device) if need[2] else None
-        nbytes = int(_lib.load().externd_gated_backward_work(m, t))
-        work = torch.empty((max(nbytes, 256),), dtype=torch.uint8, device=X2.device)
-        with _on_device(X2):
-            rc = _lib.load().externd_gated_backward(
-                _ptr(dH2), _ld(dH2), _ptr(X2), _ld8(X2), _ptr(Wg), _ld8(Wg), _ptr(Wu), _ld8(Wu), _ptr(G2), _ptr(U2), _ld(G2),
-                _DTYPE[X2.dtype], m, n, t, code, _ptr(dX), n, _ptr(dWg), _ptr(dWu), n, _ptr(work), nbytes, _ptr(async_status),
-                _stream(stream, X2.device))
+        dX = torch.empty((t, n), dtype=X2.dtype, device=dev) if need[0] else None
+        dWg = torch.empty((m, n), dtype=X2.dtype, device=dev) if need[1] else None
+        dWu = torch.empty((m, n), dtype=X2.dtype, device=dev) if need[2] else None
+        nbytes = 0
+        if t and (need[0] or need[1] or need[2]):
+            used = ([Wg, Wu] if need[0] else []) + ([X2] if need[1] or need[2] else [])
+            nbytes = 2 * ((t * ((m + 7) // 8 * 8) * 2 + 255) // 256 * 256) + _align_bytes(*used)
+        work = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
+        rc = _lib.load().externd_gated_backward(
+            dH2.data_ptr(), _ld(dH2), X2.data_ptr(), _ld(X2), Wg.data_ptr(), _ld(Wg), Wu.data_ptr(), _ld(Wu), G2.data_ptr(),
+            U2.data_ptr(), _DTYPE[G2.dtype], _ld(G2), _DTYPE[X2.dtype], m, n, t, code, _ptr(dX), n, _ptr(dWg), _ptr(dWu), n,
+            _ptr(work), nbytes, _ptr(async_status), _raw_stream())
     _check(rc, "externd_gated_backward")
-    return dX.view(*lead, n) if need[0] else None, dWg, dWu
+    return (dX if dX is None or X.dim() == 2 else dX.view(X.shape)), dWg, dWu

@@ -139,7 +139,7 @@ enum Mode { FWD = 0, DX = 1, DW = 2 };
 constexpr int BK = 64;                     // depth of one stage: 128 bytes, one swizzle span
 constexpr int THREADS = 256;               // warp 0 TMA, warp 1 MMA, warps 4-7 epilogue
 constexpr int ACC = 256;                   // accumulator columns; two accumulators fill tensor memory
-constexpr int STG_ROW = 80;                // bytes of a staged row of 32 outputs (64 + 16: no bank conflicts)
+constexpr int STG_ROW = 144;               // bytes of a staged row of 32 fp32 outputs (128 + 16: no bank conflicts)
 
 template <int CG> struct Cfg {
     static constexpr int BM = 128 * CG;                    // tile rows (128 per CTA)
@@ -158,6 +158,7 @@ struct GemmArgs {
     void* out0; int64_t ld0; // FWD H, DX dX, DW dWg
     void* out1; int64_t ld1; // FWD G, DW dWu (FWD: may be null)
     void* out2;              // FWD U, leading dimension ld1
+    int save32;              // FWD: G and U in fp32 (otherwise in the operands' type)
     int* status;             // may be null
 };
 
@@ -166,28 +167,31 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
     return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
-// 32 columns of a warp's 32 rows, packed (16 registers a row), to global memory through the warp's staging
-// buffer: four lanes write a row's 64 bytes
-template <typename T>
-__device__ __forceinline__ void store32(const uint32_t (&v)[16], uint32_t stg, const unsigned char* stg_ptr, T* out, int64_t ld,
+// 32 columns of a warp's 32 rows (a row per lane, R registers) to global memory through the warp's staging
+// buffer, so that neighbouring lanes write neighbouring 16 bytes
+template <typename T, int R>
+__device__ __forceinline__ void store32(const uint32_t (&v)[R], uint32_t stg, const unsigned char* stg_ptr, T* out, int64_t ld,
                                         int row0, int rows, int col0, int cols, int lane) {
+    static_assert(R * 4 == 32 * sizeof(T), "a lane holds 32 outputs");
+    constexpr int Q = R / 4;                  // 16-byte pieces of a row
+    constexpr int E = 16 / sizeof(T);
     #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < Q; ++i)
         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(stg + lane * STG_ROW + 16 * i), "r"(v[4 * i]), "r"(v[4 * i + 1]),
                      "r"(v[4 * i + 2]), "r"(v[4 * i + 3]) : "memory");
     __syncwarp();
-    const bool vec = col0 + 32 <= cols && (ld & 7) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    const bool vec = col0 + 32 <= cols && ld % E == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
     if (vec) {
         #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2), c = lane & 3;
+        for (int i = 0; i < Q; ++i) {
+            const int r = (32 / Q) * i + lane / Q, c = lane % Q;
             const uint4 w = *reinterpret_cast<const uint4*>(stg_ptr + r * STG_ROW + 16 * c);
-            if (row0 + r < rows) *reinterpret_cast<uint4*>(out + (int64_t)(row0 + r) * ld + col0 + 8 * c) = w;
+            if (row0 + r < rows) *reinterpret_cast<uint4*>(out + (int64_t)(row0 + r) * ld + col0 + E * c) = w;
         }
     } else {
         #pragma unroll 4
         for (int r = 0; r < 32; ++r) {
-            const T w = *reinterpret_cast<const T*>(stg_ptr + r * STG_ROW + 2 * lane);
+            const T w = *reinterpret_cast<const T*>(stg_ptr + r * STG_ROW + (int)sizeof(T) * lane);
             if (row0 + r < rows && col0 + lane < cols) out[(int64_t)(row0 + r) * ld + col0 + lane] = w;
         }
     }
@@ -383,7 +387,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
                         default: gate_chunk<T, EXTERND_ACT_RELU2>(vg, vu, h); break;
                     }
                     store32<T>(h, stg, stg_ptr, out, ld, row0, g.rows, col0, g.cols, lane);
-                    if (g.out1) {
+                    if (g.out1 && g.save32) {
+                        store32<float>(vg, stg, stg_ptr, (float*)g.out1, g.ld1, row0, g.rows, col0, g.cols, lane);
+                        store32<float>(vu, stg, stg_ptr, (float*)g.out2, g.ld1, row0, g.rows, col0, g.cols, lane);
+                    } else if (g.out1) {
                         pack_chunk<T>(vg, h);
                         store32<T>(h, stg, stg_ptr, (T*)g.out1, g.ld1, row0, g.rows, col0, g.cols, lane);
                         pack_chunk<T>(vu, h);
@@ -425,24 +432,41 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
 // dG and dU from the saved projections
 // ---------------------------------------------------------------------------------------------------
 
-// Bound by memory: reads dH, G, U and writes dG, dU, 10 bytes per entry.  dG and dU are rounded to the
-// operands' type, which the tensor cores need (as the forward pass rounds G and U where it saves them).
-template <typename T, int ACT, bool VEC>
-__global__ void __launch_bounds__(256) gate_grad_kernel(const T* __restrict__ dh, int64_t lddh, const T* __restrict__ gs,
-                                                        const T* __restrict__ us, int64_t ldgu, int64_t rows, int64_t m,
+// Bound by memory: reads dH, G, U and writes dG, dU.  dG and dU are rounded to the operands' type, which the
+// tensor cores need.  Against a step that keeps everything in 32 bits this rounding makes the gradients' error
+// 1.4 times theirs (the output's rounding alone); G and U saved in 16 bits (S = T) make it 1.8 times, with
+// relu2, which doubles their relative error, 2.5 times.
+template <typename S> struct Saved8;                                       // 8 saved values
+template <> struct Saved8<float> {
+    float4 a, b;
+    __device__ __forceinline__ explicit Saved8(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ float2 pair(int e) const {
+        return e == 0 ? make_float2(a.x, a.y) : e == 1 ? make_float2(a.z, a.w) : e == 2 ? make_float2(b.x, b.y) : make_float2(b.z, b.w);
+    }
+};
+template <typename T> struct Saved8 {
+    uint4 a;
+    __device__ __forceinline__ explicit Saved8(const T* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ float2 pair(int e) const { return unpack2<T>(e == 0 ? a.x : e == 1 ? a.y : e == 2 ? a.z : a.w); }
+};
+
+template <typename T, typename S, int ACT, bool VEC>
+__global__ void __launch_bounds__(256) gate_grad_kernel(const T* __restrict__ dh, int64_t lddh, const S* __restrict__ gs,
+                                                        const S* __restrict__ us, int64_t ldgu, int64_t rows, int64_t m,
                                                         T* __restrict__ dg, T* __restrict__ du, int64_t ldw) {
-    const int64_t per = VEC ? (m + 7) / 8 : m;
+    const int64_t per = VEC ? m / 8 : m;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / per, c = i - r * per;
         if (VEC) {
-            const uint4 h4 = __ldg(reinterpret_cast<const uint4*>(dh + r * lddh) + c);
-            const uint4 g4 = __ldg(reinterpret_cast<const uint4*>(gs + r * ldgu) + c);
-            const uint4 u4 = __ldg(reinterpret_cast<const uint4*>(us + r * ldgu) + c);
-            const uint32_t hv[4] = {h4.x, h4.y, h4.z, h4.w}, gv[4] = {g4.x, g4.y, g4.z, g4.w}, uv[4] = {u4.x, u4.y, u4.z, u4.w};
+            const Saved8<T> h8(dh + r * lddh + 8 * c);
+            const Saved8<S> g8(gs + r * ldgu + 8 * c), u8(us + r * ldgu + 8 * c);
             uint32_t og[4], ou[4];
             #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 h = unpack2<T>(hv[e]), g = unpack2<T>(gv[e]), u = unpack2<T>(uv[e]);
+                const float2 h = h8.pair(e), g = g8.pair(e), u = u8.pair(e);
                 const float2 a = act_both<ACT, false>(g.x), b = act_both<ACT, false>(g.y);
                 og[e] = pack2<T>(h.x * u.x * a.y, h.y * u.y * b.y);
                 ou[e] = pack2<T>(h.x * a.x, h.y * b.x);
@@ -469,8 +493,8 @@ template <typename T, int NT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) dense_stream_kernel(const T* __restrict__ wg, int64_t ldg, const T* __restrict__ wu,
                                                                  int64_t ldu, int64_t m, int64_t n, int act,
                                                                  const T* __restrict__ x, int64_t ldx, int64_t tokens,
-                                                                 T* __restrict__ hout, int64_t ldh, T* __restrict__ gout,
-                                                                 T* __restrict__ uout, int64_t ldgu) {
+                                                                 T* __restrict__ hout, int64_t ldh, void* __restrict__ gout,
+                                                                 void* __restrict__ uout, int64_t ldgu, int save32) {
     constexpr int COLS = 8 * NT;
     __shared__ float part[2][WARPS][16][COLS + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -526,9 +550,13 @@ __global__ void __launch_bounds__(WARPS * 32) dense_stream_kernel(const T* __res
             u += part[1][p][rr][cc];
         }
         hout[cc * ldh + row0 + rr] = from_f32<T>(act_rt<false>(act, g) * u);
-        if (gout) {
-            gout[cc * ldgu + row0 + rr] = from_f32<T>(g);
-            uout[cc * ldgu + row0 + rr] = from_f32<T>(u);
+        const int64_t at = cc * ldgu + row0 + rr;
+        if (gout && save32) {
+            ((float*)gout)[at] = g;
+            ((float*)uout)[at] = u;
+        } else if (gout) {
+            ((T*)gout)[at] = from_f32<T>(g);
+            ((T*)uout)[at] = from_f32<T>(u);
         }
     }
 }
@@ -588,97 +616,174 @@ cudaError_t launch_gemm(const CUtensorMap& a0, const CUtensorMap& a1, const CUte
     return cudaLaunchKernelEx(&cfg, gemm_kernel<T, MODE, CG>, a0, a1, b0, b1, g);
 }
 
-bool good_matrix(const void* p, int64_t ld, int64_t cols) { return p && aligned(p, 16) && ld >= cols && ld % 8 == 0 && on_device(p); }
+// ---- operands whose rows do not start on 16-byte boundaries ------------------------------------------
+
+// Up to three matrices are laid out in rows that do, in one launch: 8 columns a thread.  TMA needs that, and
+// such operands are odd-sized ones; a model's own sizes never come here.
+struct AlignJob { const unsigned short* src; int64_t lds; unsigned short* dst; int64_t ldd; int64_t rows, cols; };
+struct AlignJobs { AlignJob j[3]; int count; };
+
+__global__ void __launch_bounds__(256) align_rows_kernel(const AlignJobs jobs) {
+    for (int q = 0; q < jobs.count; ++q) {
+        const AlignJob& j = jobs.j[q];
+        const int64_t per = j.ldd / 2;                              // pairs of a row: neighbouring lanes, neighbouring pairs
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < j.rows * per; i += (int64_t)gridDim.x * 256) {
+            const int64_t r = i / per, c = 2 * (i - r * per);
+            const unsigned short* p = j.src + r * j.lds + c;
+            const uint32_t lo = c < j.cols ? __ldg(p) : 0, hi = c + 1 < j.cols ? __ldg(p + 1) : 0;
+            *reinterpret_cast<uint32_t*>(j.dst + r * j.ldd + c) = lo | hi << 16;
+        }
+    }
+}
+
+int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
+size_t plane_bytes(int64_t rows, int64_t cols) { return ((size_t)rows * (size_t)round8(cols) * 2 + 255) / 256 * 256; }
+
+// one call's arguments, with the operands' final places
+struct Call {
+    const void* X; int64_t ldx;
+    const void* W[2]; int64_t ldw[2];
+    int dtype;
+    int64_t m, n, tokens;
+    int act;
+    void* H; int64_t ldh;
+    void* S[2]; int save_dtype; int64_t lds;          // G and U
+    const void* dH; int64_t lddh;
+    void* dX; int64_t lddx;
+    void* dW[2]; int64_t lddw;
+    unsigned char* work; size_t work_bytes;
+    int* status;
+    cudaStream_t stream;
+};
+
+bool row_aligned(const void* p, int64_t rows, int64_t ld) { return aligned(p, 16) && (rows < 2 || ld % 8 == 0); }
+
+// Move the operands that need it into `work` (consumed from its start).  Returns a status.
+int align_operands(Call& c, bool x, bool w) {
+    AlignJobs jobs = {};
+    const auto place = [&](const void*& p, int64_t& ld, int64_t rows) {
+        if (row_aligned(p, rows, ld)) {
+            if (rows < 2) ld = round8(c.n);                         // one row: any leading dimension serves
+            return true;
+        }
+        const size_t bytes = plane_bytes(rows, c.n);
+        if (!c.work || c.work_bytes < bytes) return false;
+        jobs.j[jobs.count++] = {(const unsigned short*)p, ld, (unsigned short*)c.work, round8(c.n), rows, c.n};
+        p = c.work;
+        ld = round8(c.n);
+        c.work += bytes;
+        c.work_bytes -= bytes;
+        return true;
+    };
+    if (x && !place(c.X, c.ldx, c.tokens)) return EXTERND_EINVAL;
+    if (w)
+        for (int i = 0; i < 2; ++i)
+            if (!place(c.W[i], c.ldw[i], c.m)) return EXTERND_EINVAL;
+    if (jobs.count) {
+        align_rows_kernel<<<(unsigned)sm_count() * 8, 256, 0, c.stream>>>(jobs);
+        if (cudaGetLastError() != cudaSuccess) return EXTERND_ECUDA;
+    }
+    return EXTERND_OK;
+}
 
 template <typename T, int CG>
-int forward_tiles(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu, int dtype, int64_t m, int64_t n,
-                  int64_t tokens, int act, void* H, int64_t ldh, void* G, void* U, int64_t ldgu, int* status, cudaStream_t s) {
+int forward_tiles(const Call& c) {
     CUtensorMap a, bg, bu;
-    if (!make_map(&a, X, tokens, n, ldx, 128, dtype) || !make_map(&bg, Wg, m, n, ldg, 128, dtype) || !make_map(&bu, Wu, m, n, ldu, 128, dtype))
+    if (!make_map(&a, c.X, c.tokens, c.n, c.ldx, 128, c.dtype) || !make_map(&bg, c.W[0], c.m, c.n, c.ldw[0], 128, c.dtype) ||
+        !make_map(&bu, c.W[1], c.m, c.n, c.ldw[1], 128, c.dtype))
         return EXTERND_ECUDA;
     GemmArgs g = {};
-    g.rows = (int)tokens; g.cols = (int)m; g.depth = (int)n;
-    g.tiles_r = (int)((tokens + Cfg<CG>::BM - 1) / Cfg<CG>::BM);
-    g.tiles_c = (int)((m + 127) / 128);
-    g.act = act;
-    g.out0 = H; g.ld0 = ldh; g.out1 = G; g.out2 = U; g.ld1 = ldgu; g.status = status;
-    return launch_gemm<T, FWD, CG>(a, a, bg, bu, g, s) == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
+    g.rows = (int)c.tokens; g.cols = (int)c.m; g.depth = (int)c.n;
+    g.tiles_r = (int)((c.tokens + Cfg<CG>::BM - 1) / Cfg<CG>::BM);
+    g.tiles_c = (int)((c.m + 127) / 128);
+    g.act = c.act;
+    g.out0 = c.H; g.ld0 = c.ldh; g.out1 = c.S[0]; g.out2 = c.S[1]; g.ld1 = c.lds; g.save32 = c.save_dtype == EXTERND_F32;
+    g.status = c.status;
+    return launch_gemm<T, FWD, CG>(a, a, bg, bu, g, c.stream) == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
+}
+
+template <typename T, int NT>
+int forward_stream(const Call& c) {
+    dense_stream_kernel<T, NT, 8><<<(unsigned)((c.m + 15) / 16), 256, 0, c.stream>>>(
+        (const T*)c.W[0], c.ldw[0], (const T*)c.W[1], c.ldw[1], c.m, c.n, c.act, (const T*)c.X, c.ldx, c.tokens, (T*)c.H, c.ldh, c.S[0],
+        c.S[1], c.lds, c.save_dtype == EXTERND_F32);
+    return cudaGetLastError() == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
 }
 
 template <typename T>
-int forward(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu, int dtype, int64_t m, int64_t n,
-            int64_t tokens, int act, void* H, int64_t ldh, void* G, void* U, int64_t ldgu, int* status, cudaStream_t s) {
-    if (tokens <= STREAM_TOKENS) {
-        const unsigned grid = (unsigned)((m + 15) / 16);
-        if (tokens <= 8)
-            dense_stream_kernel<T, 1, 8><<<grid, 256, 0, s>>>((const T*)Wg, ldg, (const T*)Wu, ldu, m, n, act, (const T*)X, ldx, tokens,
-                                                              (T*)H, ldh, (T*)G, (T*)U, ldgu);
-        else
-            dense_stream_kernel<T, 2, 8><<<grid, 256, 0, s>>>((const T*)Wg, ldg, (const T*)Wu, ldu, m, n, act, (const T*)X, ldx, tokens,
-                                                              (T*)H, ldh, (T*)G, (T*)U, ldgu);
-        return cudaGetLastError() == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
-    }
-    return forward_tiles<T, GATED_CG>(X, ldx, Wg, ldg, Wu, ldu, dtype, m, n, tokens, act, H, ldh, G, U, ldgu, status, s);
+int forward(const Call& c) {
+    if (c.tokens <= 8) return forward_stream<T, 1>(c);
+    if (c.tokens <= STREAM_TOKENS) return forward_stream<T, 2>(c);
+    return forward_tiles<T, GATED_CG>(c);
 }
 
-template <typename T, bool VEC>
-cudaError_t launch_gate_grad(int act, const void* dH, int64_t lddh, const void* G, const void* U, int64_t ldgu, int64_t tokens, int64_t m,
-                             T* dg, T* du, int64_t ldw, cudaStream_t s) {
-    const int64_t items = tokens * (VEC ? (m + 7) / 8 : m), cap = (int64_t)sm_count() * 32;
+template <typename T, typename S, bool VEC>
+cudaError_t launch_gate_grad(const Call& c, T* dg, T* du, int64_t ldd) {
+    const int64_t items = c.tokens * (VEC ? c.m / 8 : c.m), cap = (int64_t)sm_count() * 32;
     const unsigned grid = (unsigned)((items + 255) / 256 < cap ? (items + 255) / 256 : cap);
-    const T *h = (const T*)dH, *g = (const T*)G, *u = (const T*)U;
-    switch (act) {
-        case EXTERND_ACT_SILU: gate_grad_kernel<T, EXTERND_ACT_SILU, VEC><<<grid, 256, 0, s>>>(h, lddh, g, u, ldgu, tokens, m, dg, du, ldw); break;
-        case EXTERND_ACT_GELU: gate_grad_kernel<T, EXTERND_ACT_GELU, VEC><<<grid, 256, 0, s>>>(h, lddh, g, u, ldgu, tokens, m, dg, du, ldw); break;
-        case EXTERND_ACT_GELU_TANH: gate_grad_kernel<T, EXTERND_ACT_GELU_TANH, VEC><<<grid, 256, 0, s>>>(h, lddh, g, u, ldgu, tokens, m, dg, du, ldw); break;
-        default: gate_grad_kernel<T, EXTERND_ACT_RELU2, VEC><<<grid, 256, 0, s>>>(h, lddh, g, u, ldgu, tokens, m, dg, du, ldw); break;
+    const T* h = (const T*)c.dH;
+    const S *g = (const S*)c.S[0], *u = (const S*)c.S[1];
+    switch (c.act) {
+        case EXTERND_ACT_SILU:
+            gate_grad_kernel<T, S, EXTERND_ACT_SILU, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd);
+            break;
+        case EXTERND_ACT_GELU:
+            gate_grad_kernel<T, S, EXTERND_ACT_GELU, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd);
+            break;
+        case EXTERND_ACT_GELU_TANH:
+            gate_grad_kernel<T, S, EXTERND_ACT_GELU_TANH, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd);
+            break;
+        default:
+            gate_grad_kernel<T, S, EXTERND_ACT_RELU2, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd);
+            break;
     }
     return cudaGetLastError();
 }
 
-int64_t work_ld(int64_t m) { return (m + 7) / 8 * 8; }
-size_t work_plane(int64_t tokens, int64_t m) { return ((size_t)tokens * (size_t)work_ld(m) * 2 + 255) / 256 * 256; }
+template <typename T, typename S>
+cudaError_t gate_grad(const Call& c, T* dg, T* du, int64_t ldd) {
+    // whole vectors of 8 only where every row starts on a 16-byte boundary and ends with one
+    const bool vec = c.m % 8 == 0 && c.lddh % 8 == 0 && c.lds % (16 / sizeof(S)) == 0 && aligned(c.dH, 16) && aligned(c.S[0], 16) &&
+                     aligned(c.S[1], 16);
+    return vec ? launch_gate_grad<T, S, true>(c, dg, du, ldd) : launch_gate_grad<T, S, false>(c, dg, du, ldd);
+}
 
 template <typename T, int CG>
-int backward(const void* dH, int64_t lddh, const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu,
-             const void* G, const void* U, int64_t ldgu, int dtype, int64_t m, int64_t n, int64_t tokens, int act, void* dX, int64_t lddx,
-             void* dWg, void* dWu, int64_t lddw, void* work, int* status, cudaStream_t s) {
-    const int64_t ldw = work_ld(m);
-    T* dg = (T*)work;
-    T* du = (T*)((char*)work + work_plane(tokens, m));
-    // whole vectors of 8 only where the rows' tails are inside the rows
-    const bool vec = m % 8 == 0 && lddh % 8 == 0 && ldgu % 8 == 0 && aligned(dH, 16) && aligned(G, 16) && aligned(U, 16);
-    const cudaError_t e = vec ? launch_gate_grad<T, true>(act, dH, lddh, G, U, ldgu, tokens, m, dg, du, ldw, s)
-                              : launch_gate_grad<T, false>(act, dH, lddh, G, U, ldgu, tokens, m, dg, du, ldw, s);
+int backward(const Call& c) {
+    const int64_t ldd = round8(c.m);
+    const size_t plane = plane_bytes(c.tokens, c.m);
+    if (!c.work || c.work_bytes < 2 * plane) return EXTERND_EINVAL;
+    T* dg = (T*)c.work;
+    T* du = (T*)(c.work + plane);
+    const cudaError_t e = c.save_dtype == EXTERND_F32 ? gate_grad<T, float>(c, dg, du, ldd) : gate_grad<T, T>(c, dg, du, ldd);
     if (e != cudaSuccess) return EXTERND_ECUDA;
     constexpr int BM = Cfg<CG>::BM;
     GemmArgs g = {};
-    g.act = act;
-    g.status = status;
-    if (dX) {
+    g.status = c.status;
+    if (c.dX) {
         CUtensorMap a0, a1, b0, b1;
-        if (!make_map(&a0, dg, tokens, m, ldw, 128, dtype) || !make_map(&a1, du, tokens, m, ldw, 128, dtype) ||
-            !make_map(&b0, Wg, m, n, ldg, BK, dtype) || !make_map(&b1, Wu, m, n, ldu, BK, dtype))
+        if (!make_map(&a0, dg, c.tokens, c.m, ldd, 128, c.dtype) || !make_map(&a1, du, c.tokens, c.m, ldd, 128, c.dtype) ||
+            !make_map(&b0, c.W[0], c.m, c.n, c.ldw[0], BK, c.dtype) || !make_map(&b1, c.W[1], c.m, c.n, c.ldw[1], BK, c.dtype))
             return EXTERND_ECUDA;
-        g.rows = (int)tokens; g.cols = (int)n; g.depth = (int)m;
-        g.tiles_r = (int)((tokens + BM - 1) / BM);
-        g.tiles_c = (int)((n + 255) / 256);
-        g.out0 = dX; g.ld0 = lddx;
-        if (launch_gemm<T, DX, CG>(a0, a1, b0, b1, g, s) != cudaSuccess) return EXTERND_ECUDA;
+        g.rows = (int)c.tokens; g.cols = (int)c.n; g.depth = (int)c.m;
+        g.tiles_r = (int)((c.tokens + BM - 1) / BM);
+        g.tiles_c = (int)((c.n + 255) / 256);
+        g.out0 = c.dX; g.ld0 = c.lddx;
+        if (launch_gemm<T, DX, CG>(a0, a1, b0, b1, g, c.stream) != cudaSuccess) return EXTERND_ECUDA;
     }
-    if (dWg || dWu) {
-        // with one gradient only, both halves of the tile list would be the same: the list is that half
+    if (c.dW[0] || c.dW[1]) {
+        // the tile list holds the wanted matrices one after the other
         CUtensorMap a0, a1, b0;
-        if (!make_map(&a0, dWg ? dg : du, tokens, m, ldw, BK, dtype) || !make_map(&a1, du, tokens, m, ldw, BK, dtype) ||
-            !make_map(&b0, X, tokens, n, ldx, BK, dtype))
+        if (!make_map(&a0, c.dW[0] ? dg : du, c.tokens, c.m, ldd, BK, c.dtype) || !make_map(&a1, du, c.tokens, c.m, ldd, BK, c.dtype) ||
+            !make_map(&b0, c.X, c.tokens, c.n, c.ldx, BK, c.dtype))
             return EXTERND_ECUDA;
-        g.rows = (int)m; g.cols = (int)n; g.depth = (int)tokens;
-        g.half_r = (int)((m + BM - 1) / BM);
-        g.tiles_r = (dWg && dWu ? 2 : 1) * g.half_r;
-        g.tiles_c = (int)((n + 255) / 256);
-        g.out0 = dWg ? dWg : dWu; g.ld0 = lddw;
-        g.out1 = dWu; g.ld1 = lddw;
-        if (launch_gemm<T, DW, CG>(a0, a1, b0, b0, g, s) != cudaSuccess) return EXTERND_ECUDA;
+        g.rows = (int)c.m; g.cols = (int)c.n; g.depth = (int)c.tokens;
+        g.half_r = (int)((c.m + BM - 1) / BM);
+        g.tiles_r = (c.dW[0] && c.dW[1] ? 2 : 1) * g.half_r;
+        g.tiles_c = (int)((c.n + 255) / 256);
+        g.out0 = c.dW[0] ? c.dW[0] : c.dW[1]; g.ld0 = c.lddw;
+        g.out1 = c.dW[1]; g.ld1 = c.lddw;
+        if (launch_gemm<T, DW, CG>(a0, a1, b0, b0, g, c.stream) != cudaSuccess) return EXTERND_ECUDA;
     }
     return EXTERND_OK;
 }
@@ -689,65 +794,94 @@ bool too_large(int64_t m, int64_t n, int64_t tokens) {
     return (tokens / 128 + 1) * (m / 128 + 1) > lim || (tokens / 128 + 1) * (n / 128 + 1) > lim || 2 * (m / 128 + 1) * (n / 128 + 1) > lim;
 }
 
+// a matrix of elements of `bytes` bytes with at least `cols` columns of its leading dimension
+bool good(const Device& dev, const void* p, size_t bytes, int64_t ld, int64_t cols) {
+    return p && aligned(p, bytes) && ld >= cols && dev.holds(p);
+}
+
+bool good_common(const Device& dev, const Call& c) {
+    if (c.m < 1 || c.n < 1 || c.tokens < 0 || (c.dtype != EXTERND_F16 && c.dtype != EXTERND_BF16) || !valid_act(c.act)) return false;
+    if (c.work_bytes && !c.work) return false;
+    if (c.work && (!aligned(c.work, 256) || !dev.holds(c.work))) return false;
+    return !c.status || (aligned(c.status, 4) && dev.holds(c.status));
+}
+
+bool good_saved(const Device& dev, const Call& c) {
+    if (c.save_dtype != EXTERND_F32 && c.save_dtype != c.dtype) return false;
+    const size_t b = dtype_bytes(c.save_dtype);
+    return good(dev, c.S[0], b, c.lds, c.m) && good(dev, c.S[1], b, c.lds, c.m);
+}
+
 }  // namespace externd_ffn
 
 using namespace externd_ffn;
 
 extern "C" {
 
+size_t externd_gated_work(int64_t rows, int64_t n) { return rows < 1 || n < 1 ? 0 : plane_bytes(rows, n); }
+
 int externd_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu, int dtype, int64_t m, int64_t n,
-                  int64_t tokens, int act, void* H, int64_t ldh, void* G, void* U, int64_t ldgu, int* async_status, void* stream) {
-    if (m < 1 || n < 1 || tokens < 0 || (dtype != EXTERND_F16 && dtype != EXTERND_BF16) || !valid_act(act)) return EXTERND_EINVAL;
-    if (!good_matrix(Wg, ldg, n) || !good_matrix(Wu, ldu, n) || !G != !U) return EXTERND_EINVAL;
-    if (async_status && (!aligned(async_status, 4) || !on_device(async_status))) return EXTERND_EINVAL;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+                  int64_t tokens, int act, void* H, int64_t ldh, void* G, void* U, int save_dtype, int64_t ldgu, void* work,
+                  size_t work_bytes, int* async_status, void* stream) {
+    Call c = {};
+    c.X = X; c.ldx = ldx; c.W[0] = Wg; c.ldw[0] = ldg; c.W[1] = Wu; c.ldw[1] = ldu;
+    c.dtype = dtype; c.m = m; c.n = n; c.tokens = tokens; c.act = act;
+    c.H = H; c.ldh = ldh; c.S[0] = G; c.S[1] = U; c.save_dtype = save_dtype; c.lds = ldgu;
+    c.work = (unsigned char*)work; c.work_bytes = work_bytes; c.status = async_status;
+    c.stream = reinterpret_cast<cudaStream_t>(stream);
+    const Device dev;
+    if (!good_common(dev, c) || !G != !U) return EXTERND_EINVAL;
+    if (!good(dev, Wg, 2, ldg, n) || !good(dev, Wu, 2, ldu, n)) return EXTERND_EINVAL;
     if (tokens > 0) {
-        if (!good_matrix(X, ldx, n) || !H || !aligned(H, 2) || ldh < m || !on_device(H)) return EXTERND_EINVAL;
-        if (G && (!aligned(G, 2) || !aligned(U, 2) || ldgu < m || !on_device(G) || !on_device(U))) return EXTERND_EINVAL;
+        if (!good(dev, X, 2, ldx, n) || !good(dev, H, 2, ldh, m) || (G && !good_saved(dev, c))) return EXTERND_EINVAL;
         if (too_large(m, n, tokens)) return EXTERND_ELIMIT;
     }
-    if (async_status && cudaMemsetAsync(async_status, 0, sizeof(int), s) != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
+    if (async_status && cudaMemsetAsync(async_status, 0, sizeof(int), c.stream) != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
     if (tokens == 0) return EXTERND_OK;
-    const int rc = dtype == EXTERND_F16
-                       ? forward<__half>(X, ldx, Wg, ldg, Wu, ldu, dtype, m, n, tokens, act, H, ldh, G, U, ldgu, async_status, s)
-                       : forward<__nv_bfloat16>(X, ldx, Wg, ldg, Wu, ldu, dtype, m, n, tokens, act, H, ldh, G, U, ldgu, async_status, s);
+    int rc = align_operands(c, true, true);
+    if (rc == EXTERND_OK) rc = dtype == EXTERND_F16 ? forward<__half>(c) : forward<__nv_bfloat16>(c);
     if (rc != EXTERND_OK) cudaGetLastError();
     return rc;
 }
 
-size_t externd_gated_backward_work(int64_t m, int64_t tokens) { return m < 1 || tokens < 1 ? 0 : 2 * work_plane(tokens, m); }
+size_t externd_gated_backward_work(int64_t m, int64_t tokens) { return m < 1 || tokens < 1 ? 0 : 2 * plane_bytes(tokens, m); }
 
 int externd_gated_backward(const void* dH, int64_t lddh, const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu,
-                           int64_t ldu, const void* G, const void* U, int64_t ldgu, int dtype, int64_t m, int64_t n, int64_t tokens,
-                           int act, void* dX, int64_t lddx, void* dWg, void* dWu, int64_t lddw, void* work, size_t work_bytes,
-                           int* async_status, void* stream) {
-    if (m < 1 || n < 1 || tokens < 0 || (dtype != EXTERND_F16 && dtype != EXTERND_BF16) || !valid_act(act)) return EXTERND_EINVAL;
-    if (async_status && (!aligned(async_status, 4) || !on_device(async_status))) return EXTERND_EINVAL;
-    void* dw[2] = {dWg, dWu};
-    for (void* p : dw)
-        if (p && (!aligned(p, 2) || lddw < n || !on_device(p))) return EXTERND_EINVAL;
-    if (tokens > 0) {
-        if (!dH || !G || !U || !aligned(dH, 2) || !aligned(G, 2) || !aligned(U, 2) || lddh < m || ldgu < m || !on_device(dH) ||
-            !on_device(G) || !on_device(U))
-            return EXTERND_EINVAL;
-        if (dX && (!aligned(dX, 2) || lddx < n || !on_device(dX) || !good_matrix(Wg, ldg, n) || !good_matrix(Wu, ldu, n))) return EXTERND_EINVAL;
-        if ((dWg || dWu) && !good_matrix(X, ldx, n)) return EXTERND_EINVAL;
-        if (!work || !aligned(work, 256) || work_bytes < externd_gated_backward_work(m, tokens) || !on_device(work)) return EXTERND_EINVAL;
+                           int64_t ldu, const void* G, const void* U, int save_dtype, int64_t ldgu, int dtype, int64_t m, int64_t n,
+                           int64_t tokens, int act, void* dX, int64_t lddx, void* dWg, void* dWu, int64_t lddw, void* work,
+                           size_t work_bytes, int* async_status, void* stream) {
+    Call c = {};
+    c.X = X; c.ldx = ldx; c.W[0] = Wg; c.ldw[0] = ldg; c.W[1] = Wu; c.ldw[1] = ldu;
+    c.dtype = dtype; c.m = m; c.n = n; c.tokens = tokens; c.act = act;
+    c.S[0] = const_cast<void*>(G); c.S[1] = const_cast<void*>(U); c.save_dtype = save_dtype; c.lds = ldgu;
+    c.dH = dH; c.lddh = lddh; c.dX = dX; c.lddx = lddx; c.dW[0] = dWg; c.dW[1] = dWu; c.lddw = lddw;
+    c.work = (unsigned char*)work; c.work_bytes = work_bytes; c.status = async_status;
+    c.stream = reinterpret_cast<cudaStream_t>(stream);
+    const Device dev;
+    const bool dw = dWg || dWu;
+    if (!good_common(dev, c)) return EXTERND_EINVAL;
+    for (void* p : c.dW)
+        if (p && !good(dev, p, 2, lddw, n)) return EXTERND_EINVAL;
+    if (tokens > 0 && (dX || dw)) {
+        if (!good(dev, dH, 2, lddh, m) || !good_saved(dev, c)) return EXTERND_EINVAL;
+        if (dX && (!good(dev, dX, 2, lddx, n) || !good(dev, Wg, 2, ldg, n) || !good(dev, Wu, 2, ldu, n))) return EXTERND_EINVAL;
+        if (dw && !good(dev, X, 2, ldx, n)) return EXTERND_EINVAL;
         if (too_large(m, n, tokens)) return EXTERND_ELIMIT;
+        size_t need = externd_gated_backward_work(m, tokens);
+        if (dX)
+            for (int i = 0; i < 2; ++i) need += row_aligned(c.W[i], m, c.ldw[i]) ? 0 : plane_bytes(m, n);
+        if (dw) need += row_aligned(X, tokens, ldx) ? 0 : plane_bytes(tokens, n);
+        if (!work || work_bytes < need) return EXTERND_EINVAL;
     }
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (async_status && cudaMemsetAsync(async_status, 0, sizeof(int), s) != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
+    if (async_status && cudaMemsetAsync(async_status, 0, sizeof(int), c.stream) != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
     if (tokens == 0) {
-        for (void* p : dw)   // a sum of no terms
-            if (p && cudaMemset2DAsync(p, (size_t)lddw * 2, 0, (size_t)n * 2, (size_t)m, s) != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
+        for (void* p : c.dW)   // a sum of no terms
+            if (p && cudaMemset2DAsync(p, (size_t)lddw * 2, 0, (size_t)n * 2, (size_t)m, c.stream) != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
         return EXTERND_OK;
     }
-    if (!dX && !dWg && !dWu) return EXTERND_OK;
-    const int rc = dtype == EXTERND_F16
-                       ? backward<__half, GATED_CG>(dH, lddh, X, ldx, Wg, ldg, Wu, ldu, G, U, ldgu, dtype, m, n, tokens, act, dX, lddx, dWg,
-                                                    dWu, lddw, work, async_status, s)
-                       : backward<__nv_bfloat16, GATED_CG>(dH, lddh, X, ldx, Wg, ldg, Wu, ldu, G, U, ldgu, dtype, m, n, tokens, act, dX,
-                                                           lddx, dWg, dWu, lddw, work, async_status, s);
+    if (!dX && !dw) return EXTERND_OK;
+    int rc = align_operands(c, dw, dX != nullptr);
+    if (rc == EXTERND_OK) rc = dtype == EXTERND_F16 ? backward<__half, GATED_CG>(c) : backward<__nv_bfloat16, GATED_CG>(c);
     if (rc != EXTERND_OK) cudaGetLastError();
     return rc;
 }

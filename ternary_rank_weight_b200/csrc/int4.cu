@@ -346,14 +346,15 @@ int products(const Mat4& w0, const Mat4& w1, int64_t m, int64_t n, int group, in
              int64_t batch, void* Y, int64_t ldy, void* stream) {
     if (m < 1 || n < 1 || batch < 0 || !valid_group(group) || !valid_dtype(dtype) || ldx < n || ldy < m) return EXTERND_EINVAL;
     if (NM == 2 && !valid_act(act)) return EXTERND_EINVAL;
+    const Device dev;
     const Mat4* w[2] = {&w0, &w1};
     for (int j = 0; j < NM; ++j) {
         if (!w[j]->q || !w[j]->scale || !aligned(w[j]->q, 16) || !aligned(w[j]->scale, 2) || !aligned(w[j]->offset, 2)) return EXTERND_EINVAL;
-        if (!on_device(w[j]->q) || !on_device(w[j]->scale) || (w[j]->offset && !on_device(w[j]->offset))) return EXTERND_EINVAL;
+        if (!dev.holds(w[j]->q) || !dev.holds(w[j]->scale) || (w[j]->offset && !dev.holds(w[j]->offset))) return EXTERND_EINVAL;
     }
     if (batch == 0) return EXTERND_OK;
     const size_t eb = dtype_bytes(dtype);
-    if (!X || !Y || !aligned(X, eb) || !aligned(Y, eb) || !on_device(X) || !on_device(Y)) return EXTERND_EINVAL;
+    if (!X || !Y || !aligned(X, eb) || !aligned(Y, eb) || !dev.holds(X) || !dev.holds(Y)) return EXTERND_EINVAL;
     if ((m + 15) / 16 > 0x7fffffff || (batch + 7) / 8 > 65535) return EXTERND_ELIMIT;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
@@ -405,8 +406,9 @@ int externd_int4_quantize(const void* A, int dtype, int64_t m, int64_t n, int64_
     if (!aligned(A, dtype_bytes(dtype)) || !aligned(q_out, 16) || !aligned(scale_out, 2) || !aligned(offset_out, 2) ||
         !aligned(async_status, 4))
         return EXTERND_EINVAL;
-    if (!on_device(A) || !on_device(q_out) || !on_device(scale_out) || (offset_out && !on_device(offset_out)) ||
-        (async_status && !on_device(async_status)))
+    const Device dev;
+    if (!dev.holds(A) || !dev.holds(q_out) || !dev.holds(scale_out) || (offset_out && !dev.holds(offset_out)) ||
+        (async_status && !dev.holds(async_status)))
         return EXTERND_EINVAL;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int* status = async_status;
@@ -446,7 +448,8 @@ int externd_int4_dequantize(const uint8_t* q, const void* scale, const void* off
                             int dtype, int64_t ldo, void* stream) {
     if (!q || !scale || !out || m < 1 || n < 1 || ldo < n || !valid_dtype(dtype) || !valid_group(group)) return EXTERND_EINVAL;
     if (!aligned(q, 16) || !aligned(scale, 2) || !aligned(offset, 2) || !aligned(out, dtype_bytes(dtype))) return EXTERND_EINVAL;
-    if (!on_device(q) || !on_device(scale) || (offset && !on_device(offset)) || !on_device(out)) return EXTERND_EINVAL;
+    const Device dev;
+    if (!dev.holds(q) || !dev.holds(scale) || (offset && !dev.holds(offset)) || !dev.holds(out)) return EXTERND_EINVAL;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (dtype) {

@@ -115,17 +115,19 @@ inline bool valid_act(int a) { return a >= EXTERND_ACT_SILU && a <= EXTERND_ACT_
 inline bool valid_group(int g) { return g == 32 || g == 64 || g == 128; }
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// memory that kernels on the current device may use
-inline bool on_device(const void* p) {
-    cudaPointerAttributes a;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
+// the current device, and whether its kernels may use a pointer
+struct Device {
+    int id = -1;
+    Device() { if (cudaGetDevice(&id) != cudaSuccess) { cudaGetLastError(); id = -1; } }
+    bool holds(const void* p) const {
+        cudaPointerAttributes a;
+        if (id < 0 || cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        return a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == id);
     }
-    if (a.type == cudaMemoryTypeManaged) return true;
-    return a.type == cudaMemoryTypeDevice && a.device == dev;
-}
+};
 
 inline int sm_count() {
     int dev = 0, v = 148;

@@ -34,8 +34,8 @@ def _check_forward(X, Wg, Wu, act, H, G=None, Up=None):
     assert H.dtype == X.dtype and H.shape == h.shape
     assert torch.all((H.double() - h).abs() <= bound * (1 + 2.0 ** -8) + half_step(X.dtype, h))
     if G is not None:
-        assert torch.all((G.double() - g).abs() <= dg * (1 + 2.0 ** -8) + half_step(X.dtype, g))
-        assert torch.all((Up.double() - u).abs() <= du * (1 + 2.0 ** -8) + half_step(X.dtype, u))
+        assert torch.all((G.double() - g).abs() <= dg * (1 + 2.0 ** -8) + half_step(G.dtype, g))
+        assert torch.all((Up.double() - u).abs() <= du * (1 + 2.0 ** -8) + half_step(G.dtype, u))
 
 
 def _check_backward(X, Wg, Wu, dH, act, G, Up, got):
@@ -75,8 +75,11 @@ def test_forward_matches_64_bits(t, m, n, dtype):
     for act in ACTS:
         X, Wg, Wu, _ = _make(t, m, n, dtype)
         H, G, Up = ext.gated_forward(X, Wg, Wu, act)
+        assert G.dtype == Up.dtype == torch.float32
         _check_forward(X, Wg, Wu, act, H, G, Up)
         assert torch.equal(ext.gated(X, Wg, Wu, act), H)
+        H2, G2, U2 = ext.gated_forward(X, Wg, Wu, act, save_dtype=dtype)
+        assert torch.equal(H2, H) and torch.equal(G2, G.to(dtype)) and torch.equal(U2, Up.to(dtype))
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
@@ -84,9 +87,10 @@ def test_forward_matches_64_bits(t, m, n, dtype):
 def test_backward_matches_64_bits(t, m, n, dtype):
     for act in ACTS:
         X, Wg, Wu, dH = _make(t, m, n, dtype, seed=1)
-        _, G, Up = ext.gated_forward(X, Wg, Wu, act)
-        got = ext.gated_backward(dH, X, Wg, Wu, G, Up, act)
-        _check_backward(X, Wg, Wu, dH, act, G, Up, got)
+        for save in (torch.float32, dtype):
+            _, G, Up = ext.gated_forward(X, Wg, Wu, act, save_dtype=save)
+            got = ext.gated_backward(dH, X, Wg, Wu, G, Up, act)
+            _check_backward(X, Wg, Wu, dH, act, G, Up, got)
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
@@ -185,7 +189,7 @@ def test_shapes_strides_and_partial_gradients():
     Xv, Wv, dv, Wt = bigX[:, 5:5 + n], bigW[:, 8:8 + n], bigd[:, 1:1 + m], Wu.t().contiguous().t()
     H3, G3, U3 = ext.gated_forward(Xv, Wv, Wt)
     assert torch.equal(H3, H) and torch.equal(G3, G) and torch.equal(U3, Up)
-    for a, b in zip(ext.gated_backward(dv, Xv, Wv, Wt, bigd.new_zeros(t, m + 3)[:, :m].copy_(G3), U3), ref):
+    for a, b in zip(ext.gated_backward(dv, Xv, Wv, Wt, G3.new_zeros(t, m + 3)[:, :m].copy_(G3), U3), ref):
         assert torch.equal(a, b)
     out = torch.full((t + 2, m + 7), 5.0, dtype=BF16, device="cuda")
     got = ext.gated(X, Wg, Wu, out=out[1:-1, 3:3 + m])
@@ -291,26 +295,27 @@ def test_library_refuses_bad_arguments():
     X, Wg, Wu, dH = _make(t, m, n, BF16)
     H, G, Up = ext.gated_forward(X, Wg, Wu)
     out = [torch.zeros(s, dtype=BF16, device="cuda") for s in ((t, n), (m, n), (m, n))]
-    work = torch.zeros(L.externd_gated_backward_work(m, t), dtype=torch.uint8, device="cuda")
+    need = L.externd_gated_backward_work(m, t)
+    work = torch.zeros(need + 3 * L.externd_gated_work(m, n), dtype=torch.uint8, device="cuda")
     host = torch.zeros(1 << 16, dtype=torch.uint8)
     st = torch.cuda.current_stream().cuda_stream
     base = dict(x=X.data_ptr(), ldx=n, wg=Wg.data_ptr(), ldg=n, wu=Wu.data_ptr(), ldu=n, dt=2, m=m, n=n, t=t, act=0, h=H.data_ptr(),
-                ldh=m, g=G.data_ptr(), u=Up.data_ptr(), ldgu=m, status=None, dh=dH.data_ptr(), lddh=m, dx=out[0].data_ptr(), lddx=n,
-                dwg=out[1].data_ptr(), dwu=out[2].data_ptr(), lddw=n, work=work.data_ptr(), wb=work.numel())
+                ldh=m, g=G.data_ptr(), u=Up.data_ptr(), ldgu=m, sd=0, fw=None, fwb=0, status=None, dh=dH.data_ptr(), lddh=m, dx=out[0].data_ptr(), lddx=n,
+                dwg=out[1].data_ptr(), dwu=out[2].data_ptr(), lddw=n, work=work.data_ptr(), wb=need)
 
     def fwd(**kw):
         a = dict(base, **kw)
-        return L.externd_gated(*(a[k] for k in "x ldx wg ldg wu ldu dt m n t act h ldh g u ldgu status".split()), st)
+        return L.externd_gated(*(a[k] for k in "x ldx wg ldg wu ldu dt m n t act h ldh g u sd ldgu fw fwb status".split()), st)
 
     def bwd(**kw):
         a = dict(base, **kw)
-        return L.externd_gated_backward(*(a[k] for k in "dh lddh x ldx wg ldg wu ldu g u ldgu dt m n t act dx lddx dwg dwu lddw work "
+        return L.externd_gated_backward(*(a[k] for k in "dh lddh x ldx wg ldg wu ldu g u sd ldgu dt m n t act dx lddx dwg dwu lddw work "
                                           "wb status".split()), st)
 
     assert fwd() == 0 and bwd() == 0 and fwd(g=None, u=None) == 0
     common = [dict(x=None), dict(wg=None), dict(wu=None), dict(dt=0), dict(dt=5), dict(m=0), dict(n=0), dict(t=-1), dict(act=4),
               dict(act=-1), dict(ldx=n + 1), dict(ldx=n - 8), dict(ldg=n + 4), dict(ldu=n - 8), dict(x=X.data_ptr() + 2),
-              dict(wg=Wg.data_ptr() + 8), dict(x=host.data_ptr()), dict(wu=host.data_ptr()), dict(status=host.data_ptr()),
+              dict(wg=Wg.data_ptr() + 1), dict(wg=Wg.data_ptr() + 8), dict(sd=1), dict(sd=7), dict(x=host.data_ptr()), dict(wu=host.data_ptr()), dict(status=host.data_ptr()),
               dict(u=None), dict(ldgu=m - 1), dict(g=G.data_ptr() + 1)]
     for kw in common:
         assert fwd(**kw) == einval, kw
@@ -318,8 +323,13 @@ def test_library_refuses_bad_arguments():
     for kw in (dict(h=None), dict(ldh=m - 1), dict(h=host.data_ptr()), dict(g=None)):
         assert fwd(**kw) == einval, kw
     for kw in (dict(dh=None), dict(lddh=m - 1), dict(dx=host.data_ptr()), dict(lddx=n - 1), dict(lddw=n - 1), dict(work=None),
-               dict(wb=work.numel() - 1), dict(work=work.data_ptr() + 16), dict(dwg=host.data_ptr())):
+               dict(wb=need - 1), dict(work=work.data_ptr() + 16), dict(dwg=host.data_ptr())):
         assert bwd(**kw) == einval, kw
+    # rows off the 16-byte boundaries take their place in work
+    over = (work.data_ptr(), L.externd_gated_work(t, n))
+    assert fwd(x=X.data_ptr() + 2, t=t - 1, fw=over[0], fwb=over[1]) == 0
+    assert fwd(x=X.data_ptr() + 2, t=t - 1, fw=over[0], fwb=L.externd_gated_work(t - 1, n) - 1) == einval
+    assert bwd(x=X.data_ptr() + 2, t=t - 1, wb=need + over[1]) == 0
     assert bwd(dx=None, wg=None, wu=None) == 0 and bwd(dwg=None, dwu=None, x=None) == 0
     with pytest.raises(ValueError):
         ext.gated(X.float(), Wg.float(), Wu.float())

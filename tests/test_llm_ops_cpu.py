@@ -64,13 +64,18 @@ def test_gated_entry_points_reject_bad_arguments_before_device_work():
     L = _lib.load()
     host = (ctypes.c_uint8 * 512)()
     p = (ctypes.addressof(host) + 255) // 256 * 256
-    assert L.externd_gated(p, 8, p, 8, p, 8, 2, 1, 1, 1, 0, p, 1, None, None, 1, None, None) == EINVAL   # host memory
-    assert L.externd_gated(p, 8, None, 8, p, 8, 2, 1, 1, 1, 0, p, 1, None, None, 1, None, None) == EINVAL
-    assert L.externd_gated(p, 8, p, 8, p, 8, 0, 1, 1, 1, 0, p, 1, None, None, 1, None, None) == EINVAL   # fp32
-    assert L.externd_gated(p, 8, p, 8, p, 8, 2, 1, 1, 1, 9, p, 1, None, None, 1, None, None) == EINVAL   # activation
-    assert L.externd_gated(p, 8, p, 8, p, 8, 2, 0, 1, 1, 0, p, 1, None, None, 1, None, None) == EINVAL
-    assert L.externd_gated(p, 8, p, 8, p, 8, 2, 1, 1, -1, 0, p, 1, None, None, 1, None, None) == EINVAL
-    assert L.externd_gated_backward(p, 1, p, 8, p, 8, p, 8, p, p, 1, 2, 1, 1, 1, 0, p, 1, p, p, 1, p, 512, None, None) == EINVAL
+    base = dict(x=p, w=p, dt=2, m=1, n=1, t=1, act=0, h=p, g=None, sd=0, wb=0, work=None)
+
+    def fwd(**kw):
+        a = dict(base, **kw)
+        return L.externd_gated(a["x"], 8, p, 8, a["w"], 8, a["dt"], a["m"], a["n"], a["t"], a["act"], a["h"], 1, a["g"], a["g"],
+                               a["sd"], 1, a["work"], a["wb"], None, None)
+
+    for kw in ({}, dict(w=None), dict(dt=0), dict(act=9), dict(m=0), dict(n=0), dict(t=-1), dict(h=None), dict(wb=256)):
+        assert fwd(**kw) == EINVAL, kw                                       # {}: host memory
+    assert L.externd_gated_backward(p, 1, p, 8, p, 8, p, 8, p, p, 0, 1, 2, 1, 1, 1, 0, p, 1, p, p, 1, p, 512, None, None) == EINVAL
+    assert L.externd_gated_work(0, 5) == 0 and L.externd_gated_work(5, 0) == 0
+    assert L.externd_gated_work(3, 9) == 256 and L.externd_gated_work(100, 9) == 3328
     assert L.externd_gated_backward_work(0, 5) == 0 and L.externd_gated_backward_work(5, 0) == 0
     assert L.externd_gated_backward_work(1000, 300) == 2 * ((300 * 1000 * 2 + 255) // 256 * 256)
     assert L.externd_gated_backward_work(3, 1) == 512                       # rows of 8 elements, planes on 256 bytes
