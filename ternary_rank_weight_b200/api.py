@@ -569,9 +569,9 @@ def _guard(stream, device: torch.device):
     return torch.cuda.stream(stream)
 
 
-def _raw_stream() -> int:
-    """The current stream, inside _guard."""
-    return torch.cuda.current_stream().cuda_stream
+# the current stream's handle without building a Stream object (3 us of a call's 11), where torch offers it
+_handle_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _rows_in(t, cols: int, name: str, like: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -579,24 +579,28 @@ def _rows_in(t, cols: int, name: str, like: Optional[torch.Tensor] = None) -> to
     types; rows may be strided."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda or t.dtype not in _DTYPE:
         raise ValueError(f"{name} must be a 2-D float32, float16 or bfloat16 CUDA tensor")
-    if t.shape[1] != cols:
-        raise ValueError(f"{name} must have {cols} columns, not {t.shape[1]}")
+    rows, width = t.shape
+    if width != cols:
+        raise ValueError(f"{name} must have {cols} columns, not {width}")
     if like is not None and (t.dtype != like.dtype or t.device != like.device):
         raise ValueError(f"{name} must have the element type and device of the other tensors")
-    if t.shape[0] > 0 and (t.stride(1) != 1 and cols > 1 or t.shape[0] > 1 and t.stride(0) < cols):
-        t = t.contiguous()
+    if rows:
+        ld, step = t.stride()
+        if (step != 1 and cols > 1) or (rows > 1 and ld < cols):
+            return t.contiguous()
     return t
 
 
 def _ld(t: torch.Tensor) -> int:
-    """Leading dimension (rows of at most one element's worth may carry any stride)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    """Leading dimension (that of a single row may be anything)."""
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 else max(cols, 1)
 
 
 def _result(out, rows: int, cols: int, like: torch.Tensor) -> torch.Tensor:
     if out is None:
-        return torch.empty((rows, cols), dtype=like.dtype, device=like.device)
-    if (not isinstance(out, torch.Tensor) or tuple(out.shape) != (rows, cols) or out.dtype != like.dtype
+        return like.new_empty((rows, cols))
+    if (not isinstance(out, torch.Tensor) or out.shape != (rows, cols) or out.dtype != like.dtype
             or out.device != like.device or (cols > 1 and out.stride(1) != 1)
             or (rows > 1 and out.stride(0) < cols)):
         raise ValueError(f"out must be a {rows} x {cols} {like.dtype} tensor on {like.device} with unit column stride")
@@ -628,17 +632,19 @@ class Int4Weights:
         return unpack_int4(self.q.cpu().numpy(), self.n)
 
 
-def _check_int4(w: Int4Weights, device: Optional[torch.device] = None):
-    if not isinstance(w, Int4Weights) or w.m < 1 or w.n < 1 or w.group not in (32, 64, 128):
-        raise ValueError("w must be Int4Weights with m, n >= 1 and groups of 32, 64 or 128 columns")
-    groups = (w.n + w.group - 1) // w.group
-    want = [("q", w.q, (w.m, int4_row_bytes(w.n)), torch.uint8), ("scale", w.scale, (groups, w.m), torch.float16)]
-    if w.offset is not None:
-        want.append(("offset", w.offset, (groups, w.m), torch.float16))
-    for name, t, shape, dtype in want:
-        if (not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda
-                or not t.is_contiguous() or (device is not None and t.device != device)):
-            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape} on the vectors' device")
+def _check_int4(w: Int4Weights, device: torch.device):
+    if not isinstance(w, Int4Weights):
+        raise ValueError("4-bit matrices are given as Int4Weights")
+    m, n, group = w.m, w.n, w.group
+    if m < 1 or n < 1 or group not in (32, 64, 128):
+        raise ValueError("Int4Weights need m, n >= 1 and groups of 32, 64 or 128 columns")
+    q, scale, offset = w.q, w.scale, w.offset
+    scales = ((n + group - 1) // group, m)
+    if q.dtype != torch.uint8 or q.shape != (m, (n + 127) // 128 * 64) or q.device != device or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous uint8 tensor of {m} rows of int4_row_bytes({n}) on {device}")
+    for t in (scale,) if offset is None else (scale, offset):
+        if t.dtype != torch.float16 or t.shape != scales or t.device != device or not t.is_contiguous():
+            raise ValueError(f"scale and offset must be contiguous float16 tensors of shape {scales} on {device}")
 
 
 def int4_quantize(A: torch.Tensor, group: int = 128, *, affine: bool = True, async_status=None,
@@ -653,31 +659,35 @@ def int4_quantize(A: torch.Tensor, group: int = 128, *, affine: bool = True, asy
         raise ValueError("A must be a 2-D float32, float16 or bfloat16 CUDA tensor that is not empty")
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
-    _check_status(async_status, A.device)
-    with _guard(stream, A.device):
+    dev = A.device
+    _check_status(async_status, dev)
+    with _guard(stream, dev):
         A2 = _rows_in(A, A.shape[1], "A")
         if async_status is not None and A2 is not A:
             raise ValueError("an asynchronous call needs A with unit column stride")
         m, n = A2.shape
         groups = (n + group - 1) // group
-        q = torch.empty((m, (n + 127) // 128 * 64), dtype=torch.uint8, device=A2.device)
-        scale = torch.empty((groups, m), dtype=torch.float16, device=A2.device)
-        offset = torch.empty((groups, m), dtype=torch.float16, device=A2.device) if affine else None
+        q = torch.empty((m, (n + 127) // 128 * 64), dtype=torch.uint8, device=dev)
+        scale = torch.empty((groups, m), dtype=torch.float16, device=dev)
+        offset = torch.empty((groups, m), dtype=torch.float16, device=dev) if affine else None
         rc = _lib.load().externd_int4_quantize(A2.data_ptr(), _DTYPE[A2.dtype], m, n, _ld(A2), int(group), q.data_ptr(),
-                                               scale.data_ptr(), _ptr(offset), _ptr(async_status), _raw_stream())
+                                               scale.data_ptr(), _ptr(offset), _ptr(async_status), _handle_of(dev.index))
     _check(rc, "externd_int4_quantize")
     return Int4Weights(q=q, scale=scale, offset=offset, m=m, n=n, group=int(group))
 
 
 def int4_dequantize(w: Int4Weights, dtype: torch.dtype = torch.float32, *, stream=None) -> torch.Tensor:
     """The m x n matrix that the 4 bits stand for, rounded once to dtype (externd_int4_dequantize)."""
-    _check_int4(w)
+    if not isinstance(w, Int4Weights) or not w.q.is_cuda:
+        raise ValueError("w must be Int4Weights on the GPU")
     if dtype not in _DTYPE:
         raise ValueError("dtype must be float32, float16 or bfloat16")
-    with _guard(stream, w.q.device):
-        out = torch.empty((w.m, w.n), dtype=dtype, device=w.q.device)
+    dev = w.q.device
+    _check_int4(w, dev)
+    with _guard(stream, dev):
+        out = torch.empty((w.m, w.n), dtype=dtype, device=dev)
         rc = _lib.load().externd_int4_dequantize(w.q.data_ptr(), w.scale.data_ptr(), _ptr(w.offset), w.m, w.n, w.group,
-                                                 out.data_ptr(), _DTYPE[dtype], w.n, _raw_stream())
+                                                 out.data_ptr(), _DTYPE[dtype], w.n, _handle_of(dev.index))
     _check(rc, "externd_int4_dequantize")
     return out
 
@@ -699,17 +709,19 @@ def int4_gated(wg: Int4Weights, wu: Int4Weights, X: torch.Tensor, act: str = "si
 def _int4_products(ws, X, act: int, out, stream) -> torch.Tensor:
     if not isinstance(X, torch.Tensor) or not X.is_cuda:
         raise ValueError("X must be a CUDA tensor")
+    dev = X.device
+    mats = []
     for w in ws:
-        _check_int4(w, X.device)
-    w = ws[0]
+        _check_int4(w, dev)
+        mats += (w.q.data_ptr(), w.scale.data_ptr(), None if w.offset is None else w.offset.data_ptr())
     squeeze = X.dim() == 1
-    with _guard(stream, X.device):
+    with _guard(stream, dev):
         X2 = _rows_in(X.unsqueeze(0) if squeeze else X, w.n, "X")
         if out is not None and squeeze:
             out = out.unsqueeze(0)
-        Y = _result(out, X2.shape[0], w.m, X2)
-        mats = [p for v in ws for p in (v.q.data_ptr(), v.scale.data_ptr(), _ptr(v.offset))]
-        tail = (X2.data_ptr(), _DTYPE[X2.dtype], _ld(X2), X2.shape[0], Y.data_ptr(), _ld(Y), _raw_stream())
+        batch = X2.shape[0]
+        Y = _result(out, batch, w.m, X2)
+        tail = (X2.data_ptr(), _DTYPE[X2.dtype], _ld(X2), batch, Y.data_ptr(), _ld(Y), _handle_of(dev.index))
         if len(ws) == 1:
             rc = _lib.load().externd_int4_matvec(*mats, w.m, w.n, w.group, *tail)
         else:
@@ -778,7 +790,7 @@ def _align_bytes(*tensors) -> int:
     total = 0
     for t in tensors:
         rows, cols = t.shape
-        if rows > 0 and (t.data_ptr() % 16 or (rows > 1 and t.stride(0) % 8)):
+        if t.data_ptr() % 16 or (rows > 1 and t.stride(0) % 8):
             total += (rows * ((cols + 7) // 8 * 8) * 2 + 255) // 256 * 256
     return total
 
@@ -800,13 +812,13 @@ def _gated(X, Wg, Wu, act, save, out, async_status, stream):
         H = _result(None if out is None else out.view(-1, m), t, m, X2)
         G = U = None
         if save is not None:
-            G, U = torch.empty(shape, dtype=save, device=dev), torch.empty(shape, dtype=save, device=dev)
+            G, U = X2.new_empty(shape, dtype=save), X2.new_empty(shape, dtype=save)
         nbytes = _align_bytes(X2, Wg, Wu)
         work = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
         rc = _lib.load().externd_gated(X2.data_ptr(), _ld(X2), Wg.data_ptr(), _ld(Wg), Wu.data_ptr(), _ld(Wu), _DTYPE[X2.dtype],
                                        m, n, t, code, H.data_ptr(), _ld(H), G.data_ptr() if t and save else None,
                                        U.data_ptr() if t and save else None, _DTYPE[save or X2.dtype], m, _ptr(work), nbytes,
-                                       _ptr(async_status), _raw_stream())
+                                       _ptr(async_status), _handle_of(dev.index))
     _check(rc, "externd_gated")
     return (H if X.dim() == 2 else H.view(shape)), G, U
 
@@ -853,9 +865,9 @@ def gated_backward(dH: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torc
         if _ld(G2) != _ld(U2):
             G2, U2 = G2.contiguous(), U2.contiguous()
         t = X2.shape[0]
-        dX = torch.empty((t, n), dtype=X2.dtype, device=dev) if need[0] else None
-        dWg = torch.empty((m, n), dtype=X2.dtype, device=dev) if need[1] else None
-        dWu = torch.empty((m, n), dtype=X2.dtype, device=dev) if need[2] else None
+        dX = X2.new_empty((t, n)) if need[0] else None
+        dWg = X2.new_empty((m, n)) if need[1] else None
+        dWu = X2.new_empty((m, n)) if need[2] else None
         nbytes = 0
         if t and (need[0] or need[1] or need[2]):
             used = ([Wg, Wu] if need[0] else []) + ([X2] if need[1] or need[2] else [])
@@ -864,6 +876,6 @@ def gated_backward(dH: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torc
         rc = _lib.load().externd_gated_backward(
             dH2.data_ptr(), _ld(dH2), X2.data_ptr(), _ld(X2), Wg.data_ptr(), _ld(Wg), Wu.data_ptr(), _ld(Wu), G2.data_ptr(),
             U2.data_ptr(), _DTYPE[G2.dtype], _ld(G2), _DTYPE[X2.dtype], m, n, t, code, _ptr(dX), n, _ptr(dWg), _ptr(dWu), n,
-            _ptr(work), nbytes, _ptr(async_status), _raw_stream())
+            _ptr(work), nbytes, _ptr(async_status), _handle_of(dev.index))
     _check(rc, "externd_gated_backward")
     return (dX if dX is None or X.dim() == 2 else dX.view(X.shape)), dWg, dWu

@@ -14,7 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 # externd_nt256.cu and externd_nt1024.cu compile the ALS machinery of externd.cu at other block sizes
 SOURCES = [os.path.join(HERE, "csrc", name) for name in ("externd.cu", "externd_nt256.cu", "externd_nt1024.cu", "infer.cu", "int4.cu", "gated.cu")]
-DEPS = SOURCES + [os.path.join(HERE, "csrc", name) for name in ("externd_kernels.cuh", "als_cluster.cuh", "block_als.cuh", "llm_ops.cuh")] \
+DEPS = SOURCES + [os.path.join(HERE, "csrc", name) for name in ("externd_kernels.cuh", "als_cluster.cuh", "block_als.cuh", "llm_ops.cuh", "sm100.cuh")] \
     + [os.path.join(ROOT, "include", "externd.h")]
 OUT = os.path.join(HERE, "libexternd.so")
 

@@ -13,7 +13,7 @@
 
 #include <type_traits>
 
-#include "llm_ops.cuh"
+#include "sm100.cuh"
 
 #ifndef GATED_CG
 #define GATED_CG 1
@@ -22,113 +22,6 @@
 namespace externd_ffn {
 
 using namespace externd_llm;
-
-// ---------------------------------------------------------------------------------------------------
-// PTX
-// ---------------------------------------------------------------------------------------------------
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ uint64_t timer_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-// arrive on a barrier of any CTA of the cluster (shared::cluster address)
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-    return ok != 0;
-}
-
-constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;   // per wait, as for the factorizations
-
-// Wait for a phase.  Gives up after WAIT_LIMIT_NS, or when another warp of the CTA gave up: the CTA then
-// leaves its loops and the launch reports EXTERND_ETIMEOUT.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* quit) {
-    if (mbar_try(bar, parity)) return true;
-    uint64_t t0 = 0;
-    for (;;) {
-        #pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try(bar, parity)) return true;
-        if (*quit) return false;
-        const uint64_t t = timer_ns();
-        if (t0 == 0) t0 = t;
-        else if (t - t0 > WAIT_LIMIT_NS) { *quit = 1; return false; }
-    }
-}
-
-// 2-D tiled load, box at (x, y); completes on `bar` (shared::cluster address)
-template <int CG>
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-    if constexpr (CG == 1)
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                     ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-    else
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
-                     ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-}
-
-template <int CG>
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-    if constexpr (CG == 1)
-        asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-                     ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
-    else
-        asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
-                     ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
-}
-
-// arrive on `bar` (in both CTAs of a pair) when the MMAs issued so far have finished
-template <int CG>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    if constexpr (CG == 1)
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-    else
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                     ::"r"(bar), "h"((uint16_t)3) : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
-          "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
-          "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
-          "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------------------------------
 // the tile kernel
@@ -161,11 +54,6 @@ struct GemmArgs {
     int save32;              // FWD: G and U in fp32 (otherwise in the operands' type)
     int* status;             // may be null
 };
-
-// shared-memory operand descriptor, 128-byte swizzle: start, leading and stride byte offsets
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | 1ull << 46 | 2ull << 61;
-}
 
 // 32 columns of a warp's 32 rows (a row per lane, R registers) to global memory through the warp's staging
 // buffer, so that neighbouring lanes write neighbouring 16 bytes
@@ -252,18 +140,12 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        if constexpr (CG == 1) {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)) : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-        } else {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)) : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-        }
+        tmem_alloc<CG>(smem_u32(&tmem_slot), 512);
     }
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    fence_before();
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    fence_after();
     const uint32_t tmem = *(volatile uint32_t*)&tmem_slot;
 
     const int kb_half = (g.depth + BK - 1) / BK;
@@ -322,8 +204,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         // ---- products
         constexpr bool A_MN = MODE == DW, B_MN = MODE != FWD;
         constexpr uint32_t fmt = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
-        constexpr uint32_t idesc = 1u << 4 | fmt << 7 | fmt << 10 | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) |
-                                   (uint32_t)(ACC >> 3) << 17 | (uint32_t)(C::BM >> 4) << 24;
+        constexpr uint32_t idesc = f16_idesc(fmt, A_MN, B_MN, C::BM, ACC);
         // along K: 8-row groups 1024 bytes apart, 32 bytes per 16 elements of depth.  Along M or N: 64-element
         // boxes BK * 128 bytes apart, 8-deep groups 1024 bytes apart, 2048 bytes per 16 elements of depth.
         constexpr uint32_t box = 64 * BK * 2;
@@ -332,11 +213,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         for (int t = first; t < tiles && ok; t += step, ++n) {
             const uint32_t acc = tmem + (n & 1) * ACC;
             if (!mbar_wait(tempty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, quit)) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            fence_after();
             for (int kb = 0; kb < kbs; ++kb, ++it) {
                 const int s = it % C::STAGES;
                 if (!mbar_wait(full0 + 8 * s, (it / C::STAGES) & 1, quit)) { ok = false; break; }
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                fence_after();
                 const uint32_t sa = base + s * C::STAGE, sb = sa + 128 * BK * 2;
                 const uint64_t da = A_MN ? smem_desc(sa, box, 1024) : smem_desc(sa, 16, 1024);
                 const uint64_t db = B_MN ? smem_desc(sb, box, 1024) : smem_desc(sb, 16, 1024);
@@ -364,7 +245,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
             int tr, tc;
             tile_at(t, g.tiles_r, g.tiles_c, tr, tc);
             if (!mbar_wait(tfull0 + 8 * (n & 1), (n >> 1) & 1, quit)) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            fence_after();
             const uint32_t acc = tmem + (n & 1) * ACC + ((uint32_t)(32 * w) << 16);
             T* out = (T*)g.out0;
             int64_t ld = g.ld0;
@@ -409,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
                     store32<T>(h, stg, stg_ptr, out, ld, row0, g.rows, col0, g.cols, lane);
                 }
             }
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            fence_before();
             __syncwarp();
             if (lane == 0) {
                 uint32_t bar = tempty0 + 8 * (n & 1);
@@ -422,9 +303,8 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
     if (threadIdx.x == 0 && quit_flag && g.status) atomicExch(g.status, EXTERND_ETIMEOUT);
     if constexpr (CG == 2) cluster_sync();
     if (warp == 1) {
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if constexpr (CG == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
-        else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        fence_after();
+        tmem_free<CG>(tmem, 512);
     }
 }
 
@@ -501,21 +381,22 @@ __global__ void __launch_bounds__(WARPS * 32) dense_stream_kernel(const T* __res
     const int r = lane >> 2, c = lane & 3;
     const int64_t row0 = (int64_t)blockIdx.x * 16;
     const int64_t ra = min(row0 + r, m - 1), rb = min(row0 + r + 8, m - 1);
-    const T* rows[4] = {wg + ra * ldg, wg + rb * ldg, wu + ra * ldu, wu + rb * ldu};
-    const T* xr[NT];
+    using S16 = unsigned short;
+    const S16* rows[4] = {(const S16*)(wg + ra * ldg), (const S16*)(wg + rb * ldg), (const S16*)(wu + ra * ldu), (const S16*)(wu + rb * ldu)};
+    const S16* xr[NT];
     #pragma unroll
-    for (int t = 0; t < NT; ++t) xr[t] = 8 * t + r < tokens ? x + (8 * t + r) * ldx : nullptr;
+    for (int t = 0; t < NT; ++t) xr[t] = 8 * t + r < tokens ? (const S16*)(x + (8 * t + r) * ldx) : nullptr;
     float acc[2][NT][4] = {};
     const int64_t blocks = (n + 63) / 64;
     for (int64_t blk = warp; blk < blocks; blk += WARPS) {
-        XFrag<T, 1> w[2][4], xf[2][NT];
+        uint4 w[2][4], xf[2][NT];
         #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int64_t k = blk * 64 + 32 * i + 8 * c;
             #pragma unroll
-            for (int j = 0; j < 4; ++j) load_x<T, T, 1, true>(rows[j], k, n, w[i][j]);
+            for (int j = 0; j < 4; ++j) w[i][j] = load8(rows[j], k, n, true);
             #pragma unroll
-            for (int t = 0; t < NT; ++t) load_x<T, T, 1, true>(xr[t], k, n, xf[i][t]);
+            for (int t = 0; t < NT; ++t) xf[i][t] = xr[t] ? load8(xr[t], k, n, true) : make_uint4(0, 0, 0, 0);
         }
         #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -523,11 +404,9 @@ __global__ void __launch_bounds__(WARPS * 32) dense_stream_kernel(const T* __res
             for (int j = 0; j < 2; ++j)
                 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const uint32_t(&a)[4] = w[i][2 * j].v[0];
-                    const uint32_t(&b)[4] = w[i][2 * j + 1].v[0];
-                    const uint32_t(&v)[4] = xf[i][t].v[0];
-                    mma16816<T>(acc[j][t], a[0], b[0], a[1], b[1], v[0], v[1]);
-                    mma16816<T>(acc[j][t], a[2], b[2], a[3], b[3], v[2], v[3]);
+                    const uint4 a = w[i][2 * j], b = w[i][2 * j + 1], v = xf[i][t];
+                    mma16816<T>(acc[j][t], a.x, b.x, a.y, b.y, v.x, v.y);
+                    mma16816<T>(acc[j][t], a.z, b.z, a.w, b.w, v.z, v.w);
                 }
     }
     #pragma unroll

@@ -7,7 +7,9 @@
 // consecutive columns of each of the block's four 32-column spans: the four lanes together cover one span
 // (one group at most) per word, and (word >> 4 p) & 0x000f000f is a pair of neighbouring columns, ready to
 // become two 16-bit floats.
-#include "llm_ops.cuh"
+#include <type_traits>
+
+#include "sm100.cuh"
 
 namespace externd_int4 {
 
@@ -23,121 +25,142 @@ __host__ __device__ __forceinline__ int64_t row_bytes(int64_t n) { return (n + 1
 // fp32; the format's fp64 decisions are taken in fp64 only next to a border (1e-4-wide bands around the
 // rounding borders of codes, 2^-10 of the scales), where the fp32 value cannot decide.
 
-// fp16 of the fp64 value v (rounded to fp32 first), given its fp32 estimate e with relative error below
-// 2^-21: `near` says that e does not decide it
+// says whether the fp32 estimate e (relative error below 2^-20) of a value leaves open to which fp16 it rounds
 __device__ __forceinline__ bool near_half_border(float e) {
     const uint32_t u = __float_as_uint(e) & 0x7fffffffu;
     const uint32_t low = u & 0x1fffu;                       // bits below the fp16 mantissa
-    return u < 0x38800000u + 64u || (low > 0x1000u - 16u && low < 0x1000u + 16u);   // below 2^-14: fp16 subnormals
+    return u < 0x38800000u + 64u || u >= 0x477fe000u || (low > 0x1000u - 16u && low < 0x1000u + 16u);   // subnormal or top fp16s too
 }
 
+template <typename T> constexpr int QBLOCKS = sizeof(T) == 4 ? 2 : 4;     // blocks a warp has in flight
+
 template <typename T, bool AFFINE, bool VEC>
-__global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ A, int64_t m, int64_t n, int64_t lda, int group,
+__global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ A, int64_t m, int64_t n, int64_t lda, int lg,
                                                        uint32_t* __restrict__ q, __half* __restrict__ scale,
                                                        __half* __restrict__ offset, int* __restrict__ status) {
+    constexpr int UB = QBLOCKS<T>;
     const int lane = threadIdx.x & 31;
-    const int64_t blocks = (n + 127) / 128;
-    const int64_t items = m * blocks;
-    const int64_t warps = (int64_t)gridDim.x * (blockDim.x / 32);
-    for (int64_t item = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32; item < items; item += warps) {
-        // neighbouring warps take neighbouring rows of one block: their scales share a sector
-        const int64_t blk = item / m, row = item - blk * m;
-        const int64_t j0 = blk * 128 + 4 * lane;
-        const T* a = A + row * lda + j0;
-        float w[4];
-        if (VEC && j0 + 4 <= n) {
-            if constexpr (sizeof(T) == 4) {
-                const float4 v = __ldcs(reinterpret_cast<const float4*>(a));
-                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);   // neighbouring warps, neighbouring rows: their scales share a sector
+    if (row >= m) return;
+    const int blocks = (int)((n + 127) / 128);
+    const T* const arow = A + row * lda + 4 * lane;
+    for (int b0 = blockIdx.y * UB; b0 < blocks; b0 += gridDim.y * UB) {
+        float w[UB][4];
+        #pragma unroll
+        for (int u = 0; u < UB; ++u) {
+            const int64_t j0 = (int64_t)(b0 + u) * 128 + 4 * lane;
+            const T* a = arow + (int64_t)(b0 + u) * 128;
+            if (VEC && j0 + 4 <= n) {
+                if constexpr (sizeof(T) == 4) {
+                    const float4 v = __ldcs(reinterpret_cast<const float4*>(a));
+                    w[u][0] = v.x; w[u][1] = v.y; w[u][2] = v.z; w[u][3] = v.w;
+                } else {
+                    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(a));
+                    const float2 lo = unpack2<T>(v.x), hi = unpack2<T>(v.y);
+                    w[u][0] = lo.x; w[u][1] = lo.y; w[u][2] = hi.x; w[u][3] = hi.y;
+                }
             } else {
-                const uint2 v = __ldcs(reinterpret_cast<const uint2*>(a));
-                const float2 lo = unpack2<T>(v.x), hi = unpack2<T>(v.y);
-                w[0] = lo.x; w[1] = lo.y; w[2] = hi.x; w[3] = hi.y;
+                #pragma unroll
+                for (int t = 0; t < 4; ++t) w[u][t] = j0 + t < n ? to_f32(a[t]) : 0.0f;
             }
-        } else {
+        }
+        #pragma unroll
+        for (int u = 0; u < UB; ++u) {
+            const int blk = b0 + u;
+            if (blk >= blocks) break;
+            const int64_t j0 = (int64_t)blk * 128 + 4 * lane;
+            const int left = j0 >= n ? 0 : n - j0 >= 4 ? 4 : (int)(n - j0);     // columns of this lane
+            float mn = INFINITY, mx = -INFINITY;
+            bool finite = true;
             #pragma unroll
-            for (int t = 0; t < 4; ++t) w[t] = j0 + t < n ? to_f32(a[t]) : 0.0f;
-        }
-        float mn = INFINITY, mx = -INFINITY;
-        bool finite = true;
-        #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (j0 + t < n) {
-                finite = finite && fabsf(w[t]) <= FLT_MAX;
-                mn = fminf(mn, w[t]);
-                mx = fmaxf(mx, w[t]);
+            for (int t = 0; t < 4; ++t)
+                if (t < left) {
+                    finite = finite && fabsf(w[u][t]) <= FLT_MAX;
+                    mn = fminf(mn, w[u][t]);
+                    mx = fmaxf(mx, w[u][t]);
+                }
+            for (int o = 1; o < 1 << (lg - 2); o <<= 1) {
+                mn = fminf(mn, __shfl_xor_sync(FULL, mn, o));
+                mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
             }
-        for (int o = 1; o < group / 4; o <<= 1) {
-            mn = fminf(mn, __shfl_xor_sync(FULL, mn, o));
-            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-        }
-        const bool any = j0 / group * group < n;   // the group has columns
-        float s = 0.0f, b = 0.0f;
-        if (any) {
-            float e = AFFINE ? (mx - mn) / 15.0f : fmaxf(-mn, mx) / 7.0f;
-            if (near_half_border(e) || e > 65000.0f)
-                e = (float)(AFFINE ? ((double)mx - (double)mn) / 15.0 : (double)fmaxf(-mn, mx) / 7.0);
-            s = __half2float(__float2half_rn(e));
-            if (AFFINE) {
-                float f = fmaf(8.0f, s, mn);
-                if (near_half_border(f)) f = (float)((double)mn + 8.0 * (double)s);
-                b = __half2float(__float2half_rn(f));
+            const bool any = mn <= mx || !finite;      // the group has columns (with NaN only, mn stays above mx)
+            float s = 0.0f, b = 0.0f;
+            if (any) {
+                const float range = AFFINE ? mx - mn : fmaxf(-mn, mx);
+                float e = range * (AFFINE ? 1.0f / 15.0f : 1.0f / 7.0f);
+                if (near_half_border(e)) e = (float)(AFFINE ? ((double)mx - (double)mn) / 15.0 : (double)range / 7.0);
+                s = __half2float(__float2half_rn(e));
+                if (AFFINE) {
+                    float f = fmaf(8.0f, s, mn);
+                    if (near_half_border(f)) f = (float)((double)mn + 8.0 * (double)s);
+                    b = __half2float(__float2half_rn(f));
+                }
             }
-        }
-        // a group with NaN or Inf reports that, whatever other groups report
-        if (!finite) atomicExch(status, EXTERND_ENONFINITE);
-        else if (fmaxf(-mn, mx) <= FLT_MAX && (isinf(s) || isinf(b))) atomicCAS(status, EXTERND_OK, EXTERND_ELIMIT);
-        const float inv = s > 0.0f ? 1.0f / s : 0.0f;
-        uint32_t code = 0;
-        #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const float d = AFFINE ? w[t] - b : w[t];
-            float c = d * inv;
-            float r = rintf(c);
-            // |c| <= 16 wherever it is not clamped: its error is below 1e-5
-            if (fabsf(fabsf(c - r) - 0.5f) < 1e-4f && fabsf(c) < 16.0f && s > 0.0f)
-                r = (float)rint(((double)w[t] - (double)b) / (double)s);
-            r = fminf(fmaxf(r, -8.0f), 7.0f);
-            const int v = j0 + t < n ? (int)r + 8 : 8;
-            code |= (uint32_t)v << (4 * (4 * (t & 1) + (t >> 1)));
-        }
-        if (lane & 1) code <<= 8;                              // t = 4..7 sit two nibbles above t = 0..3
-        code |= __shfl_xor_sync(FULL, code, 1);
-        if (!(lane & 1)) {
-            const int word = 4 * ((lane % 8) / 2) + lane / 8;   // 4 c + i
-            q[(row * blocks + blk) * 16 + word] = code;
-        }
-        if (any && (4 * lane) % group == 0) {
-            const int64_t at = (j0 / group) * m + row;
-            scale[at] = __float2half_rn(s);
-            if (AFFINE) offset[at] = __float2half_rn(b);
+            // a group with NaN or Inf reports that, whatever other groups report
+            if (!finite) atomicExch(status, EXTERND_ENONFINITE);
+            else if (any && fmaxf(-mn, mx) <= FLT_MAX && (isinf(s) || isinf(b))) atomicCAS(status, EXTERND_OK, EXTERND_ELIMIT);
+            const float inv = s > 0.0f ? __fdividef(1.0f, s) : 0.0f;
+            float c[4], r[4];
+            bool border = false;
+            #pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                c[t] = (AFFINE ? w[u][t] - b : w[u][t]) * inv;
+                r[t] = rintf(c[t]);
+                // |c| <= 16 wherever it is not clamped: its error is below 1e-5
+                border = border || (fabsf(fabsf(c[t] - r[t]) - 0.5f) < 1e-4f && fabsf(c[t]) < 16.0f);
+            }
+            if (border && s > 0.0f) {
+                #pragma unroll 1
+                for (int t = 0; t < 4; ++t) {
+                    const float v = t == 0 ? w[u][0] : t == 1 ? w[u][1] : t == 2 ? w[u][2] : w[u][3];
+                    const float d = (float)rint(((double)v - (double)b) / (double)s);
+                    if (t == 0) r[0] = d; else if (t == 1) r[1] = d; else if (t == 2) r[2] = d; else r[3] = d;
+                }
+            }
+            uint32_t code = 0;
+            #pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int v = t < left ? (int)fminf(fmaxf(r[t], -8.0f), 7.0f) + 8 : 8;
+                code |= (uint32_t)v << (4 * (4 * (t & 1) + (t >> 1)));
+            }
+            if (lane & 1) code <<= 8;                              // t = 4..7 sit two nibbles above t = 0..3
+            code |= __shfl_xor_sync(FULL, code, 1);
+            if (!(lane & 1)) {
+                const int word = 4 * ((lane % 8) / 2) + lane / 8;   // 4 c + i
+                q[(row * blocks + blk) * 16 + word] = code;
+            }
+            if (left > 0 && ((4 * lane) & ((1 << lg) - 1)) == 0) {
+                const int64_t at = (j0 >> lg) * m + row;
+                scale[at] = __float2half_rn(s);
+                if (AFFINE) offset[at] = __float2half_rn(b);
+            }
         }
     }
 }
 
 // ---------------------------------------------------------------------------------------------------
-// dequantise: lane L of a half-warp holds the 8 columns 8 L .. 8 L + 7 of a block
+// dequantise: a warp per row and pair of blocks, 8 columns a lane
 // ---------------------------------------------------------------------------------------------------
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint32_t* __restrict__ q, const __half* __restrict__ scale,
-                                                         const __half* __restrict__ offset, int64_t m, int64_t n, int group,
+                                                         const __half* __restrict__ offset, int64_t m, int64_t n, int lg,
                                                          T* __restrict__ out, int64_t ldo) {
-    const int64_t blocks = (n + 127) / 128;
-    const int64_t items = m * blocks;
-    const int l = threadIdx.x & 15;
-    const int64_t halves = (int64_t)gridDim.x * (blockDim.x / 16);
-    for (int64_t item = (int64_t)blockIdx.x * (blockDim.x / 16) + threadIdx.x / 16; item < items; item += halves) {
-        const int64_t row = item / blocks, blk = item - row * blocks;
-        const int64_t j0 = blk * 128 + 8 * l;
+    const int lane = threadIdx.x & 31, l = lane & 15;
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= m) return;
+    const int blocks = (int)((n + 127) / 128);
+    const uint32_t* const qrow = q + row * blocks * 16 + 4 * (l & 3) + (l >> 2);
+    #pragma unroll 2
+    for (int blk = 2 * blockIdx.y + (lane >> 4); blk < blocks; blk += 2 * gridDim.y) {
+        const int64_t j0 = (int64_t)blk * 128 + 8 * l;
         if (j0 >= n) continue;
-        const uint32_t w = q[item * 16 + 4 * (l & 3) + (l >> 2)];
-        const int64_t at = (j0 / group) * m + row;
-        const float s = __half2float(scale[at]), b = offset ? __half2float(offset[at]) : 0.0f;
+        const uint32_t w = __ldg(qrow + (int64_t)blk * 16);
+        const int64_t at = (j0 >> lg) * m + row;
+        const float s = __half2float(__ldg(scale + at)), b = offset ? __half2float(__ldg(offset + at)) : 0.0f;
         float v[8];
         #pragma unroll
-        for (int t = 0; t < 8; ++t)
-            v[t] = fmaf(s, (float)((int)((w >> (4 * (4 * (t & 1) + (t >> 1)))) & 15u) - 8), b);
+        for (int t = 0; t < 8; ++t) v[t] = fmaf(s, (float)((int)((w >> (4 * (4 * (t & 1) + (t >> 1)))) & 15u) - 8), b);
         T* o = out + row * ldo + j0;
         if (VEC && j0 + 8 <= n) {
             if constexpr (sizeof(T) == 4) {
@@ -156,16 +179,12 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint32_t* __restr
 }
 
 // ---------------------------------------------------------------------------------------------------
-// products: a CTA of WARPS warps takes 16 rows of W (of both matrices when gated) and 8 NT vectors; its warps
-// split the columns and add their partial sums in shared memory in a fixed order
+// products
 // ---------------------------------------------------------------------------------------------------
 //
-// Bound by the weights' bytes for few vectors.  The tensor cores' warp-level product does the arithmetic:
-// codes become exact 16-bit floats q - 8 two at a time, eight vectors ride in one instruction, and each
-// group's fp32 sum is scaled once.  (The tile-level product of the tensor cores reads its operands from
-// shared memory: the weights would cross it twice more, for arithmetic that does not bound here.)
-// fp32 vectors enter as three bf16 terms x = hi + mid + lo cut off from the top (8 + 8 + 8 bits: no loss),
-// three products into one sum.  The offsets' part b sum(x) takes sum(x) from a product with ones.
+// Codes become exact 16-bit floats q - 8 two at a time, the tensor cores sum each group's products in fp32, and
+// the group's sum is scaled once.  fp32 vectors enter as three bf16 terms x = hi + mid + lo cut off from the
+// top (8 + 8 + 8 bits: no loss), three products into one sum.
 
 // a pair of codes -> a pair of floats q - 8; p = 0..3 selects the pair of the word
 template <typename T> __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&a)[4]);
@@ -202,143 +221,547 @@ struct Mat4 {                       // one 4-bit matrix
     const __half* offset;           // nullptr: symmetric
 };
 
-template <typename T> __device__ constexpr uint32_t one2();
-template <> __device__ constexpr uint32_t one2<__half>() { return 0x3c003c00u; }
-template <> __device__ constexpr uint32_t one2<__nv_bfloat16>() { return 0x3f803f80u; }
+__device__ __forceinline__ uint32_t word_of(const uint4& q, int i) { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; }
 
-// X element type, T product type (bf16 for fp32 X), NM matrices (1, or 2: gated)
-template <typename X, typename T, int NT, int NM, int WARPS, bool VEC>
-__global__ void __launch_bounds__(WARPS * 32) stream4_kernel(Mat4 w0, Mat4 w1, int64_t m, int64_t n, int group, int act,
-                                                            const X* __restrict__ x, int64_t ldx, int64_t batch,
-                                                            X* __restrict__ y, int64_t ldy) {
-    constexpr int PLANES = sizeof(X) == 4 ? 3 : 1;
-    constexpr int COLS = 8 * NT;
-    __shared__ float part[NM][WARPS][16][COLS + 1];
+// d += (16 rows' codes of one word span) x (8 vectors' entries), all planes, least significant first
+template <typename T, int PLANES>
+__device__ __forceinline__ void span_mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[4], const uint32_t (&x)[PLANES][4]) {
+    #pragma unroll
+    for (int p = PLANES - 1; p >= 0; --p) {
+        mma16816<T>(d, a[0], b[0], a[1], b[1], x[p][0], x[p][1]);
+        mma16816<T>(d, a[2], b[2], a[3], b[3], x[p][2], x[p][3]);
+    }
+}
+
+// ---- up to 8 vectors ----------------------------------------------------------------------------------
+//
+// A CTA takes 16 rows (of both matrices when gated); its warps take the 128-column blocks in turn and add
+// their sums in shared memory in a fixed order.  The warp-level products carry the arithmetic: a warp's 16 rows
+// by eight vectors in one instruction, straight from registers.  (The tile-level products read their operands
+// from shared memory: the codes would cross it as 16-bit floats, and of a tile's columns 16 at least.)
+// Every lane keeps the codes of its next DEPTH blocks in flight to shared memory (its own 16 bytes of two rows:
+// no barrier, no registers), and fetches the vectors' entries and the scales of the next block while it works
+// on one.  Bound by the weights' bytes; next by instructions, 72 of them a block and matrix to unpack codes.
+// The offsets' part b sum(x) takes sum(x) from the lanes that hold x (products with ones would occupy the
+// tensor cores as long as the codes do, and those are as busy as memory).
+// X element type, T product type (bf16 for fp32 X), NM matrices, WORDS = group / 32.
+constexpr int VEC_WARPS = 8;
+template <int NM> __host__ __device__ constexpr int vec_depth() { return NM == 1 ? 6 : 4; }
+template <int NM> __host__ __device__ constexpr int vec_smem() { return VEC_WARPS * vec_depth<NM>() * NM * 1024; }
+
+__device__ __forceinline__ float sum8(const uint4& r, __half*) {
+    const float2 a = unpack2<__half>(r.x), b = unpack2<__half>(r.y), c = unpack2<__half>(r.z), d = unpack2<__half>(r.w);
+    return ((a.x + a.y) + (b.x + b.y)) + ((c.x + c.y) + (d.x + d.y));
+}
+__device__ __forceinline__ float sum8(const uint4& r, __nv_bfloat16*) {
+    const float2 a = unpack2<__nv_bfloat16>(r.x), b = unpack2<__nv_bfloat16>(r.y), c = unpack2<__nv_bfloat16>(r.z),
+                 d = unpack2<__nv_bfloat16>(r.w);
+    return ((a.x + a.y) + (b.x + b.y)) + ((c.x + c.y) + (d.x + d.y));
+}
+__device__ __forceinline__ float sum8(const F8& r, __nv_bfloat16*) {
+    return ((r.a.x + r.a.y) + (r.a.z + r.a.w)) + ((r.b.x + r.b.y) + (r.b.z + r.b.w));
+}
+
+template <typename X, typename T, int NM, int WORDS, bool AFFINE>
+__global__ void __launch_bounds__(VEC_WARPS * 32) vec4_kernel(Mat4 w0, Mat4 w1, int64_t m, int64_t n, int act, const X* __restrict__ x,
+                                                             int64_t ldx, int vec, int batch, X* __restrict__ y, int64_t ldy) {
+    using Raw = typename Raw8<X>::type;
+    constexpr int PLANES = Raw8<X>::PLANES;
+    using XE = typename std::conditional<PLANES == 3, float, unsigned short>::type;
+    constexpr int GROUPS = 4 / WORDS;                   // groups of a block
+    constexpr int DEPTH = vec_depth<NM>();
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ float part[NM][VEC_WARPS][16][9];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, c = lane & 3;
     const int64_t row0 = (int64_t)blockIdx.x * 16;
-    const int64_t col0 = (int64_t)blockIdx.y * COLS;
-    const int64_t blocks = (n + 127) / 128;
+    const int blocks = (int)((n + 127) / 128), groups = (int)((n + 32 * WORDS - 1) / (32 * WORDS));
+    const int whole = vec ? (int)(n / 128) : 0;         // blocks whose entries load 16 bytes at a time, unchecked
     // rows past the last one repeat it (their sums are not stored)
     const int64_t ra = min(row0 + r, m - 1), rb = min(row0 + r + 8, m - 1);
+    const int64_t down = rb - ra;
     const Mat4 w[2] = {w0, w1};
-    const bool affine = w0.offset != nullptr || (NM == 2 && w1.offset != nullptr);
-    const int words = group / 32;                       // words of a block that share a group
 
-    const X* xr[NT];
+    // this lane's places: codes of its two rows, scales, entries of its vector
+    const uint8_t *qa[NM], *qb[NM];
+    const __half *ps[NM], *po[NM];
     #pragma unroll
-    for (int t = 0; t < NT; ++t) xr[t] = col0 + 8 * t + r < batch ? x + (col0 + 8 * t + r) * ldx : nullptr;
+    for (int j = 0; j < NM; ++j) {
+        qa[j] = w[j].q + (ra * blocks + warp) * 64 + 16 * c;
+        qb[j] = w[j].q + (rb * blocks + warp) * 64 + 16 * c;
+        ps[j] = w[j].scale + (int64_t)warp * GROUPS * m + ra;
+        po[j] = AFFINE && w[j].offset ? w[j].offset + (int64_t)warp * GROUPS * m + ra : nullptr;
+    }
+    const XE* const xr = r < batch ? reinterpret_cast<const XE*>(x + r * ldx) : nullptr;
 
-    float out[NM][NT][4] = {};
-    for (int64_t blk = warp; blk < blocks; blk += WARPS) {
-        uint4 qa[NM], qb[NM];
+    const uint32_t mine = smem_u32(ring) + (warp * DEPTH * NM * 2 * 32 + lane) * 16;  // slot, matrix, row half: 512 bytes apart
+    const auto issue = [&](bool on, uint32_t slot) {
         #pragma unroll
         for (int j = 0; j < NM; ++j) {
-            qa[j] = __ldcs(reinterpret_cast<const uint4*>(w[j].q + (ra * blocks + blk) * 64 + 16 * c));
-            qb[j] = __ldcs(reinterpret_cast<const uint4*>(w[j].q + (rb * blocks + blk) * 64 + 16 * c));
+            if (on) {
+                const uint32_t dst = mine + slot * (NM * 1024) + j * 1024;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(qa[j]) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512), "l"(qb[j]) : "memory");
+            }
+            qa[j] += VEC_WARPS * 64;
+            qb[j] += VEC_WARPS * 64;
         }
-        float acc[NM][NT][4] = {}, sum[NT][4] = {};
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t k = blk * 128 + 32 * i + 8 * c;
-            XFrag<T, PLANES> xf[NT];
-            #pragma unroll
-            for (int t = 0; t < NT; ++t) load_x<X, T, PLANES, VEC>(xr[t], k, n, xf[t]);
-            #pragma unroll
-            for (int j = 0; j < NM; ++j) {
-                const uint32_t wa = i == 0 ? qa[j].x : i == 1 ? qa[j].y : i == 2 ? qa[j].z : qa[j].w;
-                const uint32_t wb = i == 0 ? qb[j].x : i == 1 ? qb[j].y : i == 2 ? qb[j].z : qb[j].w;
-                uint32_t a[4], b[4];
-                codes8<T>(wa, a);
-                codes8<T>(wb, b);
-                #pragma unroll
-                for (int t = 0; t < NT; ++t)
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    struct Side {                                        // what a block needs beside its codes
+        Raw x[4];
+        __half s[NM][GROUPS][2], o[AFFINE ? NM : 1][GROUPS][2];
+    };
+    const auto fetch = [&](Side& d, int blk) {
+        if (blk < blocks) {
+            if (blk < whole) {
+                if (xr) {
+                    const XE* const p = xr + blk * 128 + 8 * c;
                     #pragma unroll
-                    for (int p = PLANES - 1; p >= 0; --p) {
-                        mma16816<T>(acc[j][t], a[0], b[0], a[1], b[1], xf[t].v[p][0], xf[t].v[p][1]);
-                        mma16816<T>(acc[j][t], a[2], b[2], a[3], b[3], xf[t].v[p][2], xf[t].v[p][3]);
-                    }
+                    for (int i = 0; i < 4; ++i) d.x[i] = *reinterpret_cast<const Raw*>(p + 32 * i);
+                }
+            } else {
+                #pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    const Raw v = xr ? load8(xr, (int64_t)blk * 128 + 32 * i + 8 * c, n, vec) : Raw{};
+                    if (i == 0) d.x[0] = v; else if (i == 1) d.x[1] = v; else if (i == 2) d.x[2] = v; else d.x[3] = v;
+                }
             }
-            if (affine) {
-                #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    #pragma unroll
-                    for (int p = PLANES - 1; p >= 0; --p) {
-                        mma16816<T>(sum[t], one2<T>(), one2<T>(), one2<T>(), one2<T>(), xf[t].v[p][0], xf[t].v[p][1]);
-                        mma16816<T>(sum[t], one2<T>(), one2<T>(), one2<T>(), one2<T>(), xf[t].v[p][2], xf[t].v[p][3]);
-                    }
-            }
-            if ((i + 1) % words == 0 && blk * 128 + 32 * (i + 1 - words) < n) {   // the group ends here
-                const int64_t at = (blk * 128 + 32 * i) / group * m;
+            #pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                const bool in = GROUPS == 1 || blk * GROUPS + g < groups;   // past the last group: its entries are 0
                 #pragma unroll
                 for (int j = 0; j < NM; ++j) {
-                    const float sa = __half2float(__ldg(w[j].scale + at + ra)), sb = __half2float(__ldg(w[j].scale + at + rb));
-                    float ba = 0.0f, bb = 0.0f;
-                    if (w[j].offset) {
-                        ba = __half2float(__ldg(w[j].offset + at + ra));
-                        bb = __half2float(__ldg(w[j].offset + at + rb));
-                    }
-                    #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        out[j][t][0] = fmaf(sa, acc[j][t][0], out[j][t][0]);
-                        out[j][t][1] = fmaf(sa, acc[j][t][1], out[j][t][1]);
-                        out[j][t][2] = fmaf(sb, acc[j][t][2], out[j][t][2]);
-                        out[j][t][3] = fmaf(sb, acc[j][t][3], out[j][t][3]);
-                        if (w[j].offset) {
-                            out[j][t][0] = fmaf(ba, sum[t][0], out[j][t][0]);
-                            out[j][t][1] = fmaf(ba, sum[t][1], out[j][t][1]);
-                            out[j][t][2] = fmaf(bb, sum[t][2], out[j][t][2]);
-                            out[j][t][3] = fmaf(bb, sum[t][3], out[j][t][3]);
-                        }
-                        #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[j][t][e] = 0.0f;
+                    d.s[j][g][0] = in ? __ldg(ps[j] + g * m) : __ushort_as_half(0);
+                    d.s[j][g][1] = in ? __ldg(ps[j] + g * m + down) : __ushort_as_half(0);
+                    if (AFFINE) {
+                        d.o[j][g][0] = in && po[j] ? __ldg(po[j] + g * m) : __ushort_as_half(0);
+                        d.o[j][g][1] = in && po[j] ? __ldg(po[j] + g * m + down) : __ushort_as_half(0);
                     }
                 }
-                #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    #pragma unroll
-                    for (int e = 0; e < 4; ++e) sum[t][e] = 0.0f;
             }
         }
+        #pragma unroll
+        for (int j = 0; j < NM; ++j) {
+            ps[j] += VEC_WARPS * GROUPS * m;
+            if (AFFINE && po[j]) po[j] += VEC_WARPS * GROUPS * m;
+        }
+    };
+
+    #pragma unroll
+    for (int d = 0; d < DEPTH; ++d) issue(warp + d * VEC_WARPS < blocks, d);
+    Side next;
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) next.x[i] = Raw{};
+    fetch(next, warp);
+    float out[NM][4] = {};
+    uint32_t slot = 0;
+    #pragma unroll 1
+    for (int blk = warp; blk < blocks; blk += VEC_WARPS) {
+        const Side d = next;
+        fetch(next, blk + VEC_WARPS);
+        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+        uint4 a4[NM], b4[NM];
+        #pragma unroll
+        for (int j = 0; j < NM; ++j) {
+            const uint32_t src = mine + slot * (NM * 1024) + j * 1024;
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(a4[j].x), "=r"(a4[j].y), "=r"(a4[j].z), "=r"(a4[j].w) : "r"(src));
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(b4[j].x), "=r"(b4[j].y), "=r"(b4[j].z), "=r"(b4[j].w) : "r"(src + 512));
+        }
+        float acc[NM][4] = {}, sum = 0.0f;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t xv[PLANES][4];
+            planes8(d.x[i], xv);
+            #pragma unroll
+            for (int j = 0; j < NM; ++j) {
+                uint32_t a[4], b[4];
+                codes8<T>(word_of(a4[j], i), a);
+                codes8<T>(word_of(b4[j], i), b);
+                span_mma<T, PLANES>(acc[j], a, b, xv);
+            }
+            if (AFFINE) sum += sum8(d.x[i], (T*)nullptr);
+            if ((i + 1) % WORDS == 0) {                  // the group ends here
+                const int g = i / WORDS;
+                float s0 = 0.0f, s1 = 0.0f;              // the group's sums of this lane's two output vectors, 2 c and 2 c + 1
+                if (AFFINE) {
+                    sum += __shfl_xor_sync(FULL, sum, 1);
+                    sum += __shfl_xor_sync(FULL, sum, 2);
+                    s0 = __shfl_sync(FULL, sum, 8 * c);
+                    s1 = __shfl_sync(FULL, sum, 8 * c + 4);
+                    sum = 0.0f;
+                }
+                #pragma unroll
+                for (int j = 0; j < NM; ++j) {
+                    const float sa = __half2float(d.s[j][g][0]), sb = __half2float(d.s[j][g][1]);
+                    out[j][0] = fmaf(sa, acc[j][0], out[j][0]);
+                    out[j][1] = fmaf(sa, acc[j][1], out[j][1]);
+                    out[j][2] = fmaf(sb, acc[j][2], out[j][2]);
+                    out[j][3] = fmaf(sb, acc[j][3], out[j][3]);
+                    if (AFFINE) {
+                        const float oa = __half2float(d.o[j][g][0]), ob = __half2float(d.o[j][g][1]);
+                        out[j][0] = fmaf(oa, s0, out[j][0]);
+                        out[j][1] = fmaf(oa, s1, out[j][1]);
+                        out[j][2] = fmaf(ob, s0, out[j][2]);
+                        out[j][3] = fmaf(ob, s1, out[j][3]);
+                    }
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+                }
+            }
+        }
+        issue(blk + DEPTH * VEC_WARPS < blocks, slot);   // the slot's codes have been used
+        slot = slot + 1 == DEPTH ? 0 : slot + 1;
     }
     #pragma unroll
-    for (int j = 0; j < NM; ++j)
-        #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            part[j][warp][r][8 * t + 2 * c] = out[j][t][0];
-            part[j][warp][r][8 * t + 2 * c + 1] = out[j][t][1];
-            part[j][warp][r + 8][8 * t + 2 * c] = out[j][t][2];
-            part[j][warp][r + 8][8 * t + 2 * c + 1] = out[j][t][3];
-        }
+    for (int j = 0; j < NM; ++j) {
+        part[j][warp][r][2 * c] = out[j][0];
+        part[j][warp][r][2 * c + 1] = out[j][1];
+        part[j][warp][r + 8][2 * c] = out[j][2];
+        part[j][warp][r + 8][2 * c + 1] = out[j][3];
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * COLS; e += WARPS * 32) {
-        const int rr = e & 15, cc = e >> 4;
-        if (row0 + rr >= m || col0 + cc >= batch) continue;
+    const int e = threadIdx.x, rr = e & 15, cc = e >> 4;
+    if (e < 128 && row0 + rr < m && cc < batch) {
         float v[NM] = {};
         #pragma unroll
         for (int j = 0; j < NM; ++j)
             #pragma unroll
-            for (int p = 0; p < WARPS; ++p) v[j] += part[j][p][rr][cc];
-        const float res = NM == 1 ? v[0] : act_rt<sizeof(X) == 4>(act, v[0]) * v[NM - 1];
-        y[(col0 + cc) * ldy + row0 + rr] = from_f32<X>(res);
+            for (int p = 0; p < VEC_WARPS; ++p) v[j] += part[j][p][rr][cc];
+        const float res = NM == 1 ? v[0] : act_rt<PLANES == 3>(act, v[0]) * v[NM - 1];
+        y[cc * ldy + row0 + rr] = from_f32<X>(res);
     }
 }
 
-template <typename X, typename T, int NT, int NM, int WARPS>
-cudaError_t launch_stream4(const Mat4& w0, const Mat4& w1, int64_t m, int64_t n, int group, int act, const void* x, int64_t ldx,
-                           int64_t batch, void* y, int64_t ldy, cudaStream_t s) {
-    const dim3 grid((unsigned)((m + 15) / 16), (unsigned)((batch + 8 * NT - 1) / (8 * NT)));
-    const bool vec = aligned(x, 16) && ldx * sizeof(X) % 16 == 0;
-    if (vec) stream4_kernel<X, T, NT, NM, WARPS, true><<<grid, WARPS * 32, 0, s>>>(w0, w1, m, n, group, act, (const X*)x, ldx, batch, (X*)y, ldy);
-    else stream4_kernel<X, T, NT, NM, WARPS, false><<<grid, WARPS * 32, 0, s>>>(w0, w1, m, n, group, act, (const X*)x, ldx, batch, (X*)y, ldy);
+// ---- more vectors -------------------------------------------------------------------------------------
+//
+// A CTA takes 128 rows of one matrix (gated: 64 rows of both) and N = 16, 32 or 64 vectors on the 5th-generation
+// tensor cores; a cluster of up to 8 CTAs one such tile, each a share of its columns.  Eight warps turn codes
+// into 16-bit floats and stage them with the vectors' entries in swizzled shared memory, 128 columns a stage;
+// one thread issues the products, every group of columns into an accumulator of its own; four warps scale
+// each group's accumulator into fp32 registers, a row per thread, so that the row's scale is one register.
+// The offsets' part comes from a second product of the same entries with ones, whose accumulator holds the
+// group's sum of x in every row.  The CTAs' sums meet through distributed shared memory in a fixed order.
+// (Weights scaled before the product would need no accumulator per group, but s (q - 8) + b does not fit 16
+// bits: measured against 64 bits that costs bf16 results 1.4 times the error of their own rounding.)
+// Bound by the codes' unpacking and staging at few vectors' worth of arithmetic a weight.
+constexpr int TC_EPI = 4, TC_PROD = 8, TC_THREADS = (TC_EPI + 1 + TC_PROD) * 32;
+constexpr int TC_BUFS = 4;                                // accumulators in flight
+template <typename X> __host__ __device__ constexpr int tc_stages() { return Raw8<X>::PLANES == 3 ? 2 : 4; }
+template <typename X, int N> __host__ __device__ constexpr int tc_stage() { return 128 * 256 + Raw8<X>::PLANES * N * 256; }
+template <typename X, int N> __host__ __device__ constexpr int tc_smem() {
+    return tc_stages<X>() * tc_stage<X, N>() + 128 * 128 + 1024;          // stages, the ones, alignment
+}
+
+template <typename X, typename T, int N, int NM, int WORDS, bool AFFINE>
+__global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, int64_t m, int64_t n, int act, const X* __restrict__ x,
+                                                             int64_t ldx, int vec, int64_t batch, X* __restrict__ y, int64_t ldy,
+                                                             int splits) {
+    using Raw = typename Raw8<X>::type;
+    constexpr int PLANES = Raw8<X>::PLANES;
+    using XE = typename std::conditional<PLANES == 3, float, unsigned short>::type;
+    constexpr int GROUPS = 4 / WORDS, STAGES = tc_stages<X>(), STAGE = tc_stage<X, N>(), ROWS = 128 / NM;
+    constexpr uint32_t COLUMNS = TC_BUFS * N * 2;           // tensor memory: products and sums (power of two, 128 .. 512)
+    static_assert(128 * (N + 1) * 4 <= STAGES * STAGE, "the tile of sums takes the stages' place");
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(8) uint64_t bars[2 * STAGES + 2 * TC_BUFS + 1];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int quit_flag;
+    const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;
+    unsigned char* const smem = raw + (base - smem_u32(raw));
+    const uint32_t ones = base + STAGES * STAGE;
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * STAGES, dfull0 = empty0 + 8 * STAGES, dempty0 = dfull0 + 8 * TC_BUFS,
+                   drain = dempty0 + 8 * TC_BUFS;
+    volatile int* const quit = &quit_flag;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int split = blockIdx.x % splits;
+    const int64_t row0 = (int64_t)(blockIdx.x / splits) * ROWS, col0 = (int64_t)blockIdx.y * N;
+    const int blocks = (int)((n + 127) / 128), groups = (int)((n + 32 * WORDS - 1) / (32 * WORDS));
+    const int first = (int)((int64_t)blocks * split / splits), last = (int)((int64_t)blocks * (split + 1) / splits);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(full0 + 8 * i, TC_PROD * 32);
+            mbar_init(empty0 + 8 * i, 1);
+        }
+        for (int i = 0; i < TC_BUFS; ++i) {
+            mbar_init(dfull0 + 8 * i, 1);
+            mbar_init(dempty0 + 8 * i, TC_EPI);
+        }
+        mbar_init(drain, 1);
+        quit_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == TC_EPI) tmem_alloc<1>(smem_u32(&tmem_slot), COLUMNS);
+    if (AFFINE) {                                            // 128 rows of ones, 64 deep (every 16 of them serve)
+        const uint32_t one = std::is_same<T, __half>::value ? 0x3c003c00u : 0x3f803f80u;
+        for (int e = threadIdx.x; e < 128 * 8; e += TC_THREADS)
+            *reinterpret_cast<uint4*>(smem + STAGES * STAGE + 16 * e) = make_uint4(one, one, one, one);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *(volatile uint32_t*)&tmem_slot;
+
+    float out[N];
+    if (warp > TC_EPI) {
+        // ---- codes and entries into shared memory: thread p unpacks half of row p % 128, and a share of the entries
+        const int p = threadIdx.x - (TC_EPI + 1) * 32, r = p & 127, h = p >> 7;
+        const Mat4 w = NM == 2 && r >= 64 ? w1 : w0;
+        const int64_t row = min(row0 + (NM == 2 ? r & 63 : r), m - 1);    // rows past the last one repeat it
+        const uint4* const src = reinterpret_cast<const uint4*>(w.q + row * blocks * 64) + 2 * h;
+        constexpr int PIECES = N * 16 / (TC_PROD * 32);      // pieces of 8 entries a thread
+        constexpr int AHEAD = PLANES == 3 ? 1 : 2;           // blocks in flight
+        uint4 code[AHEAD][2];
+        Raw ent[AHEAD][PIECES];
+        const XE* xp[PIECES];
+        #pragma unroll
+        for (int e = 0; e < PIECES; ++e) {
+            const int64_t col = col0 + (p >> 4) + e * (TC_PROD * 2);
+            xp[e] = col < batch ? reinterpret_cast<const XE*>(x + col * ldx) : nullptr;
+        }
+        const auto load = [&](int u, int blk) {
+            if (blk >= last) return;
+            code[u][0] = __ldcs(src + (int64_t)blk * 4);
+            code[u][1] = __ldcs(src + (int64_t)blk * 4 + 1);
+            const int64_t k = (int64_t)blk * 128 + 8 * (p & 15);
+            #pragma unroll
+            for (int e = 0; e < PIECES; ++e) {
+                ent[u][e] = Raw{};
+                if (xp[e]) ent[u][e] = load8(xp[e], k, n, vec);
+            }
+        };
+        #pragma unroll
+        for (int u = 0; u < AHEAD; ++u) load(u, first + u);
+        int it = 0;
+        bool ok = true;
+        for (int b0 = first; b0 < last && ok; b0 += AHEAD) {
+            #pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int blk = b0 + u;
+                if (blk >= last) break;
+                const int s = it % STAGES;
+                if (!mbar_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1, quit)) { ok = false; break; }
+                ++it;
+                unsigned char* const st = smem + s * STAGE;
+                #pragma unroll
+                for (int cc = 0; cc < 2; ++cc)
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        // columns 32 i + 8 c of the block: half i / 2, 16-byte chunk 4 (i % 2) + c, swizzled by the row
+                        uint32_t v[4];
+                        codes8<T>(word_of(code[u][cc], i), v);
+                        const int chunk = 4 * (i & 1) + 2 * h + cc;
+                        *reinterpret_cast<uint4*>(st + (i >> 1) * (128 * 128) + r * 128 + ((chunk ^ (r & 7)) << 4)) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                #pragma unroll
+                for (int e = 0; e < PIECES; ++e) {
+                    const int col = (p >> 4) + e * (TC_PROD * 2), piece = p & 15;
+                    uint32_t v[PLANES][4];
+                    planes8(ent[u][e], v);
+                    #pragma unroll
+                    for (int q = 0; q < PLANES; ++q)
+                        *reinterpret_cast<uint4*>(st + 128 * 256 + q * N * 256 + (piece >> 3) * (N * 128) + col * 128 +
+                                                  (((piece & 7) ^ (col & 7)) << 4)) = make_uint4(v[q][0], v[q][1], v[q][2], v[q][3]);
+                }
+                load(u, blk + AHEAD);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive_cluster(full0 + 8 * s);          // an address of this CTA is one of the cluster's
+            }
+        }
+    } else if (warp == TC_EPI) {
+        if (lane == 0) {
+            // ---- products
+            constexpr uint32_t idesc = f16_idesc(std::is_same<T, __half>::value ? 0 : 1, false, false, 128, N);
+            int it = 0, buf = 0;
+            bool ok = true;
+            for (int blk = first; blk < last && ok; ++blk, ++it) {
+                const int s = it % STAGES;
+                if (!mbar_wait(full0 + 8 * s, (it / STAGES) & 1, quit)) break;
+                fence_after();
+                const uint32_t sa = base + s * STAGE, sb = sa + 128 * 256;
+                const uint64_t one = smem_desc(ones, 16, 1024);
+                for (int g = 0; g < GROUPS; ++g, ++buf) {
+                    const int d = buf % TC_BUFS;
+                    if (!mbar_wait(dempty0 + 8 * d, ((buf / TC_BUFS) & 1) ^ 1, quit)) { ok = false; break; }
+                    fence_after();
+                    #pragma unroll
+                    for (int k = 0; k < 2 * WORDS; ++k) {
+                        const int kk = g * 2 * WORDS + k;    // 16 columns of the block: half kk / 4, 32 bytes each
+                        const uint64_t da = smem_desc(sa + (kk >> 2) * (128 * 128) + (kk & 3) * 32, 16, 1024);
+                        #pragma unroll
+                        for (int q = PLANES - 1; q >= 0; --q) {
+                            const uint64_t db = smem_desc(sb + q * N * 256 + (kk >> 2) * (N * 128) + (kk & 3) * 32, 16, 1024);
+                            const bool more = k > 0 || q < PLANES - 1;
+                            mma_f16<1>(tmem + d * N, da, db, idesc, more);
+                            if (AFFINE) mma_f16<1>(tmem + (TC_BUFS + d) * N, one, db, idesc, more);
+                        }
+                    }
+                    mma_commit<1>(dfull0 + 8 * d);
+                }
+                mma_commit<1>(empty0 + 8 * s);
+            }
+            // the tensor memory is freed and the stages reused only when everything issued has ended
+            mma_commit<1>(drain);
+            const uint64_t t0 = timer_ns();
+            while (!mbar_try(drain, 0) && timer_ns() - t0 < WAIT_LIMIT_NS) {}
+        }
+    } else {
+        // ---- scaling: warp w holds rows 32 w .. 32 w + 31 of the tile
+        const int r = 32 * warp + lane;
+        const Mat4 w = NM == 2 && r >= 64 ? w1 : w0;
+        const int64_t row = min(row0 + (NM == 2 ? r & 63 : r), m - 1);
+        const __half* ps = w.scale + (int64_t)first * GROUPS * m + row;
+        const __half* po = AFFINE && w.offset ? w.offset + (int64_t)first * GROUPS * m + row : nullptr;
+        const int count = min(last * GROUPS, groups) - first * GROUPS, all = (last - first) * GROUPS;
+        #pragma unroll
+        for (int t = 0; t < N; ++t) out[t] = 0.0f;
+        __half s_next = count > 0 ? __ldg(ps) : __ushort_as_half(0), o_next = count > 0 && po ? __ldg(po) : __ushort_as_half(0);
+        for (int g = 0; g < all; ++g) {
+            const float s = __half2float(s_next), o = __half2float(o_next);
+            if (g + 1 < count) {
+                s_next = __ldg(ps += m);
+                if (AFFINE && po) o_next = __ldg(po += m);
+            } else {
+                s_next = o_next = __ushort_as_half(0);       // past the last group: its entries are 0
+            }
+            const int d = g % TC_BUFS;
+            if (!mbar_wait(dfull0 + 8 * d, (g / TC_BUFS) & 1, quit)) break;
+            fence_after();
+            const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16) + d * N;
+            constexpr int CH = N < 32 ? N : 32;
+            #pragma unroll
+            for (int t = 0; t < N; t += CH) {
+                uint32_t v[CH];
+                if constexpr (CH == 32) tmem_ld32(at + t, v); else tmem_ld16(at + t, v);
+                tmem_wait_ld();
+                #pragma unroll
+                for (int e = 0; e < CH; ++e) out[t + e] = fmaf(s, __uint_as_float(v[e]), out[t + e]);
+                if (AFFINE) {
+                    if constexpr (CH == 32) tmem_ld32(at + TC_BUFS * N + t, v); else tmem_ld16(at + TC_BUFS * N + t, v);
+                    tmem_wait_ld();
+                    #pragma unroll
+                    for (int e = 0; e < CH; ++e) out[t + e] = fmaf(o, __uint_as_float(v[e]), out[t + e]);
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(dempty0 + 8 * d);
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    // the stages become the tile of sums (all products have ended)
+    float* const red = reinterpret_cast<float*>(smem);
+    if (warp < TC_EPI) {
+        const bool bad = *quit != 0;                         // a wait gave up: NaN rather than a wrong number
+        #pragma unroll
+        for (int t = 0; t < N; ++t) red[(32 * warp + lane) * (N + 1) + t] = bad ? __uint_as_float(0x7fffffffu) : out[t];
+    }
+    if (warp == TC_EPI) tmem_free<1>(tmem, COLUMNS);
+    if (splits > 1) cluster_sync();
+    else __syncthreads();
+    // each CTA of the cluster adds and stores a share of the rows
+    const int r0 = ROWS * split / splits, share = ROWS * (split + 1) / splits - r0;
+    for (int e = threadIdx.x; e < share * N; e += TC_THREADS) {
+        const int rr = r0 + e % share, cc = e / share;
+        if (row0 + rr >= m || col0 + cc >= batch) continue;
+        float v[NM] = {};
+        #pragma unroll
+        for (int j = 0; j < NM; ++j) {
+            const float* const p = red + (64 * j + rr) * (N + 1) + cc;
+            if (splits == 1) v[j] = *p;
+            else
+                for (int q = 0; q < splits; ++q) v[j] += ld_cluster(map_rank(smem_u32(p), q));
+        }
+        const float res = NM == 1 ? v[0] : act_rt<PLANES == 3>(act, v[0]) * v[NM - 1];
+        y[(col0 + cc) * ldy + row0 + rr] = from_f32<X>(res);
+    }
+    if (splits > 1) cluster_sync();                          // peers may still read this CTA's sums
+}
+
+// one call's arguments
+struct Product {
+    Mat4 w0, w1;
+    int64_t m, n;
+    int group, act;
+    const void* x; int64_t ldx;
+    int64_t batch;
+    void* y; int64_t ldy;
+    cudaStream_t stream;
+};
+
+// dynamic shared memory beside at most 10 KB of static: what the 48 KB every kernel has does not hold
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes) {
+    return bytes > 38 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) : cudaSuccess;
+}
+
+template <typename X, typename T, int NM, int WORDS, bool AFFINE>
+cudaError_t launch_vec4(const Product& p) {
+    const auto kernel = vec4_kernel<X, T, NM, WORDS, AFFINE>;
+    const cudaError_t e = allow_smem(kernel, vec_smem<NM>());
+    if (e != cudaSuccess) return e;
+    const bool vec = aligned(p.x, 16) && p.ldx * sizeof(X) % 16 == 0;
+    kernel<<<(unsigned)((p.m + 15) / 16), VEC_WARPS * 32, vec_smem<NM>(), p.stream>>>(p.w0, p.w1, p.m, p.n, p.act, (const X*)p.x, p.ldx,
+                                                                                    vec, (int)p.batch, (X*)p.y, p.ldy);
     return cudaGetLastError();
 }
 
+template <typename X, typename T, int NM, int WORDS, bool AFFINE, int N>
+cudaError_t launch_tile4(const Product& p) {
+    const auto kernel = tile4_kernel<X, T, N, NM, WORDS, AFFINE>;
+    constexpr int smem = tc_smem<X, N>();
+    const cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    const bool vec = aligned(p.x, 16) && p.ldx * sizeof(X) % 16 == 0;
+    const int64_t tiles = (p.m + 128 / NM - 1) / (128 / NM), cols = (p.batch + N - 1) / N, blocks = (p.n + 127) / 128;
+    // shares of the columns: the fewest rounds of CTAs times the blocks of a share, each CTA costing about
+    // three blocks' time to start, fill its stages and add up
+    int splits = 1;
+    int64_t best = INT64_MAX;
+    for (int c = 1; c <= 8 && c <= blocks; ++c) {
+        const int64_t cost = (tiles * cols * c + sm_count() - 1) / sm_count() * ((blocks + c - 1) / c + 3);
+        if (cost < best) { best = cost; splits = c; }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * splits), (unsigned)cols);
+    cfg.blockDim = dim3(TC_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = p.stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)splits;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p.w0, p.w1, p.m, p.n, p.act, (const X*)p.x, p.ldx, (int)vec, p.batch, (X*)p.y, p.ldy, splits);
+}
+
+template <typename X, typename T, int NM, int WORDS, bool AFFINE>
+cudaError_t run_kernel(const Product& p) {
+    if (p.batch <= 8) return launch_vec4<X, T, NM, WORDS, AFFINE>(p);
+    if (p.batch <= 16) return launch_tile4<X, T, NM, WORDS, AFFINE, 16>(p);
+    if (p.batch <= 32) return launch_tile4<X, T, NM, WORDS, AFFINE, 32>(p);
+    return launch_tile4<X, T, NM, WORDS, AFFINE, 64>(p);
+}
+
+template <typename X, typename T, int NM, int WORDS>
+cudaError_t run_group(const Product& p) {
+    return p.w0.offset || (NM == 2 && p.w1.offset) ? run_kernel<X, T, NM, WORDS, true>(p) : run_kernel<X, T, NM, WORDS, false>(p);
+}
+
 template <typename X, typename T, int NM>
-cudaError_t run_stream4(const Mat4& w0, const Mat4& w1, int64_t m, int64_t n, int group, int act, const void* x, int64_t ldx,
-                        int64_t batch, void* y, int64_t ldy, cudaStream_t s) {
-    if (batch <= 8) return launch_stream4<X, T, 1, NM, 8>(w0, w1, m, n, group, act, x, ldx, batch, y, ldy, s);
-    return launch_stream4<X, T, 4, NM, 4>(w0, w1, m, n, group, act, x, ldx, batch, y, ldy, s);
+cudaError_t run_product(const Product& p) {
+    switch (p.group) {
+        case 32: return run_group<X, T, NM, 1>(p);
+        case 64: return run_group<X, T, NM, 2>(p);
+        default: return run_group<X, T, NM, 4>(p);
+    }
 }
 
 template <int NM>
@@ -355,40 +778,46 @@ int products(const Mat4& w0, const Mat4& w1, int64_t m, int64_t n, int group, in
     if (batch == 0) return EXTERND_OK;
     const size_t eb = dtype_bytes(dtype);
     if (!X || !Y || !aligned(X, eb) || !aligned(Y, eb) || !dev.holds(X) || !dev.holds(Y)) return EXTERND_EINVAL;
-    if ((m + 15) / 16 > 0x7fffffff || (batch + 7) / 8 > 65535) return EXTERND_ELIMIT;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    // grid dimensions, 32-bit column blocks
+    if ((m + 15) / 16 > 0x7fffffff / 8 || (batch + 63) / 64 > 65535 || n > 0x7fffffff - 128) return EXTERND_ELIMIT;
+    const Product p = {w0, w1, m, n, group, act, X, ldx, batch, Y, ldy, reinterpret_cast<cudaStream_t>(stream)};
     cudaError_t e;
     switch (dtype) {
-        case EXTERND_F32: e = run_stream4<float, __nv_bfloat16, NM>(w0, w1, m, n, group, act, X, ldx, batch, Y, ldy, s); break;
-        case EXTERND_F16: e = run_stream4<__half, __half, NM>(w0, w1, m, n, group, act, X, ldx, batch, Y, ldy, s); break;
-        default: e = run_stream4<__nv_bfloat16, __nv_bfloat16, NM>(w0, w1, m, n, group, act, X, ldx, batch, Y, ldy, s); break;
+        case EXTERND_F32: e = run_product<float, __nv_bfloat16, NM>(p); break;
+        case EXTERND_F16: e = run_product<__half, __half, NM>(p); break;
+        default: e = run_product<__nv_bfloat16, __nv_bfloat16, NM>(p); break;
     }
     if (e != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
     return EXTERND_OK;
 }
 
-unsigned grid_for(int64_t items, int per_cta) {
-    const int64_t want = (items + per_cta - 1) / per_cta, cap = (int64_t)sm_count() * 64;
-    return (unsigned)(want < cap ? want : cap);
+// rows in x; y splits a row where the rows alone leave the SMs short of warps
+dim3 row_grid(int64_t m, int64_t steps) {
+    const int64_t x = (m + 7) / 8, want = (int64_t)sm_count() * 16;
+    int64_t y = x >= want ? 1 : (want + x - 1) / x;
+    y = y < steps ? y : steps;
+    return dim3((unsigned)x, (unsigned)(y < 65535 ? y : 65535));
 }
+
+int log2_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
 
 template <typename T, bool AFFINE>
 cudaError_t run_quantize(const void* A, int64_t m, int64_t n, int64_t lda, int group, uint8_t* q, void* scale, void* offset,
                          int* status, cudaStream_t s) {
-    const unsigned grid = grid_for(m * ((n + 127) / 128), 8);
+    const dim3 grid = row_grid(m, ((n + 127) / 128 + QBLOCKS<T> - 1) / QBLOCKS<T>);
     const bool vec = aligned(A, 4 * sizeof(T)) && lda % 4 == 0;
-    if (vec) quantize_kernel<T, AFFINE, true><<<grid, 256, 0, s>>>((const T*)A, m, n, lda, group, (uint32_t*)q, (__half*)scale, (__half*)offset, status);
-    else quantize_kernel<T, AFFINE, false><<<grid, 256, 0, s>>>((const T*)A, m, n, lda, group, (uint32_t*)q, (__half*)scale, (__half*)offset, status);
+    const auto kernel = vec ? quantize_kernel<T, AFFINE, true> : quantize_kernel<T, AFFINE, false>;
+    kernel<<<grid, 256, 0, s>>>((const T*)A, m, n, lda, log2_of(group), (uint32_t*)q, (__half*)scale, (__half*)offset, status);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t run_dequantize(const uint8_t* q, const void* scale, const void* offset, int64_t m, int64_t n, int group, void* out,
                            int64_t ldo, cudaStream_t s) {
-    const unsigned grid = grid_for(m * ((n + 127) / 128), 16);
+    const dim3 grid = row_grid(m, ((n + 127) / 128 + 1) / 2);
     const bool vec = aligned(out, 16) && ldo * sizeof(T) % 16 == 0;
-    if (vec) dequantize_kernel<T, true><<<grid, 256, 0, s>>>((const uint32_t*)q, (const __half*)scale, (const __half*)offset, m, n, group, (T*)out, ldo);
-    else dequantize_kernel<T, false><<<grid, 256, 0, s>>>((const uint32_t*)q, (const __half*)scale, (const __half*)offset, m, n, group, (T*)out, ldo);
+    const auto kernel = vec ? dequantize_kernel<T, true> : dequantize_kernel<T, false>;
+    kernel<<<grid, 256, 0, s>>>((const uint32_t*)q, (const __half*)scale, (const __half*)offset, m, n, log2_of(group), (T*)out, ldo);
     return cudaGetLastError();
 }
 
@@ -406,6 +835,7 @@ int externd_int4_quantize(const void* A, int dtype, int64_t m, int64_t n, int64_
     if (!aligned(A, dtype_bytes(dtype)) || !aligned(q_out, 16) || !aligned(scale_out, 2) || !aligned(offset_out, 2) ||
         !aligned(async_status, 4))
         return EXTERND_EINVAL;
+    if (m > 0x7fffffffll * 8 || n > 0x7fffffff - 128) return EXTERND_ELIMIT;
     const Device dev;
     if (!dev.holds(A) || !dev.holds(q_out) || !dev.holds(scale_out) || (offset_out && !dev.holds(offset_out)) ||
         (async_status && !dev.holds(async_status)))
@@ -448,6 +878,7 @@ int externd_int4_dequantize(const uint8_t* q, const void* scale, const void* off
                             int dtype, int64_t ldo, void* stream) {
     if (!q || !scale || !out || m < 1 || n < 1 || ldo < n || !valid_dtype(dtype) || !valid_group(group)) return EXTERND_EINVAL;
     if (!aligned(q, 16) || !aligned(scale, 2) || !aligned(offset, 2) || !aligned(out, dtype_bytes(dtype))) return EXTERND_EINVAL;
+    if (m > 0x7fffffffll * 8 || n > 0x7fffffff - 128) return EXTERND_ELIMIT;
     const Device dev;
     if (!dev.holds(q) || !dev.holds(scale) || (offset && !dev.holds(offset)) || !dev.holds(out)) return EXTERND_EINVAL;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -145,13 +145,13 @@ template <typename T> __device__ __forceinline__ void mma16816(float (&d)[4], ui
                                                                uint32_t a3, uint32_t b0, uint32_t b1);
 template <> __device__ __forceinline__ void mma16816<__half>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                                              uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 template <> __device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                                                     uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -170,52 +170,77 @@ __device__ __forceinline__ void split3(float x, uint32_t& hi, uint32_t& mid, uin
     lo = __float_as_uint(r2) >> 16;
 }
 
-// eight consecutive entries of one vector as product operands
-template <typename T, int PLANES>
-struct XFrag { uint32_t v[PLANES][4]; };
+// Eight consecutive 16-bit entries k .. k + 7 of a row (entries from n on are 0).  vec: rows start on 16-byte
+// boundaries.
+__device__ __forceinline__ uint4 load8(const unsigned short* __restrict__ x, int64_t k, int64_t n, bool vec) {
+    if (vec && k + 8 <= n) return __ldg(reinterpret_cast<const uint4*>(x + k));
+    uint32_t v[4];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = k + 2 * i < n ? __ldg(x + k + 2 * i) : 0;
+        const uint32_t b = k + 2 * i + 1 < n ? __ldg(x + k + 2 * i + 1) : 0;
+        v[i] = a | (b << 16);
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
 
-// X is the vector's row; entries from n on (and whole vectors, x == nullptr) are 0
-template <typename X, typename T, int PLANES, bool VEC>
-__device__ __forceinline__ void load_x(const X* __restrict__ x, int64_t k, int64_t n, XFrag<T, PLANES>& f) {
-    if (x == nullptr || k >= n) {
-        #pragma unroll
-        for (int p = 0; p < PLANES; ++p)
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) f.v[p][i] = 0;
-        return;
+struct F8 { float4 a, b; };
+__device__ __forceinline__ F8 load8(const float* __restrict__ x, int64_t k, int64_t n, bool vec) {
+    if (vec && k + 8 <= n) return {__ldg(reinterpret_cast<const float4*>(x + k)), __ldg(reinterpret_cast<const float4*>(x + k) + 1)};
+    float v[8];
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = k + i < n ? __ldg(x + k + i) : 0.0f;
+    return {make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7])};
+}
+
+// ... as product operands: one plane of 16-bit pairs, or the three bf16 planes of fp32 entries
+template <typename X> struct Raw8;
+template <> struct Raw8<float> { using type = F8; static constexpr int PLANES = 3; };
+template <> struct Raw8<__half> { using type = uint4; static constexpr int PLANES = 1; };
+template <> struct Raw8<__nv_bfloat16> { using type = uint4; static constexpr int PLANES = 1; };
+
+__device__ __forceinline__ void planes8(const uint4& r, uint32_t (&v)[1][4]) {
+    v[0][0] = r.x; v[0][1] = r.y; v[0][2] = r.z; v[0][3] = r.w;
+}
+__device__ __forceinline__ void planes8(const F8& r, uint32_t (&v)[3][4]) {
+    const float e[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h0, m0, l0, h1, m1, l1;
+        split3(e[2 * i], h0, m0, l0);
+        split3(e[2 * i + 1], h1, m1, l1);
+        v[0][i] = h0 | (h1 << 16);
+        v[1][i] = m0 | (m1 << 16);
+        v[2][i] = l0 | (l1 << 16);
     }
-    if constexpr (PLANES == 1) {
-        if (VEC && k + 8 <= n) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(x + k));
-            f.v[0][0] = v.x; f.v[0][1] = v.y; f.v[0][2] = v.z; f.v[0][3] = v.w;
-        } else {
-            const unsigned short* xs = reinterpret_cast<const unsigned short*>(x);
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t a = k + 2 * i < n ? __ldg(xs + k + 2 * i) : 0;
-                const uint32_t b = k + 2 * i + 1 < n ? __ldg(xs + k + 2 * i + 1) : 0;
-                f.v[0][i] = a | (b << 16);
-            }
-        }
-    } else {
-        float e[8];
-        if (VEC && k + 8 <= n) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(x + k)), b = __ldg(reinterpret_cast<const float4*>(x + k) + 1);
-            e[0] = a.x; e[1] = a.y; e[2] = a.z; e[3] = a.w; e[4] = b.x; e[5] = b.y; e[6] = b.z; e[7] = b.w;
-        } else {
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = k + i < n ? __ldg(x + k + i) : 0.0f;
-        }
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t h0, m0, l0, h1, m1, l1;
-            split3(e[2 * i], h0, m0, l0);
-            split3(e[2 * i + 1], h1, m1, l1);
-            f.v[0][i] = h0 | (h1 << 16);
-            f.v[1][i] = m0 | (m1 << 16);
-            f.v[2][i] = l0 | (l1 << 16);
-        }
-    }
+}
+
+// ---- clusters ------------------------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// a shared-memory address of this CTA -> the same place in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 }  // namespace externd_llm
