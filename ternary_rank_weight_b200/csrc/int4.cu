@@ -18,12 +18,12 @@ using namespace externd_llm;
 __host__ __device__ __forceinline__ int64_t row_bytes(int64_t n) { return (n + 127) / 128 * 64; }
 
 // ---------------------------------------------------------------------------------------------------
-// quantise: one warp per row and block of 128 columns; lane L holds columns 4 L .. 4 L + 3
+// quantise: a warp per row and pair of blocks, 8 columns (one word of codes) a lane
 // ---------------------------------------------------------------------------------------------------
 //
 // One pass over A: the group's extremes stay in registers.  Bound by memory when the arithmetic stays in
 // fp32; the format's fp64 decisions are taken in fp64 only next to a border (1e-4-wide bands around the
-// rounding borders of codes, 2^-10 of the scales), where the fp32 value cannot decide.
+// rounding borders of codes, 2^-8 of the scales), where the fp32 value cannot decide.
 
 // says whether the fp32 estimate e (relative error below 2^-20) of a value leaves open to which fp16 it rounds
 __device__ __forceinline__ bool near_half_border(float e) {
@@ -32,109 +32,187 @@ __device__ __forceinline__ bool near_half_border(float e) {
     return u < 0x38800000u + 64u || u >= 0x477fe000u || (low > 0x1000u - 16u && low < 0x1000u + 16u);   // subnormal or top fp16s too
 }
 
-template <typename T> constexpr int QBLOCKS = sizeof(T) == 4 ? 2 : 4;     // blocks a warp has in flight
+// Greatest entry and greatest negated entry of a lane's eight, then of the LANES lanes of its group.  16-bit
+// entries travel as a pair in one register.  `bad` becomes NaN where an entry is not finite.
+template <int LANES>
+__device__ __forceinline__ float2 group_extremes(const float (&w)[8], float& bad) {
+    float mx = w[0], mn = w[0];
+    #pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        bad = fmaf(w[t], 0.0f, bad);
+        mx = fmaxf(mx, w[t]);
+        mn = fminf(mn, w[t]);
+    }
+    #pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+        mn = fminf(mn, __shfl_xor_sync(FULL, mn, o));
+    }
+    return make_float2(mx, -mn);
+}
+template <int LANES, typename T, typename T2>
+__device__ __forceinline__ float2 pair_extremes(const T (&w)[8], float& bad) {
+    const T2* const v = reinterpret_cast<const T2*>(w);
+    const T zero = from_f32<T>(0.0f);
+    T2 z;
+    z.x = z.y = zero;
+    const T2 zz = z;
+    #pragma unroll
+    for (int t = 0; t < 4; ++t) z = __hfma2(v[t], zz, z);
+    bad += to_f32(z.x) + to_f32(z.y);
+    const T2 hi = __hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3])), lo = __hmin2(__hmin2(v[0], v[1]), __hmin2(v[2], v[3]));
+    T2 e;
+    e.x = __hmax(hi.x, hi.y);
+    e.y = __hneg(__hmin(lo.x, lo.y));
+    #pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) {
+        const uint32_t u = __shfl_xor_sync(FULL, *reinterpret_cast<const uint32_t*>(&e), o);
+        e = __hmax2(e, *reinterpret_cast<const T2*>(&u));
+    }
+    return make_float2(to_f32(e.x), to_f32(e.y));
+}
+template <int LANES> __device__ __forceinline__ float2 group_extremes(const __half (&w)[8], float& bad) {
+    return pair_extremes<LANES, __half, __half2>(w, bad);
+}
+template <int LANES> __device__ __forceinline__ float2 group_extremes(const __nv_bfloat16 (&w)[8], float& bad) {
+    return pair_extremes<LANES, __nv_bfloat16, __nv_bfloat162>(w, bad);
+}
 
-template <typename T, bool AFFINE, bool VEC>
-__global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ A, int64_t m, int64_t n, int64_t lda, int lg,
+constexpr int QPAIRS = 4;                               // pairs of blocks a warp works on at once
+
+// LG = log2(group).  A warp takes QPAIRS pairs of blocks of its row at once: the loads are in flight together, and
+// of the lanes that share a group each quarter computes the scale of another pair (they would all compute the same).
+template <typename T, bool AFFINE, bool VEC, int LG>
+__global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ A, int64_t m, int64_t n, int64_t lda,
                                                        uint32_t* __restrict__ q, __half* __restrict__ scale,
                                                        __half* __restrict__ offset, int* __restrict__ status) {
-    constexpr int UB = QBLOCKS<T>;
+    constexpr int LANES = 1 << (LG - 3), QUARTER = LANES / QPAIRS;      // lanes of a group
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);   // neighbouring warps, neighbouring rows: their scales share a sector
     if (row >= m) return;
-    const int blocks = (int)((n + 127) / 128);
-    const T* const arow = A + row * lda + 4 * lane;
-    for (int b0 = blockIdx.y * UB; b0 < blocks; b0 += gridDim.y * UB) {
-        float w[UB][4];
+    const int blocks = (int)((n + 127) / 128), pairs = (blocks + 1) / 2, sub = lane >> 4, l = lane & 15;
+    const T* const arow = A + row * lda;
+    uint32_t* const qrow = q + row * blocks * 16 + 16 * sub + 4 * (l & 3) + (l >> 2);    // word 4 c + i of a block
+    const int mine = (lane % LANES) / QUARTER;              // the pair whose scale this lane computes
+    const int head = lane & ~(LANES - 1);                   // the group's first lane
+    for (int p0 = blockIdx.y * QPAIRS; p0 < pairs; p0 += gridDim.y * QPAIRS) {
+        __align__(16) T w[QPAIRS][8];
         #pragma unroll
-        for (int u = 0; u < UB; ++u) {
-            const int64_t j0 = (int64_t)(b0 + u) * 128 + 4 * lane;
-            const T* a = arow + (int64_t)(b0 + u) * 128;
-            if (VEC && j0 + 4 <= n) {
-                if constexpr (sizeof(T) == 4) {
-                    const float4 v = __ldcs(reinterpret_cast<const float4*>(a));
-                    w[u][0] = v.x; w[u][1] = v.y; w[u][2] = v.z; w[u][3] = v.w;
-                } else {
-                    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(a));
-                    const float2 lo = unpack2<T>(v.x), hi = unpack2<T>(v.y);
-                    w[u][0] = lo.x; w[u][1] = lo.y; w[u][2] = hi.x; w[u][3] = hi.y;
-                }
-            } else {
+        for (int u = 0; u < QPAIRS; ++u) {
+            const int64_t j0 = (int64_t)(p0 + u) * 256 + 8 * lane;
+            if (VEC && j0 + 8 <= n) {
                 #pragma unroll
-                for (int t = 0; t < 4; ++t) w[u][t] = j0 + t < n ? to_f32(a[t]) : 0.0f;
+                for (int h = 0; h < (int)sizeof(T) / 2; ++h)
+                    reinterpret_cast<uint4*>(w[u])[h] = __ldcs(reinterpret_cast<const uint4*>(arow + j0) + h);
+            } else {
+                // columns past the last one repeat the group's first: they change no extreme
+                const int64_t g0 = j0 >> LG << LG;
+                #pragma unroll
+                for (int t = 0; t < 8; ++t) w[u][t] = g0 < n ? arow[j0 + t < n ? j0 + t : g0] : from_f32<T>(0.0f);
             }
         }
+        float2 ext = make_float2(0.0f, 0.0f);               // greatest, greatest negated: of this lane's pair
+        float bad = 0.0f;
         #pragma unroll
-        for (int u = 0; u < UB; ++u) {
-            const int blk = b0 + u;
-            if (blk >= blocks) break;
-            const int64_t j0 = (int64_t)blk * 128 + 4 * lane;
-            const int left = j0 >= n ? 0 : n - j0 >= 4 ? 4 : (int)(n - j0);     // columns of this lane
-            float mn = INFINITY, mx = -INFINITY;
-            bool finite = true;
-            #pragma unroll
-            for (int t = 0; t < 4; ++t)
-                if (t < left) {
-                    finite = finite && fabsf(w[u][t]) <= FLT_MAX;
-                    mn = fminf(mn, w[u][t]);
-                    mx = fmaxf(mx, w[u][t]);
-                }
-            for (int o = 1; o < 1 << (lg - 2); o <<= 1) {
-                mn = fminf(mn, __shfl_xor_sync(FULL, mn, o));
-                mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-            }
-            const bool any = mn <= mx || !finite;      // the group has columns (with NaN only, mn stays above mx)
-            float s = 0.0f, b = 0.0f;
-            if (any) {
-                const float range = AFFINE ? mx - mn : fmaxf(-mn, mx);
-                float e = range * (AFFINE ? 1.0f / 15.0f : 1.0f / 7.0f);
-                if (near_half_border(e)) e = (float)(AFFINE ? ((double)mx - (double)mn) / 15.0 : (double)range / 7.0);
-                s = __half2float(__float2half_rn(e));
-                if (AFFINE) {
-                    float f = fmaf(8.0f, s, mn);
-                    if (near_half_border(f)) f = (float)((double)mn + 8.0 * (double)s);
-                    b = __half2float(__float2half_rn(f));
-                }
-            }
-            // a group with NaN or Inf reports that, whatever other groups report
-            if (!finite) atomicExch(status, EXTERND_ENONFINITE);
-            else if (any && fmaxf(-mn, mx) <= FLT_MAX && (isinf(s) || isinf(b))) atomicCAS(status, EXTERND_OK, EXTERND_ELIMIT);
-            const float inv = s > 0.0f ? __fdividef(1.0f, s) : 0.0f;
-            float c[4], r[4];
-            bool border = false;
-            #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                c[t] = (AFFINE ? w[u][t] - b : w[u][t]) * inv;
-                r[t] = rintf(c[t]);
-                // |c| <= 16 wherever it is not clamped: its error is below 1e-5
-                border = border || (fabsf(fabsf(c[t] - r[t]) - 0.5f) < 1e-4f && fabsf(c[t]) < 16.0f);
-            }
-            if (border && s > 0.0f) {
-                #pragma unroll 1
-                for (int t = 0; t < 4; ++t) {
-                    const float v = t == 0 ? w[u][0] : t == 1 ? w[u][1] : t == 2 ? w[u][2] : w[u][3];
-                    const float d = (float)rint(((double)v - (double)b) / (double)s);
-                    if (t == 0) r[0] = d; else if (t == 1) r[1] = d; else if (t == 2) r[2] = d; else r[3] = d;
-                }
-            }
+        for (int u = 0; u < QPAIRS; ++u) {
+            const float2 e = group_extremes<LANES>(w[u], bad);
+            if (u == mine) ext = e;
+        }
+        const float mx = ext.x, mn = -ext.y;
+        const float range = AFFINE ? mx - mn : fmaxf(mx, ext.y);
+        float e = range * (AFFINE ? 1.0f / 15.0f : 1.0f / 7.0f);
+        if (near_half_border(e)) e = (float)(AFFINE ? ((double)mx - (double)mn) / 15.0 : (double)range / 7.0);
+        const __half sh = __float2half_rn(e);
+        const float s1 = __half2float(sh);
+        float b1 = 0.0f;
+        if (AFFINE) {
+            float f = fmaf(8.0f, s1, mn);
+            if (near_half_border(f)) f = (float)((double)mn + 8.0 * (double)s1);
+            b1 = __half2float(__float2half_rn(f));
+        }
+        const float inv1 = s1 > 0.0f ? __fdividef(1.0f, s1) : 0.0f;
+        // a group with NaN or Inf reports that, whatever other groups report
+        if (!(bad == 0.0f)) atomicExch(status, EXTERND_ENONFINITE);
+        else if (fmaxf(mx, ext.y) <= FLT_MAX && (isinf(s1) || isinf(b1))) atomicCAS(status, EXTERND_OK, EXTERND_ELIMIT);
+        #pragma unroll
+        for (int u = 0; u < QPAIRS; ++u) {
+            if (p0 + u >= pairs) break;
+            const int from = head + u * QUARTER;
+            const float s = __shfl_sync(FULL, s1, from), inv = __shfl_sync(FULL, inv1, from);
+            const float b = AFFINE ? __shfl_sync(FULL, b1, from) : 0.0f;
+            const int64_t j0 = (int64_t)(p0 + u) * 256 + 8 * lane;
             uint32_t code = 0;
+            float off = 0.0f;                               // distance from an integer, the largest of the eight
             #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int v = t < left ? (int)fminf(fmaxf(r[t], -8.0f), 7.0f) + 8 : 8;
-                code |= (uint32_t)v << (4 * (4 * (t & 1) + (t >> 1)));
+            for (int t = 0; t < 8; ++t) {
+                // c in -8 .. 7 plus 1.5 2^23 + 8: rounded to an integer, ties to even, whose low bits are the code.
+                // The error of c stays below 1e-5.
+                const float v = to_f32(w[u][t]);
+                const float c = fminf(fmaxf((AFFINE ? v - b : v) * inv, -8.0f), 7.0f);
+                const float k = c + 12582920.0f;
+                off = fmaxf(off, fabsf(c - (k - 12582920.0f)));
+                code |= (__float_as_uint(k) & 15u) << (4 * (4 * (t & 1) + (t >> 1)));
             }
-            if (lane & 1) code <<= 8;                              // t = 4..7 sit two nibbles above t = 0..3
-            code |= __shfl_xor_sync(FULL, code, 1);
-            if (!(lane & 1)) {
-                const int word = 4 * ((lane % 8) / 2) + lane / 8;   // 4 c + i
-                q[(row * blocks + blk) * 16 + word] = code;
+            if (off > 0.4999f || j0 + 8 > n) {
+                code = 0;
+                #pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    const double c = s > 0.0f ? rint(((double)to_f32(w[u][t]) - (double)b) / (double)s) : 0.0;
+                    const uint32_t d = j0 + t < n ? (uint32_t)((int)fmin(fmax(c, -8.0), 7.0) + 8) : 8u;
+                    code |= d << (4 * (4 * (t & 1) + (t >> 1)));
+                }
             }
-            if (left > 0 && ((4 * lane) & ((1 << lg) - 1)) == 0) {
-                const int64_t at = (j0 >> lg) * m + row;
-                scale[at] = __float2half_rn(s);
-                if (AFFINE) offset[at] = __float2half_rn(b);
+            if (2 * (p0 + u) + sub < blocks) qrow[(int64_t)(p0 + u) * 32] = code;
+        }
+        // the lane at the head of a pair's quarter stores its scale
+        if (lane % QUARTER == 0) {
+            const int64_t j = (int64_t)(p0 + mine) * 256 + 8 * head;
+            if (j < n) {
+                const int64_t at = (j >> LG) * m + row;
+                scale[at] = sh;
+                if (AFFINE) offset[at] = __float2half_rn(b1);
             }
         }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------
+// codes -> 16-bit floats
+// ---------------------------------------------------------------------------------------------------
+
+// (w & mask) | magic in one instruction (two immediates would make it two)
+__device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t mask, uint32_t magic) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
+    return d;
+}
+
+// the four pairs of codes of a word -> pairs of floats q - 8
+template <typename T> __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&a)[4]);
+template <> __device__ __forceinline__ void codes8<__half>(uint32_t w, uint32_t (&a)[4]) {
+    // 0x6400 | q = 1024 + q, 0x6400 | 16 q = 1024 + 16 q (exact); subtract 1032, or scale by 1/16 and subtract 72
+    const __half2 k1032 = __half2half2(__ushort_as_half(0x6408)), sixteenth = __half2half2(__ushort_as_half(0x2c00)),
+                  m72 = __half2half2(__ushort_as_half(0xd480));
+    const uint32_t w8 = w >> 8;
+    const uint32_t u0 = pick(w, 0x000f000fu, 0x64006400u), u1 = pick(w, 0x00f000f0u, 0x64006400u);
+    const uint32_t u2 = pick(w8, 0x000f000fu, 0x64006400u), u3 = pick(w8, 0x00f000f0u, 0x64006400u);
+    const __half2 v0 = __hsub2(*reinterpret_cast<const __half2*>(&u0), k1032);
+    const __half2 v1 = __hfma2(*reinterpret_cast<const __half2*>(&u1), sixteenth, m72);
+    const __half2 v2 = __hsub2(*reinterpret_cast<const __half2*>(&u2), k1032);
+    const __half2 v3 = __hfma2(*reinterpret_cast<const __half2*>(&u3), sixteenth, m72);
+    a[0] = *reinterpret_cast<const uint32_t*>(&v0);
+    a[1] = *reinterpret_cast<const uint32_t*>(&v1);
+    a[2] = *reinterpret_cast<const uint32_t*>(&v2);
+    a[3] = *reinterpret_cast<const uint32_t*>(&v3);
+}
+template <> __device__ __forceinline__ void codes8<__nv_bfloat16>(uint32_t w, uint32_t (&a)[4]) {
+    // 0x4300 | q = 128 + q; subtract 136
+    const __nv_bfloat162 k136 = __bfloat162bfloat162(__ushort_as_bfloat16(0x4308));
+    #pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t u = pick(w >> (4 * p), 0x000f000fu, 0x43004300u);
+        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), k136);
+        a[p] = *reinterpret_cast<const uint32_t*>(&v);
     }
 }
 
@@ -151,29 +229,47 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint32_t* __restr
     if (row >= m) return;
     const int blocks = (int)((n + 127) / 128);
     const uint32_t* const qrow = q + row * blocks * 16 + 4 * (l & 3) + (l >> 2);
-    #pragma unroll 2
-    for (int blk = 2 * blockIdx.y + (lane >> 4); blk < blocks; blk += 2 * gridDim.y) {
-        const int64_t j0 = (int64_t)blk * 128 + 8 * l;
-        if (j0 >= n) continue;
-        const uint32_t w = __ldg(qrow + (int64_t)blk * 16);
-        const int64_t at = (j0 >> lg) * m + row;
-        const float s = __half2float(__ldg(scale + at)), b = offset ? __half2float(__ldg(offset + at)) : 0.0f;
-        float v[8];
+    const int64_t jump = (256 >> lg) * m;               // a pair of blocks on in the scales
+    constexpr int UB = 4;                               // pairs of blocks in flight
+    for (int b0 = 2 * UB * blockIdx.y + (lane >> 4); b0 < blocks; b0 += 2 * UB * gridDim.y) {
+        uint32_t w[UB];
+        __half s[UB], b[UB];
+        const int64_t at = ((int64_t)b0 * 128 + 8 * l >> lg) * m + row;
         #pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] = fmaf(s, (float)((int)((w >> (4 * (4 * (t & 1) + (t >> 1)))) & 15u) - 8), b);
-        T* o = out + row * ldo + j0;
-        if (VEC && j0 + 8 <= n) {
-            if constexpr (sizeof(T) == 4) {
-                __stcs(reinterpret_cast<float4*>(o), make_float4(v[0], v[1], v[2], v[3]));
-                __stcs(reinterpret_cast<float4*>(o) + 1, make_float4(v[4], v[5], v[6], v[7]));
-            } else {
-                __stcs(reinterpret_cast<uint4*>(o), make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]),
-                                                               pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])));
-            }
-        } else {
+        for (int u = 0; u < UB; ++u) {
+            const bool in = (int64_t)(b0 + 2 * u) * 128 + 8 * l < n;
+            w[u] = in ? __ldg(qrow + (b0 + 2 * u) * 16ll) : 0;
+            s[u] = in ? __ldg(scale + at + u * jump) : __ushort_as_half(0);
+            b[u] = in && offset ? __ldg(offset + at + u * jump) : __ushort_as_half(0);
+        }
+        #pragma unroll
+        for (int u = 0; u < UB; ++u) {
+            const int64_t j0 = (int64_t)(b0 + 2 * u) * 128 + 8 * l;
+            if (j0 >= n) break;
+            const float sf = __half2float(s[u]), bf = __half2float(b[u]);
+            uint32_t c4[4];
+            codes8<__half>(w[u], c4);                    // q - 8, exactly
+            float v[8];
             #pragma unroll
-            for (int t = 0; t < 8; ++t)
-                if (j0 + t < n) o[t] = from_f32<T>(v[t]);
+            for (int t = 0; t < 4; ++t) {
+                const float2 f = unpack2<__half>(c4[t]);
+                v[2 * t] = fmaf(sf, f.x, bf);
+                v[2 * t + 1] = fmaf(sf, f.y, bf);
+            }
+            T* o = out + row * ldo + j0;
+            if (VEC && j0 + 8 <= n) {
+                if constexpr (sizeof(T) == 4) {
+                    __stcs(reinterpret_cast<float4*>(o), make_float4(v[0], v[1], v[2], v[3]));
+                    __stcs(reinterpret_cast<float4*>(o) + 1, make_float4(v[4], v[5], v[6], v[7]));
+                } else {
+                    __stcs(reinterpret_cast<uint4*>(o), make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]),
+                                                                   pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])));
+                }
+            } else {
+                #pragma unroll
+                for (int t = 0; t < 8; ++t)
+                    if (j0 + t < n) o[t] = from_f32<T>(v[t]);
+            }
         }
     }
 }
@@ -185,35 +281,6 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const uint32_t* __restr
 // Codes become exact 16-bit floats q - 8 two at a time, the tensor cores sum each group's products in fp32, and
 // the group's sum is scaled once.  fp32 vectors enter as three bf16 terms x = hi + mid + lo cut off from the
 // top (8 + 8 + 8 bits: no loss), three products into one sum.
-
-// a pair of codes -> a pair of floats q - 8; p = 0..3 selects the pair of the word
-template <typename T> __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&a)[4]);
-template <> __device__ __forceinline__ void codes8<__half>(uint32_t w, uint32_t (&a)[4]) {
-    // 0x6400 | q = 1024 + q, 0x6400 | 16 q = 1024 + 16 q (exact); subtract 1032, or scale by 1/16 and subtract 72
-    const __half2 k1032 = __half2half2(__ushort_as_half(0x6408)), sixteenth = __half2half2(__ushort_as_half(0x2c00)),
-                  m72 = __half2half2(__ushort_as_half(0xd480));
-    const uint32_t w8 = w >> 8;
-    const uint32_t u0 = (w & 0x000f000fu) | 0x64006400u, u1 = (w & 0x00f000f0u) | 0x64006400u;
-    const uint32_t u2 = (w8 & 0x000f000fu) | 0x64006400u, u3 = (w8 & 0x00f000f0u) | 0x64006400u;
-    const __half2 v0 = __hsub2(*reinterpret_cast<const __half2*>(&u0), k1032);
-    const __half2 v1 = __hfma2(*reinterpret_cast<const __half2*>(&u1), sixteenth, m72);
-    const __half2 v2 = __hsub2(*reinterpret_cast<const __half2*>(&u2), k1032);
-    const __half2 v3 = __hfma2(*reinterpret_cast<const __half2*>(&u3), sixteenth, m72);
-    a[0] = *reinterpret_cast<const uint32_t*>(&v0);
-    a[1] = *reinterpret_cast<const uint32_t*>(&v1);
-    a[2] = *reinterpret_cast<const uint32_t*>(&v2);
-    a[3] = *reinterpret_cast<const uint32_t*>(&v3);
-}
-template <> __device__ __forceinline__ void codes8<__nv_bfloat16>(uint32_t w, uint32_t (&a)[4]) {
-    // 0x4300 | q = 128 + q; subtract 136
-    const __nv_bfloat162 k136 = __bfloat162bfloat162(__ushort_as_bfloat16(0x4308));
-    #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const uint32_t u = ((w >> (4 * p)) & 0x000f000fu) | 0x43004300u;
-        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), k136);
-        a[p] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-}
 
 struct Mat4 {                       // one 4-bit matrix
     const uint8_t* q;
@@ -239,15 +306,16 @@ __device__ __forceinline__ void span_mma(float (&d)[4], const uint32_t (&a)[4], 
 // their sums in shared memory in a fixed order.  The warp-level products carry the arithmetic: a warp's 16 rows
 // by eight vectors in one instruction, straight from registers.  (The tile-level products read their operands
 // from shared memory: the codes would cross it as 16-bit floats, and of a tile's columns 16 at least.)
-// Every lane keeps the codes of its next DEPTH blocks in flight to shared memory (its own 16 bytes of two rows:
-// no barrier, no registers), and fetches the vectors' entries and the scales of the next block while it works
-// on one.  Bound by the weights' bytes; next by instructions, 72 of them a block and matrix to unpack codes.
+// Every lane keeps the codes of its next DEPTH blocks in flight to shared memory (its own 16 bytes of each row:
+// no barrier, no registers); the scales, whose way from memory is as long, come four blocks ahead through
+// registers; the vectors' entries come from the first-level cache.  Bound by instructions: 163 a block of 128
+// columns and 16 rows, 72 of them to unpack the codes.  8192 x 28672, one fp16 vector: 34 us, 3.5 TB/s (0.54 of
+// the measured copy rate).  Measured and not taken: bulk copies (a warp issues them one lane at a time: 271
+// instructions), the entries through the ring too (183), 32 rows a warp (the same time), 6 blocks ahead (slower).
 // The offsets' part b sum(x) takes sum(x) from the lanes that hold x (products with ones would occupy the
-// tensor cores as long as the codes do, and those are as busy as memory).
+// tensor cores as long as the codes do, and those are nearly as busy as memory).
 // X element type, T product type (bf16 for fp32 X), NM matrices, WORDS = group / 32.
-constexpr int VEC_WARPS = 8;
-template <int NM> __host__ __device__ constexpr int vec_depth() { return NM == 1 ? 6 : 4; }
-template <int NM> __host__ __device__ constexpr int vec_smem() { return VEC_WARPS * vec_depth<NM>() * NM * 1024; }
+constexpr int VEC_DEPTH = 4, VEC_WARPS = 8;
 
 __device__ __forceinline__ float sum8(const uint4& r, __half*) {
     const float2 a = unpack2<__half>(r.x), b = unpack2<__half>(r.y), c = unpack2<__half>(r.z), d = unpack2<__half>(r.w);
@@ -269,120 +337,106 @@ __global__ void __launch_bounds__(VEC_WARPS * 32) vec4_kernel(Mat4 w0, Mat4 w1, 
     constexpr int PLANES = Raw8<X>::PLANES;
     using XE = typename std::conditional<PLANES == 3, float, unsigned short>::type;
     constexpr int GROUPS = 4 / WORDS;                   // groups of a block
-    constexpr int DEPTH = vec_depth<NM>();
+    constexpr int FAR = 4;                              // blocks whose scales are fetched at a time
+    constexpr int KINDS = NM * (AFFINE ? 2 : 1), HALVES = FAR * GROUPS / 2;
     extern __shared__ __align__(16) unsigned char ring[];
-    __shared__ float part[NM][VEC_WARPS][16][9];
+    __shared__ __half side[VEC_WARPS][KINDS][FAR * GROUPS][16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane >> 2, c = lane & 3;
     const int64_t row0 = (int64_t)blockIdx.x * 16;
     const int blocks = (int)((n + 127) / 128), groups = (int)((n + 32 * WORDS - 1) / (32 * WORDS));
     const int whole = vec ? (int)(n / 128) : 0;         // blocks whose entries load 16 bytes at a time, unchecked
-    // rows past the last one repeat it (their sums are not stored)
-    const int64_t ra = min(row0 + r, m - 1), rb = min(row0 + r + 8, m - 1);
-    const int64_t down = rb - ra;
-    const Mat4 w[2] = {w0, w1};
 
-    // this lane's places: codes of its two rows, scales, entries of its vector
-    const uint8_t *qa[NM], *qb[NM];
-    const __half *ps[NM], *po[NM];
+    // this lane's codes: rows r and r + 8.  Rows past the last one repeat it (their sums are not stored)
+    const uint8_t* q[NM][2];
     #pragma unroll
-    for (int j = 0; j < NM; ++j) {
-        qa[j] = w[j].q + (ra * blocks + warp) * 64 + 16 * c;
-        qb[j] = w[j].q + (rb * blocks + warp) * 64 + 16 * c;
-        ps[j] = w[j].scale + (int64_t)warp * GROUPS * m + ra;
-        po[j] = AFFINE && w[j].offset ? w[j].offset + (int64_t)warp * GROUPS * m + ra : nullptr;
-    }
-    const XE* const xr = r < batch ? reinterpret_cast<const XE*>(x + r * ldx) : nullptr;
-
-    const uint32_t mine = smem_u32(ring) + (warp * DEPTH * NM * 2 * 32 + lane) * 16;  // slot, matrix, row half: 512 bytes apart
+    for (int j = 0; j < NM; ++j)
+        #pragma unroll
+        for (int h = 0; h < 2; ++h)
+            q[j][h] = (NM == 2 && j == 1 ? w1.q : w0.q) + (min(row0 + r + 8 * h, m - 1) * blocks + warp) * 64 + 16 * c;
+    const uint32_t mine = smem_u32(ring) + (warp * (VEC_DEPTH * NM * 2) * 32 + lane) * 16;     // 512 bytes a row half
     const auto issue = [&](bool on, uint32_t slot) {
         #pragma unroll
-        for (int j = 0; j < NM; ++j) {
-            if (on) {
-                const uint32_t dst = mine + slot * (NM * 1024) + j * 1024;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(qa[j]) : "memory");
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512), "l"(qb[j]) : "memory");
+        for (int j = 0; j < NM; ++j)
+            #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (on) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine + slot + (2 * j + h) * 512), "l"(q[j][h]) : "memory");
+                q[j][h] += VEC_WARPS * 64;
             }
-            qa[j] += VEC_WARPS * 64;
-            qb[j] += VEC_WARPS * 64;
-        }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    struct Side {                                        // what a block needs beside its codes
-        Raw x[4];
-        __half s[NM][GROUPS][2], o[AFFINE ? NM : 1][GROUPS][2];
-    };
-    const auto fetch = [&](Side& d, int blk) {
-        if (blk < blocks) {
-            if (blk < whole) {
-                if (xr) {
-                    const XE* const p = xr + blk * 128 + 8 * c;
-                    #pragma unroll
-                    for (int i = 0; i < 4; ++i) d.x[i] = *reinterpret_cast<const Raw*>(p + 32 * i);
-                }
-            } else {
-                #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const Raw v = xr ? load8(xr, (int64_t)blk * 128 + 32 * i + 8 * c, n, vec) : Raw{};
-                    if (i == 0) d.x[0] = v; else if (i == 1) d.x[1] = v; else if (i == 2) d.x[2] = v; else d.x[3] = v;
-                }
-            }
-            #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-                const bool in = GROUPS == 1 || blk * GROUPS + g < groups;   // past the last group: its entries are 0
-                #pragma unroll
-                for (int j = 0; j < NM; ++j) {
-                    d.s[j][g][0] = in ? __ldg(ps[j] + g * m) : __ushort_as_half(0);
-                    d.s[j][g][1] = in ? __ldg(ps[j] + g * m + down) : __ushort_as_half(0);
-                    if (AFFINE) {
-                        d.o[j][g][0] = in && po[j] ? __ldg(po[j] + g * m) : __ushort_as_half(0);
-                        d.o[j][g][1] = in && po[j] ? __ldg(po[j] + g * m + down) : __ushort_as_half(0);
-                    }
-                }
-            }
-        }
+    // scales (and offsets) of the warp's next FAR blocks: 16 rows, a lane two groups at a time, fetched while the
+    // FAR blocks before them are worked on and then laid down in the warp's own shared memory
+    __half ahead[KINDS][HALVES];
+    const int srow = lane & 15, sgroup = lane >> 4;
+    const auto fetch = [&](int blk0) {                   // blk0: the warp's first block of the FAR
         #pragma unroll
-        for (int j = 0; j < NM; ++j) {
-            ps[j] += VEC_WARPS * GROUPS * m;
-            if (AFFINE && po[j]) po[j] += VEC_WARPS * GROUPS * m;
+        for (int h = 0; h < HALVES; ++h) {
+            const int e = 2 * h + sgroup, g = (blk0 + e / GROUPS * VEC_WARPS) * GROUPS + e % GROUPS;
+            #pragma unroll
+            for (int k = 0; k < KINDS; ++k) {
+                const int j = k % NM;
+                const Mat4& w = NM == 2 && j == 1 ? w1 : w0;
+                const __half* const p = k < NM ? w.scale : w.offset;
+                const int64_t sr = min(row0 + srow, m - 1);
+                ahead[k][h] = p && g < groups ? __ldg(p + g * m + sr) : __ushort_as_half(0);   // past the last group: entries are 0
+            }
         }
     };
-
     #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) issue(warp + d * VEC_WARPS < blocks, d);
-    Side next;
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) next.x[i] = Raw{};
-    fetch(next, warp);
+    for (int d = 0; d < VEC_DEPTH; ++d) issue(warp + d * VEC_WARPS < blocks, d * (NM * 1024));
+    fetch(warp);
+    // columns of the products past the last vector repeat it (they are not stored)
+    const XE* const xr = reinterpret_cast<const XE*>(x + min(r, batch - 1) * ldx);
+    const XE* xp = xr + warp * 128 + 8 * c;
     float out[NM][4] = {};
     uint32_t slot = 0;
+    int step = 0;                                        // block within the FAR
     #pragma unroll 1
     for (int blk = warp; blk < blocks; blk += VEC_WARPS) {
-        const Side d = next;
-        fetch(next, blk + VEC_WARPS);
-        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-        uint4 a4[NM], b4[NM];
-        #pragma unroll
-        for (int j = 0; j < NM; ++j) {
-            const uint32_t src = mine + slot * (NM * 1024) + j * 1024;
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(a4[j].x), "=r"(a4[j].y), "=r"(a4[j].z), "=r"(a4[j].w) : "r"(src));
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(b4[j].x), "=r"(b4[j].y), "=r"(b4[j].z), "=r"(b4[j].w) : "r"(src + 512));
+        Raw xs[4];
+        if (blk < whole) {
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) xs[i] = *reinterpret_cast<const Raw*>(xp + 32 * i);
+        } else {
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) xs[i] = load8(xr, (int64_t)blk * 128 + 32 * i + 8 * c, n, vec);
         }
+        xp += VEC_WARPS * 128;
+        if (step == 0) {
+            __syncwarp();
+            #pragma unroll
+            for (int h = 0; h < HALVES; ++h)
+                #pragma unroll
+                for (int k = 0; k < KINDS; ++k) side[warp][k][2 * h + sgroup][srow] = ahead[k][h];
+            __syncwarp();
+            fetch(blk + FAR * VEC_WARPS);
+        }
+        const __half* const sp = &side[warp][0][step * GROUPS][r];
+        step = (step + 1) & (FAR - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(VEC_DEPTH - 1) : "memory");
+        uint4 code[NM][2];
+        #pragma unroll
+        for (int j = 0; j < NM; ++j)
+            #pragma unroll
+            for (int h = 0; h < 2; ++h)
+                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(code[j][h].x), "=r"(code[j][h].y), "=r"(code[j][h].z), "=r"(code[j][h].w)
+                             : "r"(mine + slot + (2 * j + h) * 512));
         float acc[NM][4] = {}, sum = 0.0f;
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t xv[PLANES][4];
-            planes8(d.x[i], xv);
+            planes8(xs[i], xv);
             #pragma unroll
             for (int j = 0; j < NM; ++j) {
                 uint32_t a[4], b[4];
-                codes8<T>(word_of(a4[j], i), a);
-                codes8<T>(word_of(b4[j], i), b);
+                codes8<T>(word_of(code[j][0], i), a);
+                codes8<T>(word_of(code[j][1], i), b);
                 span_mma<T, PLANES>(acc[j], a, b, xv);
             }
-            if (AFFINE) sum += sum8(d.x[i], (T*)nullptr);
+            if (AFFINE) sum += sum8(xs[i], (T*)nullptr);
             if ((i + 1) % WORDS == 0) {                  // the group ends here
-                const int g = i / WORDS;
+                const __half* const sg = sp + i / WORDS * 16;
                 float s0 = 0.0f, s1 = 0.0f;              // the group's sums of this lane's two output vectors, 2 c and 2 c + 1
                 if (AFFINE) {
                     sum += __shfl_xor_sync(FULL, sum, 1);
@@ -393,13 +447,13 @@ __global__ void __launch_bounds__(VEC_WARPS * 32) vec4_kernel(Mat4 w0, Mat4 w1, 
                 }
                 #pragma unroll
                 for (int j = 0; j < NM; ++j) {
-                    const float sa = __half2float(d.s[j][g][0]), sb = __half2float(d.s[j][g][1]);
+                    const float sa = __half2float(sg[j * FAR * GROUPS * 16]), sb = __half2float(sg[j * FAR * GROUPS * 16 + 8]);
                     out[j][0] = fmaf(sa, acc[j][0], out[j][0]);
                     out[j][1] = fmaf(sa, acc[j][1], out[j][1]);
                     out[j][2] = fmaf(sb, acc[j][2], out[j][2]);
                     out[j][3] = fmaf(sb, acc[j][3], out[j][3]);
                     if (AFFINE) {
-                        const float oa = __half2float(d.o[j][g][0]), ob = __half2float(d.o[j][g][1]);
+                        const float oa = __half2float(sg[(NM + j) * FAR * GROUPS * 16]), ob = __half2float(sg[(NM + j) * FAR * GROUPS * 16 + 8]);
                         out[j][0] = fmaf(oa, s0, out[j][0]);
                         out[j][1] = fmaf(oa, s1, out[j][1]);
                         out[j][2] = fmaf(ob, s0, out[j][2]);
@@ -410,17 +464,21 @@ __global__ void __launch_bounds__(VEC_WARPS * 32) vec4_kernel(Mat4 w0, Mat4 w1, 
                 }
             }
         }
-        issue(blk + DEPTH * VEC_WARPS < blocks, slot);   // the slot's codes have been used
-        slot = slot + 1 == DEPTH ? 0 : slot + 1;
+        issue(blk + VEC_DEPTH * VEC_WARPS < blocks, slot);   // the slot's codes have been used
+        slot = slot == (VEC_DEPTH - 1) * (NM * 1024) ? 0 : slot + NM * 1024;
     }
+    // the ring becomes the warps' sums
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    float* const part = reinterpret_cast<float*>(ring);  // [matrix][warp][row][9]
     #pragma unroll
     for (int j = 0; j < NM; ++j) {
-        part[j][warp][r][2 * c] = out[j][0];
-        part[j][warp][r][2 * c + 1] = out[j][1];
-        part[j][warp][r + 8][2 * c] = out[j][2];
-        part[j][warp][r + 8][2 * c + 1] = out[j][3];
+        float* const p = part + ((j * VEC_WARPS + warp) * 16 + r) * 9 + 2 * c;
+        p[0] = out[j][0];
+        p[1] = out[j][1];
+        p[72] = out[j][2];
+        p[73] = out[j][3];
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     const int e = threadIdx.x, rr = e & 15, cc = e >> 4;
     if (e < 128 && row0 + rr < m && cc < batch) {
@@ -428,7 +486,7 @@ __global__ void __launch_bounds__(VEC_WARPS * 32) vec4_kernel(Mat4 w0, Mat4 w1, 
         #pragma unroll
         for (int j = 0; j < NM; ++j)
             #pragma unroll
-            for (int p = 0; p < VEC_WARPS; ++p) v[j] += part[j][p][rr][cc];
+            for (int p = 0; p < VEC_WARPS; ++p) v[j] += part[((j * VEC_WARPS + p) * 16 + rr) * 9 + cc];
         const float res = NM == 1 ? v[0] : act_rt<PLANES == 3>(act, v[0]) * v[NM - 1];
         y[cc * ldy + row0 + rr] = from_f32<X>(res);
     }
@@ -463,7 +521,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
     using XE = typename std::conditional<PLANES == 3, float, unsigned short>::type;
     constexpr int GROUPS = 4 / WORDS, STAGES = tc_stages<X>(), STAGE = tc_stage<X, N>(), ROWS = 128 / NM;
     constexpr uint32_t COLUMNS = TC_BUFS * N * 2;           // tensor memory: products and sums (power of two, 128 .. 512)
-    static_assert(128 * (N + 1) * 4 <= STAGES * STAGE, "the tile of sums takes the stages' place");
+    static_assert(128 * N * 4 <= STAGES * STAGE, "the tile of sums takes the stages' place");
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t bars[2 * STAGES + 2 * TC_BUFS + 1];
     __shared__ uint32_t tmem_slot;
@@ -619,37 +677,51 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
         const int count = min(last * GROUPS, groups) - first * GROUPS, all = (last - first) * GROUPS;
         #pragma unroll
         for (int t = 0; t < N; ++t) out[t] = 0.0f;
-        __half s_next = count > 0 ? __ldg(ps) : __ushort_as_half(0), o_next = count > 0 && po ? __ldg(po) : __ushort_as_half(0);
-        for (int g = 0; g < all; ++g) {
-            const float s = __half2float(s_next), o = __half2float(o_next);
-            if (g + 1 < count) {
-                s_next = __ldg(ps += m);
-                if (AFFINE && po) o_next = __ldg(po += m);
-            } else {
-                s_next = o_next = __ushort_as_half(0);       // past the last group: its entries are 0
-            }
-            const int d = g % TC_BUFS;
-            if (!mbar_wait(dfull0 + 8 * d, (g / TC_BUFS) & 1, quit)) break;
-            fence_after();
-            const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16) + d * N;
-            constexpr int CH = N < 32 ? N : 32;
+        // scales and offsets come from memory while seven groups are worked on: one group takes a fraction of the way
+        constexpr int FAR = 8;
+        __half sr[FAR], orr[FAR];
+        #pragma unroll
+        for (int i = 0; i < FAR; ++i) {
+            sr[i] = i < count ? __ldg(ps + i * m) : __ushort_as_half(0);
+            orr[i] = AFFINE && po && i < count ? __ldg(po + i * m) : __ushort_as_half(0);
+        }
+        ps += FAR * m;
+        if (AFFINE && po) po += FAR * m;
+        bool ok = true;
+        for (int g0 = 0; g0 < all && ok; g0 += FAR) {
             #pragma unroll
-            for (int t = 0; t < N; t += CH) {
-                uint32_t v[CH];
-                if constexpr (CH == 32) tmem_ld32(at + t, v); else tmem_ld16(at + t, v);
-                tmem_wait_ld();
+            for (int i = 0; i < FAR; ++i) {
+                const int g = g0 + i;
+                if (g >= all) break;
+                const float s = __half2float(sr[i]), o = __half2float(orr[i]);
+                // past the last group the entries are 0
+                sr[i] = g + FAR < count ? __ldg(ps) : __ushort_as_half(0);
+                if (AFFINE) orr[i] = po && g + FAR < count ? __ldg(po) : __ushort_as_half(0);
+                ps += m;
+                if (AFFINE && po) po += m;
+                const int d = i % TC_BUFS;
+                if (!mbar_wait(dfull0 + 8 * d, (g / TC_BUFS) & 1, quit)) { ok = false; break; }
+                fence_after();
+                const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16) + d * N;
+                constexpr int CH = N < 32 ? N : 32;
                 #pragma unroll
-                for (int e = 0; e < CH; ++e) out[t + e] = fmaf(s, __uint_as_float(v[e]), out[t + e]);
-                if (AFFINE) {
-                    if constexpr (CH == 32) tmem_ld32(at + TC_BUFS * N + t, v); else tmem_ld16(at + TC_BUFS * N + t, v);
+                for (int t = 0; t < N; t += CH) {
+                    uint32_t v[CH];
+                    if constexpr (CH == 32) tmem_ld32(at + t, v); else tmem_ld16(at + t, v);
                     tmem_wait_ld();
                     #pragma unroll
-                    for (int e = 0; e < CH; ++e) out[t + e] = fmaf(o, __uint_as_float(v[e]), out[t + e]);
+                    for (int e = 0; e < CH; ++e) out[t + e] = fmaf(s, __uint_as_float(v[e]), out[t + e]);
+                    if (AFFINE) {
+                        if constexpr (CH == 32) tmem_ld32(at + TC_BUFS * N + t, v); else tmem_ld16(at + TC_BUFS * N + t, v);
+                        tmem_wait_ld();
+                        #pragma unroll
+                        for (int e = 0; e < CH; ++e) out[t + e] = fmaf(o, __uint_as_float(v[e]), out[t + e]);
+                    }
                 }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(dempty0 + 8 * d);
             }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(dempty0 + 8 * d);
         }
     }
     fence_before();
@@ -660,12 +732,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
     if (warp < TC_EPI) {
         const bool bad = *quit != 0;                         // a wait gave up: NaN rather than a wrong number
         #pragma unroll
-        for (int t = 0; t < N; ++t) red[(32 * warp + lane) * (N + 1) + t] = bad ? __uint_as_float(0x7fffffffu) : out[t];
+        for (int t = 0; t < N; ++t) red[t * 128 + 32 * warp + lane] = bad ? __uint_as_float(0x7fffffffu) : out[t];
     }
     if (warp == TC_EPI) tmem_free<1>(tmem, COLUMNS);
     if (splits > 1) cluster_sync();
     else __syncthreads();
-    // each CTA of the cluster adds and stores a share of the rows
+    // each CTA of the cluster adds and stores a share of the rows: neighbouring lanes, neighbouring rows, so that a
+    // warp's read of a peer is one piece
     const int r0 = ROWS * split / splits, share = ROWS * (split + 1) / splits - r0;
     for (int e = threadIdx.x; e < share * N; e += TC_THREADS) {
         const int rr = r0 + e % share, cc = e / share;
@@ -673,10 +746,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
         float v[NM] = {};
         #pragma unroll
         for (int j = 0; j < NM; ++j) {
-            const float* const p = red + (64 * j + rr) * (N + 1) + cc;
-            if (splits == 1) v[j] = *p;
-            else
-                for (int q = 0; q < splits; ++q) v[j] += ld_cluster(map_rank(smem_u32(p), q));
+            const float* const p = red + cc * 128 + 64 * j + rr;
+            float part[8];
+            #pragma unroll
+            for (int q = 0; q < 8; ++q) part[q] = q < splits ? ld_cluster(map_rank(smem_u32(p), q)) : 0.0f;
+            #pragma unroll
+            for (int q = 0; q < 8; ++q) v[j] += part[q];
         }
         const float res = NM == 1 ? v[0] : act_rt<PLANES == 3>(act, v[0]) * v[NM - 1];
         y[(col0 + cc) * ldy + row0 + rr] = from_f32<X>(res);
@@ -695,20 +770,21 @@ struct Product {
     cudaStream_t stream;
 };
 
-// dynamic shared memory beside at most 10 KB of static: what the 48 KB every kernel has does not hold
+// dynamic shared memory beside at most 32 KB of static: what the 48 KB every kernel has do not hold
 template <typename K>
 cudaError_t allow_smem(K kernel, int bytes) {
-    return bytes > 38 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) : cudaSuccess;
+    return bytes > 16 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) : cudaSuccess;
 }
 
 template <typename X, typename T, int NM, int WORDS, bool AFFINE>
 cudaError_t launch_vec4(const Product& p) {
     const auto kernel = vec4_kernel<X, T, NM, WORDS, AFFINE>;
-    const cudaError_t e = allow_smem(kernel, vec_smem<NM>());
+    constexpr int smem = VEC_WARPS * VEC_DEPTH * NM * 1024;
+    const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
     const bool vec = aligned(p.x, 16) && p.ldx * sizeof(X) % 16 == 0;
-    kernel<<<(unsigned)((p.m + 15) / 16), VEC_WARPS * 32, vec_smem<NM>(), p.stream>>>(p.w0, p.w1, p.m, p.n, p.act, (const X*)p.x, p.ldx,
-                                                                                    vec, (int)p.batch, (X*)p.y, p.ldy);
+    kernel<<<(unsigned)((p.m + 15) / 16), VEC_WARPS * 32, smem, p.stream>>>(p.w0, p.w1, p.m, p.n, p.act, (const X*)p.x, p.ldx, vec,
+                                                                           (int)p.batch, (X*)p.y, p.ldy);
     return cudaGetLastError();
 }
 
@@ -801,20 +877,33 @@ dim3 row_grid(int64_t m, int64_t steps) {
 
 int log2_of(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
 
-template <typename T, bool AFFINE>
+template <typename T, bool AFFINE, int LG>
+cudaError_t run_quantize(const void* A, int64_t m, int64_t n, int64_t lda, uint8_t* q, void* scale, void* offset, int* status,
+                         cudaStream_t s) {
+    const dim3 grid = row_grid(m, ((n + 255) / 256 + QPAIRS - 1) / QPAIRS);
+    const bool vec = aligned(A, 16) && lda * sizeof(T) % 16 == 0;
+    const auto kernel = vec ? quantize_kernel<T, AFFINE, true, LG> : quantize_kernel<T, AFFINE, false, LG>;
+    kernel<<<grid, 256, 0, s>>>((const T*)A, m, n, lda, (uint32_t*)q, (__half*)scale, (__half*)offset, status);
+    return cudaGetLastError();
+}
+
+template <typename T>
 cudaError_t run_quantize(const void* A, int64_t m, int64_t n, int64_t lda, int group, uint8_t* q, void* scale, void* offset,
                          int* status, cudaStream_t s) {
-    const dim3 grid = row_grid(m, ((n + 127) / 128 + QBLOCKS<T> - 1) / QBLOCKS<T>);
-    const bool vec = aligned(A, 4 * sizeof(T)) && lda % 4 == 0;
-    const auto kernel = vec ? quantize_kernel<T, AFFINE, true> : quantize_kernel<T, AFFINE, false>;
-    kernel<<<grid, 256, 0, s>>>((const T*)A, m, n, lda, log2_of(group), (uint32_t*)q, (__half*)scale, (__half*)offset, status);
-    return cudaGetLastError();
+    switch (log2_of(group) + (offset ? 8 : 0)) {
+        case 5: return run_quantize<T, false, 5>(A, m, n, lda, q, scale, offset, status, s);
+        case 6: return run_quantize<T, false, 6>(A, m, n, lda, q, scale, offset, status, s);
+        case 7: return run_quantize<T, false, 7>(A, m, n, lda, q, scale, offset, status, s);
+        case 13: return run_quantize<T, true, 5>(A, m, n, lda, q, scale, offset, status, s);
+        case 14: return run_quantize<T, true, 6>(A, m, n, lda, q, scale, offset, status, s);
+        default: return run_quantize<T, true, 7>(A, m, n, lda, q, scale, offset, status, s);
+    }
 }
 
 template <typename T>
 cudaError_t run_dequantize(const uint8_t* q, const void* scale, const void* offset, int64_t m, int64_t n, int group, void* out,
                            int64_t ldo, cudaStream_t s) {
-    const dim3 grid = row_grid(m, ((n + 127) / 128 + 1) / 2);
+    const dim3 grid = row_grid(m, ((n + 127) / 128 + 7) / 8);
     const bool vec = aligned(out, 16) && ldo * sizeof(T) % 16 == 0;
     const auto kernel = vec ? dequantize_kernel<T, true> : dequantize_kernel<T, false>;
     kernel<<<grid, 256, 0, s>>>((const uint32_t*)q, (const __half*)scale, (const __half*)offset, m, n, log2_of(group), (T*)out, ldo);
@@ -846,20 +935,10 @@ int externd_int4_quantize(const void* A, int dtype, int64_t m, int64_t n, int64_
     int rc = EXTERND_OK;
     cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int), s);
     if (e == cudaSuccess) {
-        const bool aff = offset_out != nullptr;
         switch (dtype) {
-            case EXTERND_F32:
-                e = aff ? run_quantize<float, true>(A, m, n, lda, group, q_out, scale_out, offset_out, status, s)
-                        : run_quantize<float, false>(A, m, n, lda, group, q_out, scale_out, offset_out, status, s);
-                break;
-            case EXTERND_F16:
-                e = aff ? run_quantize<__half, true>(A, m, n, lda, group, q_out, scale_out, offset_out, status, s)
-                        : run_quantize<__half, false>(A, m, n, lda, group, q_out, scale_out, offset_out, status, s);
-                break;
-            default:
-                e = aff ? run_quantize<__nv_bfloat16, true>(A, m, n, lda, group, q_out, scale_out, offset_out, status, s)
-                        : run_quantize<__nv_bfloat16, false>(A, m, n, lda, group, q_out, scale_out, offset_out, status, s);
-                break;
+            case EXTERND_F32: e = run_quantize<float>(A, m, n, lda, group, q_out, scale_out, offset_out, status, s); break;
+            case EXTERND_F16: e = run_quantize<__half>(A, m, n, lda, group, q_out, scale_out, offset_out, status, s); break;
+            default: e = run_quantize<__nv_bfloat16>(A, m, n, lda, group, q_out, scale_out, offset_out, status, s); break;
         }
     }
     if (e != cudaSuccess) { cudaGetLastError(); rc = EXTERND_ECUDA; }

@@ -170,15 +170,33 @@ __device__ __forceinline__ void split3(float x, uint32_t& hi, uint32_t& mid, uin
     lo = __float_as_uint(r2) >> 16;
 }
 
-// Eight consecutive 16-bit entries k .. k + 7 of a row (entries from n on are 0).  vec: rows start on 16-byte
-// boundaries.
+// Eight consecutive 16-bit entries k .. k + 7 (k a multiple of 8) of a row; entries from n on are 0.  vec: rows
+// start on 16-byte boundaries.  Otherwise, away from the row's ends, the two aligned 16-byte pieces that hold the
+// entries are shifted into place.
 __device__ __forceinline__ uint4 load8(const unsigned short* __restrict__ x, int64_t k, int64_t n, bool vec) {
-    if (vec && k + 8 <= n) return __ldg(reinterpret_cast<const uint4*>(x + k));
+    const unsigned short* const p = x + k;
+    if (vec && k + 8 <= n) return __ldg(reinterpret_cast<const uint4*>(p));
+    if (k >= 8 && k + 16 <= n) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        const uint32_t off = (uint32_t)(at & 15);                        // even
+        const uint4* const q = reinterpret_cast<const uint4*>(at - off);
+        const uint4 a = __ldg(q), b = __ldg(q + 1);
+        uint32_t w[5];                                                   // the five words from word off / 4 on
+        const uint32_t word = off >> 2;
+        w[0] = word == 0 ? a.x : word == 1 ? a.y : word == 2 ? a.z : a.w;
+        w[1] = word == 0 ? a.y : word == 1 ? a.z : word == 2 ? a.w : b.x;
+        w[2] = word == 0 ? a.z : word == 1 ? a.w : word == 2 ? b.x : b.y;
+        w[3] = word == 0 ? a.w : word == 1 ? b.x : word == 2 ? b.y : b.z;
+        w[4] = word == 0 ? b.x : word == 1 ? b.y : word == 2 ? b.z : b.w;
+        const uint32_t sh = (off & 2) * 8;
+        return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh), __funnelshift_r(w[2], w[3], sh),
+                          __funnelshift_r(w[3], w[4], sh));
+    }
     uint32_t v[4];
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t a = k + 2 * i < n ? __ldg(x + k + 2 * i) : 0;
-        const uint32_t b = k + 2 * i + 1 < n ? __ldg(x + k + 2 * i + 1) : 0;
+        const uint32_t a = k + 2 * i < n ? __ldg(p + 2 * i) : 0;
+        const uint32_t b = k + 2 * i + 1 < n ? __ldg(p + 2 * i + 1) : 0;
         v[i] = a | (b << 16);
     }
     return make_uint4(v[0], v[1], v[2], v[3]);
@@ -234,7 +252,7 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
 
