@@ -343,9 +343,9 @@ int externd_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const
  *   dX, dWg, dWu  [out] any of them may be NULL: it is then not computed.  The inputs are needed (and
  *                       checked) only for what is computed: X for dWg and dWu, Wg and Wu for dX.
  *   G, U, save_dtype, ldgu  as externd_gated returned them.
- *   work          [tmp] as for externd_gated, with externd_gated_backward_work(m, tokens) bytes besides.
+ *   work          [tmp] as for externd_gated, with externd_gated_backward_work(m, n, tokens) bytes besides.
  * tokens = 0 sets dWg and dWu to 0.  The same call gives the same bits (no atomics). */
-size_t externd_gated_backward_work(int64_t m, int64_t tokens);
+size_t externd_gated_backward_work(int64_t m, int64_t n, int64_t tokens);
 int externd_gated_backward(const void* dH, int64_t lddh, const void* X, int64_t ldx, const void* Wg, int64_t ldg,
                            const void* Wu, int64_t ldu, const void* G, const void* U, int save_dtype, int64_t ldgu,
                            int dtype, int64_t m, int64_t n, int64_t tokens, int act, void* dX, int64_t lddx, void* dWg,

@@ -186,7 +186,7 @@ def load():
     L.externd_gated.argtypes = [vp, i64, vp, i64, vp, i64, c_int, i64, i64, i64, c_int, vp, i64, vp, vp, c_int, i64, vp, sz, vp,
                                 vp]
     L.externd_gated.restype = c_int
-    L.externd_gated_backward_work.argtypes = [i64, i64]
+    L.externd_gated_backward_work.argtypes = [i64, i64, i64]
     L.externd_gated_backward_work.restype = sz
     L.externd_gated_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, c_int, i64, c_int, i64, i64, i64, c_int,
                                          vp, i64, vp, vp, i64, vp, sz, vp, vp]

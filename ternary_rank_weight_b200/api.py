@@ -871,7 +871,7 @@ def gated_backward(dH: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torc
         nbytes = 0
         if t and (need[0] or need[1] or need[2]):
             used = ([Wg, Wu] if need[0] else []) + ([X2] if need[1] or need[2] else [])
-            nbytes = 2 * ((t * ((m + 7) // 8 * 8) * 2 + 255) // 256 * 256) + _align_bytes(*used)
+            nbytes = _lib.load().externd_gated_backward_work(m, n, t) + _align_bytes(*used)
         work = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
         rc = _lib.load().externd_gated_backward(
             dH2.data_ptr(), _ld(dH2), X2.data_ptr(), _ld(X2), Wg.data_ptr(), _ld(Wg), Wu.data_ptr(), _ld(Wu), G2.data_ptr(),

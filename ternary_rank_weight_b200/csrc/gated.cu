@@ -46,6 +46,7 @@ struct TileList {
     int tiles_r, tiles_c;    // tile grid
     int rows, cols;          // outputs
     int blocks;              // stages of depth BK of a tile
+    int splits;              // shares of the depth, each a tile of its own
 };
 
 struct GemmArgs {
@@ -58,13 +59,19 @@ struct GemmArgs {
     void* h; int64_t ldh;    // FWD H, BWD dX
     void* s[2]; int64_t lds; // FWD G and U (or null), BWD dWg and dWu
     int save32;              // FWD: G and U in fp32 (otherwise in the operands' type)
+    float* part;             // BWD, main.splits > 1: the shares' sums (splits x tokens x ldp) instead of dX
+    int64_t ldp;
     int* status;             // may be null
 };
 
-struct Tile { bool grad; int r, c; };
+struct Tile { bool grad; int r, c, split, first, last; };    // stages first .. last - 1
 
 // tile t of a list: bands of 8 row tiles walked column by column, so the tiles in flight share operands in L2
 __device__ __forceinline__ void tile_at(int t, const TileList& l, Tile& o) {
+    o.split = t % l.splits;
+    t /= l.splits;
+    o.first = (int)((int64_t)l.blocks * o.split / l.splits);
+    o.last = (int)((int64_t)l.blocks * (o.split + 1) / l.splits);
     const int band = t / (8 * l.tiles_c), first = band * 8;
     const int h = min(8, l.tiles_r - first), in = t - band * 8 * l.tiles_c;
     o.c = in / h;
@@ -75,7 +82,7 @@ __device__ __forceinline__ void tile_at(int t, const TileList& l, Tile& o) {
 // workers that got one main tile more (the first `more`) sit out the first `skip`: dX tiles are longer than dW
 // tiles, and so all end at about the same time.
 __device__ __forceinline__ bool tile_of(const GemmArgs& g, int worker, int workers, int i, Tile& o) {
-    const int nm = g.main.tiles_r * g.main.tiles_c, ng = g.grad.tiles_r * g.grad.tiles_c;
+    const int nm = g.main.tiles_r * g.main.tiles_c * g.main.splits, ng = g.grad.tiles_r * g.grad.tiles_c;
     const int mine = nm > worker ? (nm - worker + workers - 1) / workers : 0;
     if (i < mine) {
         o.grad = false;
@@ -184,8 +191,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         bool ok = true;
         Tile t;
         for (int i = 0; ok && tile_of(g, worker, workers, i, t); ++i) {
-            const TileList& l = MODE == BWD && t.grad ? g.grad : g.main;
-            for (int kb = 0; kb < l.blocks; ++kb, ++it) {
+            for (int kb = t.first; kb < t.last; ++kb, ++it) {
                 const int s = it % C::STAGES;
                 if (!mbar_wait(empty0 + 8 * s, ((it / C::STAGES) & 1) ^ 1, quit)) { ok = false; break; }
                 const uint32_t sa = base + s * C::STAGE, sb = sa + 128 * BK * 2;
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
                 } else {
                     const int x = t.c * g.width + (int)(g.width / CG * rank);
                     if (!t.grad) {
-                        const int half = l.blocks / 2, which = kb >= half, k = (which ? kb - half : kb) * BK;
+                        const int half = g.main.blocks / 2, which = kb >= half, k = (which ? kb - half : kb) * BK;
                         tma_load<CG>(sa, &maps.a[which], k, t.r * C::BM + 128 * (int)rank, bar);
                         for (int i = 0; i < g.width / CG; i += 64) tma_load<CG>(sb + i * (BK * 2), &maps.b[which], x + i, k, bar);
                     } else {
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
             const bool a_mn = MODE == BWD && t.grad, b_mn = MODE == BWD;
             const uint32_t idesc = f16_idesc(fmt, a_mn, b_mn, C::BM, g.width);
             const uint32_t a_lbo = a_mn ? box : 16, b_lbo = b_mn ? box : 16, a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
-            const int kbs = MODE == BWD && t.grad ? g.grad.blocks : g.main.blocks;
+            const int kbs = t.last - t.first;
             const uint32_t acc = tmem + (n & 1) * ACC;
             if (!mbar_wait(tempty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, quit)) break;
             fence_after();
@@ -309,6 +315,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
                     uint32_t v[32], h[16];
                     tmem_ld32(acc + c, v);
                     tmem_wait_ld();
+                    if (!t.grad && g.part) {
+                        store32<float>(v, stg, stg_ptr, g.part + (int64_t)t.split * l.rows * g.ldp, g.ldp, row0, l.rows, col0, l.cols, lane);
+                        continue;
+                    }
                     pack_chunk<T>(v, h);
                     store32<T>(h, stg, stg_ptr, out, ld, row0, l.rows, col0, l.cols, lane);
                 }
@@ -382,6 +392,25 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const T* __restrict__ dh
             dg[r * ldw + c] = from_f32<T>(h * u * a.y);
             du[r * ldw + c] = from_f32<T>(h * a.x);
         }
+    }
+}
+
+// dX from the shares' sums, in their order
+template <typename T>
+__global__ void __launch_bounds__(256) add_shares_kernel(const float* __restrict__ part, int64_t ldp, int splits, int64_t rows, int64_t cols,
+                                                         T* __restrict__ out, int64_t ld) {
+    const int64_t per = ldp / 4;                             // ldp: cols rounded up to 8
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / per, c = 4 * (i - r * per);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int s = 0; s < splits; ++s) {
+            const float4 p = __ldg(reinterpret_cast<const float4*>(part + (s * rows + r) * ldp + c));
+            v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+        }
+        const float e[4] = {v.x, v.y, v.z, v.w};
+        #pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (c + t < cols) out[r * ld + c + t] = from_f32<T>(e[t]);
     }
 }
 
@@ -502,7 +531,7 @@ template <typename T, int MODE, int CG>
 cudaError_t launch_gemm(const Maps& maps, const GemmArgs& g, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(gemm_kernel<T, MODE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<CG>::SMEM);
     if (e != cudaSuccess) return e;
-    const int tiles = g.main.tiles_r * g.main.tiles_c + g.grad.tiles_r * g.grad.tiles_c, slots = sm_count() / CG;
+    const int tiles = g.main.tiles_r * g.main.tiles_c * g.main.splits + g.grad.tiles_r * g.grad.tiles_c, slots = sm_count() / CG;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((tiles < slots ? tiles : slots) * CG));
     cfg.blockDim = dim3(THREADS);
@@ -591,7 +620,8 @@ int forward_tiles(const Call& c, int width) {
         !make_map(&maps.b[1], c.W[1], c.m, c.n, c.ldw[1], width / 2, c.dtype))
         return EXTERND_ECUDA;
     GemmArgs g = {};
-    g.main = {ceil_div(c.tokens, Cfg<CG>::BM), ceil_div(c.m, width / 2), (int)c.tokens, (int)c.m, ceil_div(c.n, BK)};
+    g.main = {ceil_div(c.tokens, Cfg<CG>::BM), ceil_div(c.m, width / 2), (int)c.tokens, (int)c.m, ceil_div(c.n, BK), 1};
+    g.grad.splits = 1;
     g.width = width;
     g.act = c.act;
     g.h = c.H; g.ldh = c.ldh; g.s[0] = c.S[0]; g.s[1] = c.S[1]; g.lds = c.lds; g.save32 = c.save_dtype == EXTERND_F32;
@@ -599,17 +629,19 @@ int forward_tiles(const Call& c, int width) {
     return launch_gemm<T, FWD, CG>(maps, g, c.stream) == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
 }
 
-// Pairs of CTAs or single ones, and how wide the tiles: the fewest rounds times the width.  A single CTA of full
-// width takes 1.1 times a pair's time for its half of the pair's tile; narrower tiles lose a little to the operand
-// they share less (measured: 5 percent at 192 columns, 12 at 128).
+// Pairs of CTAs or single ones, and how wide the tiles: the fewest rounds, each weighted with its measured time.
+// Narrow tiles save little of it: shared memory writes and reads of both operands bound a round, and a narrower
+// tile still moves all of A.  4096 tokens x 6912 x 2560, us a round: pairs 14.3 / 13.2 / 12.1 at 256 / 192 / 128
+// columns, single CTAs 16.7 / 14.6 / 12.9.
 template <typename T>
 int forward_tiles(const Call& c) {
+    constexpr double ROUND[2][3] = {{1.20, 1.03, 0.91}, {1.00, 0.93, 0.85}};
     int best_cg = 1, best_width = 256;
     double best = 1e300;
     for (int cg = 1; cg <= 2; ++cg)
-        for (int width = 256; width >= 128; width -= 64) {
-            const double rounds = ceil_div((int64_t)ceil_div(c.tokens, 128 * cg) * ceil_div(c.m, width / 2), sm_count() / cg);
-            const double cost = rounds * width * (cg == 1 ? 1.1 : 1.0) * (width == 256 ? 1.0 : width == 192 ? 1.05 : 1.12);
+        for (int i = 0; i < 3; ++i) {
+            const int width = 256 - 64 * i;
+            const double cost = ceil_div((int64_t)ceil_div(c.tokens, 128 * cg) * ceil_div(c.m, width / 2), sm_count() / cg) * ROUND[cg - 1][i];
             if (cost < best) { best = cost; best_cg = cg; best_width = width; }
         }
     return best_cg == 1 ? forward_tiles<T, 1>(c, best_width) : forward_tiles<T, 2>(c, best_width);
@@ -661,19 +693,37 @@ cudaError_t gate_grad(const Call& c, T* dg, T* du, int64_t ldd) {
     return vec ? launch_gate_grad<T, S, true>(c, dg, du, ldd) : launch_gate_grad<T, S, false>(c, dg, du, ldd);
 }
 
+// Shares of the depth of dX's 2 m terms: with few tokens its tiles are few and long, and a tile is left to as many
+// workers as there are for each (64 tokens x 6912 x 2560: 88 us without).  For the widest tiles; narrower ones have
+// no fewer workers each.
+constexpr int MAX_SPLITS = 16;
+int dx_splits(int64_t m, int64_t n, int64_t tokens) {
+    const int64_t tiles = (int64_t)ceil_div(tokens, 128) * ceil_div(n, 256), most = ceil_div(m, BK) / 4;
+    int64_t s = sm_count() / tiles;
+    s = s < MAX_SPLITS ? s : MAX_SPLITS;
+    s = s < most ? s : most;
+    return s < 1 ? 1 : (int)s;
+}
+size_t share_bytes(int64_t m, int64_t n, int64_t tokens) {
+    const int s = dx_splits(m, n, tokens);
+    return s == 1 ? 0 : ((size_t)s * (size_t)tokens * (size_t)round8(n) * 4 + 255) / 256 * 256;
+}
+
 template <typename T, int CG>
-int backward_tiles(const Call& c, const T* dg, const T* du, int64_t ldd, int width) {
+int backward_tiles(const Call& c, const T* dg, const T* du, int64_t ldd, float* part, int splits, int width) {
     constexpr int BM = Cfg<CG>::BM;
     GemmArgs g = {};
     Maps maps = {};
     g.width = width;
     g.status = c.status;
+    g.main.splits = g.grad.splits = 1;
     if (c.dX) {
         if (!make_map(&maps.a[0], dg, c.tokens, c.m, ldd, 128, c.dtype) || !make_map(&maps.a[1], du, c.tokens, c.m, ldd, 128, c.dtype) ||
             !make_map(&maps.b[0], c.W[0], c.m, c.n, c.ldw[0], BK, c.dtype) || !make_map(&maps.b[1], c.W[1], c.m, c.n, c.ldw[1], BK, c.dtype))
             return EXTERND_ECUDA;
-        g.main = {ceil_div(c.tokens, BM), ceil_div(c.n, width), (int)c.tokens, (int)c.n, 2 * ceil_div(c.m, BK)};
+        g.main = {ceil_div(c.tokens, BM), ceil_div(c.n, width), (int)c.tokens, (int)c.n, 2 * ceil_div(c.m, BK), splits};
         g.h = c.dX; g.ldh = c.lddx;
+        if (splits > 1) { g.part = part; g.ldp = round8(c.n); }
     }
     if (c.dW[0] || c.dW[1]) {
         // the list holds the wanted matrices one after the other
@@ -685,9 +735,9 @@ int backward_tiles(const Call& c, const T* dg, const T* du, int64_t ldd, int wid
         }
         if (!make_map(&maps.x, c.X, c.tokens, c.n, c.ldx, BK, c.dtype)) return EXTERND_ECUDA;
         g.half_r = ceil_div(c.m, BM);
-        g.grad = {(c.dW[0] && c.dW[1] ? 2 : 1) * g.half_r, ceil_div(c.n, width), (int)c.m, (int)c.n, ceil_div(c.tokens, BK)};
+        g.grad = {(c.dW[0] && c.dW[1] ? 2 : 1) * g.half_r, ceil_div(c.n, width), (int)c.m, (int)c.n, ceil_div(c.tokens, BK), 1};
         g.lds = c.lddw;
-        g.skip = g.main.tiles_r ? (g.main.blocks + g.grad.blocks / 2) / g.grad.blocks : 0;
+        g.skip = g.main.tiles_r ? (g.main.blocks / splits + g.grad.blocks / 2) / g.grad.blocks : 0;
     }
     return launch_gemm<T, BWD, CG>(maps, g, c.stream) == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
 }
@@ -696,24 +746,34 @@ template <typename T>
 int backward(const Call& c) {
     const int64_t ldd = round8(c.m);
     const size_t plane = plane_bytes(c.tokens, c.m);
-    if (!c.work || c.work_bytes < 2 * plane) return EXTERND_EINVAL;
-    T* dg = (T*)c.work;
-    T* du = (T*)(c.work + plane);
+    const int splits = c.dX ? dx_splits(c.m, c.n, c.tokens) : 1;
+    if (!c.work || c.work_bytes < 2 * plane + share_bytes(c.m, c.n, c.tokens)) return EXTERND_EINVAL;
+    T* const dg = (T*)c.work;
+    T* const du = (T*)(c.work + plane);
+    float* const part = (float*)(c.work + 2 * plane);
     const cudaError_t e = c.save_dtype == EXTERND_F32 ? gate_grad<T, float>(c, dg, du, ldd) : gate_grad<T, T>(c, dg, du, ldd);
     if (e != cudaSuccess) return EXTERND_ECUDA;
-    // as for the forward pass, by the stages the busiest worker goes through
-    int best_cg = 1, best_width = 256;
+    // as for the forward pass: the stages the busiest worker goes through, weighted with a stage's measured time
+    // (4096 x 6912 x 2560, whole pass: pairs 478 us, single CTAs 560, half as wide 795 with twice the stages)
+    struct { int cg, width; double stage; } const shapes[3] = {{2, 256, 1.00}, {1, 256, 1.17}, {1, 128, 0.85}};
+    int best_i = 0;
     double best = 1e300;
-    for (int cg = 1; cg <= 2; ++cg)
-        for (int width = 256; width >= 128 * cg; width /= 2) {
-            const double workers = sm_count() / cg, cols = ceil_div(c.n, width);
-            const double nx = c.dX ? ceil_div(c.tokens, 128 * cg) * cols : 0, lx = 2 * ceil_div(c.m, BK);
-            const double nw = ((c.dW[0] ? 1 : 0) + (c.dW[1] ? 1 : 0)) * ceil_div(c.m, 128 * cg) * cols, lw = ceil_div(c.tokens, BK);
-            const double even = (nx * lx + nw * lw) / workers + (nw > 0 ? lw / 2 : 0), longest = ceil_div((int64_t)nx, (int64_t)workers) * lx;
-            const double cost = (even > longest ? even : longest) * width * (cg == 1 ? 1.1 : 1.0) * (width == 256 ? 1.0 : 1.12);
-            if (cost < best) { best = cost; best_cg = cg; best_width = width; }
-        }
-    return best_cg == 1 ? backward_tiles<T, 1>(c, dg, du, ldd, best_width) : backward_tiles<T, 2>(c, dg, du, ldd, best_width);
+    for (int i = 0; i < 3; ++i) {
+        const int cg = shapes[i].cg, workers = sm_count() / cg, cols = ceil_div(c.n, shapes[i].width);
+        const double nx = c.dX ? (double)ceil_div(c.tokens, 128 * cg) * cols * splits : 0, lx = 2.0 * ceil_div(c.m, BK) / splits;
+        const double nw = ((c.dW[0] ? 1.0 : 0.0) + (c.dW[1] ? 1.0 : 0.0)) * ceil_div(c.m, 128 * cg) * cols, lw = ceil_div(c.tokens, BK);
+        const double even = (nx * lx + nw * lw) / workers + (nw > 0 ? lw / 2 : 0), longest = ceil_div((int64_t)nx, workers) * lx;
+        const double cost = (even > longest ? even : longest) * shapes[i].stage;
+        if (cost < best) { best = cost; best_i = i; }
+    }
+    const int rc = best_i == 0   ? backward_tiles<T, 2>(c, dg, du, ldd, part, splits, 256)
+                   : best_i == 1 ? backward_tiles<T, 1>(c, dg, du, ldd, part, splits, 256)
+                                 : backward_tiles<T, 1>(c, dg, du, ldd, part, splits, 128);
+    if (rc != EXTERND_OK || splits == 1) return rc;
+    const int64_t items = c.tokens * (round8(c.n) / 4), cap = (int64_t)sm_count() * 16;
+    add_shares_kernel<T><<<(unsigned)((items + 255) / 256 < cap ? (items + 255) / 256 : cap), 256, 0, c.stream>>>(
+        part, round8(c.n), splits, c.tokens, c.n, (T*)c.dX, c.lddx);
+    return cudaGetLastError() == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
 }
 
 bool too_large(int64_t m, int64_t n, int64_t tokens) {
@@ -772,7 +832,9 @@ int externd_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const
     return rc;
 }
 
-size_t externd_gated_backward_work(int64_t m, int64_t tokens) { return m < 1 || tokens < 1 ? 0 : 2 * plane_bytes(tokens, m); }
+size_t externd_gated_backward_work(int64_t m, int64_t n, int64_t tokens) {
+    return m < 1 || n < 1 || tokens < 1 || too_large(m, n, tokens) ? 0 : 2 * plane_bytes(tokens, m) + share_bytes(m, n, tokens);
+}
 
 int externd_gated_backward(const void* dH, int64_t lddh, const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu,
                            int64_t ldu, const void* G, const void* U, int save_dtype, int64_t ldgu, int dtype, int64_t m, int64_t n,
@@ -795,7 +857,7 @@ int externd_gated_backward(const void* dH, int64_t lddh, const void* X, int64_t 
         if (dX && (!good(dev, dX, 2, lddx, n) || !good(dev, Wg, 2, ldg, n) || !good(dev, Wu, 2, ldu, n))) return EXTERND_EINVAL;
         if (dw && !good(dev, X, 2, ldx, n)) return EXTERND_EINVAL;
         if (too_large(m, n, tokens)) return EXTERND_ELIMIT;
-        size_t need = externd_gated_backward_work(m, tokens);
+        size_t need = externd_gated_backward_work(m, n, tokens);
         if (dX)
             for (int i = 0; i < 2; ++i) need += row_aligned(c.W[i], m, c.ldw[i]) ? 0 : plane_bytes(m, n);
         if (dw) need += row_aligned(X, tokens, ldx) ? 0 : plane_bytes(tokens, n);

@@ -295,7 +295,7 @@ def test_library_refuses_bad_arguments():
     X, Wg, Wu, dH = _make(t, m, n, BF16)
     H, G, Up = ext.gated_forward(X, Wg, Wu)
     out = [torch.zeros(s, dtype=BF16, device="cuda") for s in ((t, n), (m, n), (m, n))]
-    need = L.externd_gated_backward_work(m, t)
+    need = L.externd_gated_backward_work(m, n, t)
     work = torch.zeros(need + 3 * L.externd_gated_work(m, n), dtype=torch.uint8, device="cuda")
     host = torch.zeros(1 << 16, dtype=torch.uint8)
     st = torch.cuda.current_stream().cuda_stream

@@ -76,9 +76,11 @@ def test_gated_entry_points_reject_bad_arguments_before_device_work():
     assert L.externd_gated_backward(p, 1, p, 8, p, 8, p, 8, p, p, 0, 1, 2, 1, 1, 1, 0, p, 1, p, p, 1, p, 512, None, None) == EINVAL
     assert L.externd_gated_work(0, 5) == 0 and L.externd_gated_work(5, 0) == 0
     assert L.externd_gated_work(3, 9) == 256 and L.externd_gated_work(100, 9) == 3328
-    assert L.externd_gated_backward_work(0, 5) == 0 and L.externd_gated_backward_work(5, 0) == 0
-    assert L.externd_gated_backward_work(1000, 300) == 2 * ((300 * 1000 * 2 + 255) // 256 * 256)
-    assert L.externd_gated_backward_work(3, 1) == 512                       # rows of 8 elements, planes on 256 bytes
+    assert L.externd_gated_backward_work(0, 5, 5) == 0 and L.externd_gated_backward_work(5, 5, 0) == 0
+    # two planes of 8-element rows on 256 bytes; besides, with few tokens, shares of dX
+    assert L.externd_gated_backward_work(3, 3, 1) == 512
+    assert L.externd_gated_backward_work(1000, 2560, 4096) == 2 * 4096 * 1000 * 2
+    assert L.externd_gated_backward_work(6912, 2560, 64) > 2 * 64 * 6912 * 2
 
 
 def test_gated_binding_rejects_bad_tensors():
