@@ -27,9 +27,10 @@ using namespace externd_llm;
 enum Mode { FWD = 0, BWD = 1 };
 
 constexpr int BK = 64;                     // depth of one stage: 128 bytes, one swizzle span
-constexpr int THREADS = 256;               // warp 0 TMA, warp 1 MMA, warps 4-7 epilogue
+constexpr int EPI = 8;                     // epilogue warps: two for each quarter of the accumulator's rows
+constexpr int THREADS = 128 + 32 * EPI;    // warp 0 TMA, warp 1 MMA, warps 4-11 epilogue
 constexpr int ACC = 256;                   // accumulator columns; two accumulators fill tensor memory
-constexpr int STG_ROW = 144;               // bytes of a staged row of 32 fp32 outputs (128 + 16: no bank conflicts)
+constexpr int STG_ROW = 80;                // bytes of a staged row: 64 of outputs, 16 more against bank conflicts
 
 // CG = 2: a pair of CTAs works on one tile of 256 rows, each fetching its 128 rows of A and half of B, so that B
 // crosses shared memory once for two SMs.  4096 tokens through 6912 x 2560: forward 191 us against 208 with CG = 1.
@@ -38,7 +39,7 @@ template <int CG> struct Cfg {
     static constexpr int BBYTES = 256 / CG * BK * 2;       // a CTA's share of at most 256 B rows
     static constexpr int STAGE = 128 * BK * 2 + BBYTES;
     static constexpr int STAGES = CG == 1 ? 4 : 6;
-    static constexpr int SMEM = STAGES * STAGE + 4 * 32 * STG_ROW + 1024 + 256;
+    static constexpr int SMEM = STAGES * STAGE + EPI * 32 * STG_ROW + 1024 + 256;
 };
 
 // one list of output tiles
@@ -98,32 +99,31 @@ __device__ __forceinline__ bool tile_of(const GemmArgs& g, int worker, int worke
     return true;
 }
 
-// 32 columns of a warp's 32 rows (a row per lane, R registers) to global memory through the warp's staging
+// 64 bytes of each of a warp's 32 rows (a row per lane, 16 registers) to global memory through the warp's staging
 // buffer, so that neighbouring lanes write neighbouring 16 bytes
-template <typename T, int R>
-__device__ __forceinline__ void store32(const uint32_t (&v)[R], uint32_t stg, const unsigned char* stg_ptr, T* out, int64_t ld,
-                                        int row0, int rows, int col0, int cols, int lane) {
-    static_assert(R * 4 == 32 * sizeof(T), "a lane holds 32 outputs");
-    constexpr int Q = R / 4;                  // 16-byte pieces of a row
-    constexpr int E = 16 / sizeof(T);
+template <typename T>
+__device__ __forceinline__ void store64(const uint32_t* v, uint32_t stg, const unsigned char* stg_ptr, T* out, int64_t ld, int row0, int rows,
+                                        int col0, int cols, int lane) {
+    constexpr int E = 16 / sizeof(T);         // outputs of a 16-byte piece
     #pragma unroll
-    for (int i = 0; i < Q; ++i)
+    for (int i = 0; i < 4; ++i)
         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(stg + lane * STG_ROW + 16 * i), "r"(v[4 * i]), "r"(v[4 * i + 1]),
                      "r"(v[4 * i + 2]), "r"(v[4 * i + 3]) : "memory");
     __syncwarp();
-    const bool vec = col0 + 32 <= cols && ld % E == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    const bool vec = col0 + 4 * E <= cols && ld % E == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
     if (vec) {
         #pragma unroll
-        for (int i = 0; i < Q; ++i) {
-            const int r = (32 / Q) * i + lane / Q, c = lane % Q;
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2), c = lane & 3;
             const uint4 w = *reinterpret_cast<const uint4*>(stg_ptr + r * STG_ROW + 16 * c);
             if (row0 + r < rows) *reinterpret_cast<uint4*>(out + (int64_t)(row0 + r) * ld + col0 + E * c) = w;
         }
     } else {
         #pragma unroll 4
-        for (int r = 0; r < 32; ++r) {
-            const T w = *reinterpret_cast<const T*>(stg_ptr + r * STG_ROW + (int)sizeof(T) * lane);
-            if (row0 + r < rows && col0 + lane < cols) out[(int64_t)(row0 + r) * ld + col0 + lane] = w;
+        for (int r = 0; r < 32; r += 32 / (4 * E)) {
+            const int rr = 4 * E == 32 ? r : r + (lane >> 4), c = 4 * E == 32 ? lane : lane & 15;
+            const T w = *reinterpret_cast<const T*>(stg_ptr + rr * STG_ROW + (int)sizeof(T) * c);
+            if (row0 + rr < rows && col0 + c < cols) out[(int64_t)(row0 + rr) * ld + col0 + c] = w;
         }
     }
     __syncwarp();
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull0 + 8 * i, 1);
-            mbar_init(tempty0 + 8 * i, 4 * CG);                      // one arrival per epilogue warp of the pair
+            mbar_init(tempty0 + 8 * i, EPI * CG);                      // one arrival per epilogue warp of the pair
         }
         mbar_init(drain, 1);
         quit_flag = 0;
@@ -266,10 +266,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
             while (!mbar_try(drain, 0) && timer_ns() - t0 < WAIT_LIMIT_NS) {}
         }
     } else if (warp >= 4) {
-        // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31 of the accumulator, a row per thread
-        const int w = warp - 4;
-        const uint32_t stg = smem_u32(stg_base) + w * 32 * STG_ROW;
-        const unsigned char* stg_ptr = stg_base + w * 32 * STG_ROW;
+        // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31 of the accumulator, a row per thread, and every other
+        // 32 columns
+        const int w = warp & 3, turn = 32 * ((warp >> 2) - 1);
+        const uint32_t stg = smem_u32(stg_base) + (warp - 4) * 32 * STG_ROW;
+        const unsigned char* stg_ptr = stg_base + (warp - 4) * 32 * STG_ROW;
         Tile t;
         for (int n = 0; tile_of(g, worker, workers, n, t); ++n) {
             if (!mbar_wait(tfull0 + 8 * (n & 1), (n >> 1) & 1, quit)) break;
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
             if constexpr (MODE == FWD) {
                 const int row0 = t.r * C::BM + 128 * (int)rank + 32 * w, half = g.width / 2;
                 #pragma unroll 1
-                for (int c = 0; c < half; c += 32) {
+                for (int c = turn; c < half; c += 64) {
                     const int col0 = t.c * half + c;
                     if (col0 >= g.main.cols || row0 >= g.main.rows) break;     // the whole warp
                     uint32_t vg[32], vu[32], h[16];
@@ -291,15 +292,19 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
                         case EXTERND_ACT_GELU_TANH: gate_chunk<T, EXTERND_ACT_GELU_TANH>(vg, vu, h); break;
                         default: gate_chunk<T, EXTERND_ACT_RELU2>(vg, vu, h); break;
                     }
-                    store32<T>(h, stg, stg_ptr, (T*)g.h, g.ldh, row0, g.main.rows, col0, g.main.cols, lane);
+                    store64<T>(h, stg, stg_ptr, (T*)g.h, g.ldh, row0, g.main.rows, col0, g.main.cols, lane);
                     if (g.s[0] && g.save32) {
-                        store32<float>(vg, stg, stg_ptr, (float*)g.s[0], g.lds, row0, g.main.rows, col0, g.main.cols, lane);
-                        store32<float>(vu, stg, stg_ptr, (float*)g.s[1], g.lds, row0, g.main.rows, col0, g.main.cols, lane);
+                        #pragma unroll
+                        for (int e = 0; e < 32; e += 16) {
+                            if (col0 + e >= g.main.cols) break;
+                            store64<float>(vg + e, stg, stg_ptr, (float*)g.s[0], g.lds, row0, g.main.rows, col0 + e, g.main.cols, lane);
+                            store64<float>(vu + e, stg, stg_ptr, (float*)g.s[1], g.lds, row0, g.main.rows, col0 + e, g.main.cols, lane);
+                        }
                     } else if (g.s[0]) {
                         pack_chunk<T>(vg, h);
-                        store32<T>(h, stg, stg_ptr, (T*)g.s[0], g.lds, row0, g.main.rows, col0, g.main.cols, lane);
+                        store64<T>(h, stg, stg_ptr, (T*)g.s[0], g.lds, row0, g.main.rows, col0, g.main.cols, lane);
                         pack_chunk<T>(vu, h);
-                        store32<T>(h, stg, stg_ptr, (T*)g.s[1], g.lds, row0, g.main.rows, col0, g.main.cols, lane);
+                        store64<T>(h, stg, stg_ptr, (T*)g.s[1], g.lds, row0, g.main.rows, col0, g.main.cols, lane);
                     }
                 }
             } else {
@@ -309,18 +314,21 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
                 const int64_t ld = t.grad ? g.lds : g.ldh;
                 const int row0 = (t.r - (which ? g.half_r : 0)) * C::BM + 128 * (int)rank + 32 * w;
                 #pragma unroll 1
-                for (int c = 0; c < g.width; c += 32) {
+                for (int c = turn; c < g.width; c += 64) {
                     const int col0 = t.c * g.width + c;
                     if (col0 >= l.cols || row0 >= l.rows) break;
                     uint32_t v[32], h[16];
                     tmem_ld32(acc + c, v);
                     tmem_wait_ld();
                     if (!t.grad && g.part) {
-                        store32<float>(v, stg, stg_ptr, g.part + (int64_t)t.split * l.rows * g.ldp, g.ldp, row0, l.rows, col0, l.cols, lane);
+                        #pragma unroll
+                        for (int e = 0; e < 32; e += 16)
+                            if (col0 + e < l.cols)
+                                store64<float>(v + e, stg, stg_ptr, g.part + (int64_t)t.split * l.rows * g.ldp, g.ldp, row0, l.rows, col0 + e, l.cols, lane);
                         continue;
                     }
                     pack_chunk<T>(v, h);
-                    store32<T>(h, stg, stg_ptr, out, ld, row0, l.rows, col0, l.cols, lane);
+                    store64<T>(h, stg, stg_ptr, out, ld, row0, l.rows, col0, l.cols, lane);
                 }
             }
             fence_before();
@@ -755,13 +763,13 @@ int backward(const Call& c) {
     if (e != cudaSuccess) return EXTERND_ECUDA;
     // as for the forward pass: the stages the busiest worker goes through, weighted with a stage's measured time
     // (4096 x 6912 x 2560, whole pass: pairs 478 us, single CTAs 560, half as wide 795 with twice the stages)
-    struct { int cg, width; double stage; } const shapes[3] = {{2, 256, 1.00}, {1, 256, 1.17}, {1, 128, 0.85}};
+    struct { int cg, width; double stage; } const shapes[3] = {{2, 256, 1.00}, {1, 256, 1.20}, {1, 128, 0.85}};
     int best_i = 0;
     double best = 1e300;
     for (int i = 0; i < 3; ++i) {
         const int cg = shapes[i].cg, workers = sm_count() / cg, cols = ceil_div(c.n, shapes[i].width);
         const double nx = c.dX ? (double)ceil_div(c.tokens, 128 * cg) * cols * splits : 0, lx = 2.0 * ceil_div(c.m, BK) / splits;
-        const double nw = ((c.dW[0] ? 1.0 : 0.0) + (c.dW[1] ? 1.0 : 0.0)) * ceil_div(c.m, 128 * cg) * cols, lw = ceil_div(c.tokens, BK);
+        const double nw = ((c.dW[0] ? 1.0 : 0.0) + (c.dW[1] ? 1.0 : 0.0)) * ceil_div(c.m, 128 * cg) * cols, lw = ceil_div(c.tokens, BK) > 8 ? ceil_div(c.tokens, BK) : 8;   // storing a tile takes 8 stages' time
         const double even = (nx * lx + nw * lw) / workers + (nw > 0 ? lw / 2 : 0), longest = ceil_div((int64_t)nx, workers) * lx;
         const double cost = (even > longest ? even : longest) * shapes[i].stage;
         if (cost < best) { best = cost; best_i = i; }

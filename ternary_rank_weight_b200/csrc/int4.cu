@@ -497,15 +497,16 @@ __global__ void __launch_bounds__(VEC_WARPS * 32) vec4_kernel(Mat4 w0, Mat4 w1, 
 // A CTA takes 128 rows of one matrix (gated: 64 rows of both) and N = 16, 32 or 64 vectors on the 5th-generation
 // tensor cores; a cluster of up to 8 CTAs one such tile, each a share of its columns.  Eight warps turn codes
 // into 16-bit floats and stage them with the vectors' entries in swizzled shared memory, 128 columns a stage;
-// one thread issues the products, every group of columns into an accumulator of its own; four warps scale
-// each group's accumulator into fp32 registers, a row per thread, so that the row's scale is one register.
+// one thread issues the products, every group of columns into an accumulator of its own; eight warps scale
+// each group's accumulator into fp32 registers, a row and half of the vectors per thread, so that the row's scale
+// is one register.
 // The offsets' part comes from a second product of the same entries with ones, whose accumulator holds the
 // group's sum of x in every row.  The CTAs' sums meet through distributed shared memory in a fixed order.
 // (Weights scaled before the product would need no accumulator per group, but s (q - 8) + b does not fit 16
 // bits: measured against 64 bits that costs bf16 results 1.4 times the error of their own rounding.)
 // Bound by the codes' unpacking and staging at few vectors' worth of arithmetic a weight.
-constexpr int TC_EPI = 4, TC_PROD = 8, TC_THREADS = (TC_EPI + 1 + TC_PROD) * 32;
-constexpr int TC_BUFS = 4;                                // accumulators in flight
+constexpr int TC_EPI = 8, TC_PROD = 8, TC_THREADS = (TC_EPI + 1 + TC_PROD) * 32;
+template <int N> __host__ __device__ constexpr int tc_bufs() { return N == 64 ? 4 : 8; }     // accumulators in flight
 template <typename X> __host__ __device__ constexpr int tc_stages() { return Raw8<X>::PLANES == 3 ? 2 : 4; }
 template <typename X, int N> __host__ __device__ constexpr int tc_stage() { return 128 * 256 + Raw8<X>::PLANES * N * 256; }
 template <typename X, int N> __host__ __device__ constexpr int tc_smem() {
@@ -520,7 +521,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
     constexpr int PLANES = Raw8<X>::PLANES;
     using XE = typename std::conditional<PLANES == 3, float, unsigned short>::type;
     constexpr int GROUPS = 4 / WORDS, STAGES = tc_stages<X>(), STAGE = tc_stage<X, N>(), ROWS = 128 / NM;
-    constexpr uint32_t COLUMNS = TC_BUFS * N * 2;           // tensor memory: products and sums (power of two, 128 .. 512)
+    constexpr int TC_BUFS = tc_bufs<N>();
+    constexpr uint32_t COLUMNS = TC_BUFS * N * 2;           // tensor memory: products and sums (256 or 512 columns)
     static_assert(128 * N * 4 <= STAGES * STAGE, "the tile of sums takes the stages' place");
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t bars[2 * STAGES + 2 * TC_BUFS + 1];
@@ -563,120 +565,131 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
     fence_after();
     const uint32_t tmem = *(volatile uint32_t*)&tmem_slot;
 
-    float out[N];
+    constexpr int W = N / 2;                                 // vectors of a scaling warp
+    float out[W];
     if (warp > TC_EPI) {
         // ---- codes and entries into shared memory: thread p unpacks half of row p % 128, and a share of the entries
         const int p = threadIdx.x - (TC_EPI + 1) * 32, r = p & 127, h = p >> 7;
         const Mat4 w = NM == 2 && r >= 64 ? w1 : w0;
         const int64_t row = min(row0 + (NM == 2 ? r & 63 : r), m - 1);    // rows past the last one repeat it
-        const uint4* const src = reinterpret_cast<const uint4*>(w.q + row * blocks * 64) + 2 * h;
-        constexpr int PIECES = N * 16 / (TC_PROD * 32);      // pieces of 8 entries a thread
+        const uint4* src = reinterpret_cast<const uint4*>(w.q + (row * blocks + first) * 64) + 2 * h;
+        constexpr int PIECES = N * 16 / (TC_PROD * 32);      // pieces of 8 entries a thread: vectors col, col + 16, ..
         constexpr int AHEAD = PLANES == 3 ? 1 : 2;           // blocks in flight
+        const int whole = vec ? (int)(n / 128) : 0;          // blocks whose entries load 16 bytes at a time, unchecked
+        const int col = p >> 4, piece = p & 15;
         uint4 code[AHEAD][2];
         Raw ent[AHEAD][PIECES];
+        // vectors past the last one repeat it: their sums are not stored
         const XE* xp[PIECES];
         #pragma unroll
-        for (int e = 0; e < PIECES; ++e) {
-            const int64_t col = col0 + (p >> 4) + e * (TC_PROD * 2);
-            xp[e] = col < batch ? reinterpret_cast<const XE*>(x + col * ldx) : nullptr;
-        }
+        for (int e = 0; e < PIECES; ++e) xp[e] = reinterpret_cast<const XE*>(x + min(col0 + col + 16 * e, batch - 1) * ldx) + (int64_t)first * 128 + 8 * piece;
         const auto load = [&](int u, int blk) {
             if (blk >= last) return;
-            code[u][0] = __ldcs(src + (int64_t)blk * 4);
-            code[u][1] = __ldcs(src + (int64_t)blk * 4 + 1);
-            const int64_t k = (int64_t)blk * 128 + 8 * (p & 15);
-            #pragma unroll
-            for (int e = 0; e < PIECES; ++e) {
-                ent[u][e] = Raw{};
-                if (xp[e]) ent[u][e] = load8(xp[e], k, n, vec);
+            code[u][0] = __ldcs(src);
+            code[u][1] = __ldcs(src + 1);
+            src += 4;
+            if (blk < whole) {
+                #pragma unroll
+                for (int e = 0; e < PIECES; ++e) ent[u][e] = *reinterpret_cast<const Raw*>(xp[e]);
+            } else {
+                const int64_t k = (int64_t)blk * 128 + 8 * piece;
+                #pragma unroll
+                for (int e = 0; e < PIECES; ++e) ent[u][e] = load8(xp[e] - k, k, n, vec);
             }
+            #pragma unroll
+            for (int e = 0; e < PIECES; ++e) xp[e] += 128;
+        };
+        // places within a stage: columns 32 i + 8 c (c = 2 h, 2 h + 1) of the block are 16-byte chunk 4 (i % 2) + c of half
+        // i / 2, a row 128 bytes, chunks swizzled by the row; entries alike (vectors 16 apart share their swizzle)
+        const uint32_t place = r * 128 + (((2 * h) ^ (r & 7)) << 4), xplace = 128 * 256 + (piece >> 3) * (N * 128) + col * 128 + (((piece & 7) ^ (col & 7)) << 4);
+        const auto sts = [&](uint32_t at, const uint32_t (&v)[4]) {
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
         };
         #pragma unroll
         for (int u = 0; u < AHEAD; ++u) load(u, first + u);
-        int it = 0;
+        int s = 0, phase = 1;
         bool ok = true;
         for (int b0 = first; b0 < last && ok; b0 += AHEAD) {
             #pragma unroll
             for (int u = 0; u < AHEAD; ++u) {
                 const int blk = b0 + u;
                 if (blk >= last) break;
-                const int s = it % STAGES;
-                if (!mbar_wait(empty0 + 8 * s, ((it / STAGES) & 1) ^ 1, quit)) { ok = false; break; }
-                ++it;
-                unsigned char* const st = smem + s * STAGE;
+                if (!mbar_wait(empty0 + 8 * s, phase, quit)) { ok = false; break; }
+                const uint32_t st = base + s * STAGE, at = st + place;
                 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc)
+                for (int i = 0; i < 4; ++i)
                     #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        // columns 32 i + 8 c of the block: half i / 2, 16-byte chunk 4 (i % 2) + c, swizzled by the row
+                    for (int cc = 0; cc < 2; ++cc) {
                         uint32_t v[4];
                         codes8<T>(word_of(code[u][cc], i), v);
-                        const int chunk = 4 * (i & 1) + 2 * h + cc;
-                        *reinterpret_cast<uint4*>(st + (i >> 1) * (128 * 128) + r * 128 + ((chunk ^ (r & 7)) << 4)) =
-                            make_uint4(v[0], v[1], v[2], v[3]);
+                        sts(((at ^ (16u * cc)) ^ (64u * (i & 1))) + (i >> 1) * (128 * 128), v);
                     }
                 #pragma unroll
                 for (int e = 0; e < PIECES; ++e) {
-                    const int col = (p >> 4) + e * (TC_PROD * 2), piece = p & 15;
                     uint32_t v[PLANES][4];
                     planes8(ent[u][e], v);
                     #pragma unroll
-                    for (int q = 0; q < PLANES; ++q)
-                        *reinterpret_cast<uint4*>(st + 128 * 256 + q * N * 256 + (piece >> 3) * (N * 128) + col * 128 +
-                                                  (((piece & 7) ^ (col & 7)) << 4)) = make_uint4(v[q][0], v[q][1], v[q][2], v[q][3]);
+                    for (int q = 0; q < PLANES; ++q) sts(st + xplace + q * N * 256 + e * 2048, v[q]);
                 }
                 load(u, blk + AHEAD);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive_cluster(full0 + 8 * s);          // an address of this CTA is one of the cluster's
+                mbar_arrive(full0 + 8 * s);
+                if (++s == STAGES) { s = 0; phase ^= 1; }
             }
         }
     } else if (warp == TC_EPI) {
-        if (lane == 0) {
-            // ---- products
-            constexpr uint32_t idesc = f16_idesc(std::is_same<T, __half>::value ? 0 : 1, false, false, 128, N);
-            int it = 0, buf = 0;
-            bool ok = true;
-            for (int blk = first; blk < last && ok; ++blk, ++it) {
-                const int s = it % STAGES;
-                if (!mbar_wait(full0 + 8 * s, (it / STAGES) & 1, quit)) break;
+        // ---- products
+        const bool leader = elect_one();
+        constexpr uint32_t idesc = f16_idesc(std::is_same<T, __half>::value ? 0 : 1, false, false, 128, N);
+        const uint64_t a0 = smem_desc(base, 16, 1024), one = smem_desc(ones, 16, 1024);
+        int s = 0, phase = 0, d = 0, dphase = 1;
+        bool ok = true;
+        for (int blk = first; blk < last && ok; ++blk) {
+            if (!mbar_wait(full0 + 8 * s, phase, quit)) break;
+            fence_after();
+            const uint64_t da = a0 + (uint32_t)(s * (STAGE >> 4));   // the address field counts 16 bytes
+            #pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                if (!mbar_wait(dempty0 + 8 * d, dphase, quit)) { ok = false; break; }
                 fence_after();
-                const uint32_t sa = base + s * STAGE, sb = sa + 128 * 256;
-                const uint64_t one = smem_desc(ones, 16, 1024);
-                for (int g = 0; g < GROUPS; ++g, ++buf) {
-                    const int d = buf % TC_BUFS;
-                    if (!mbar_wait(dempty0 + 8 * d, ((buf / TC_BUFS) & 1) ^ 1, quit)) { ok = false; break; }
-                    fence_after();
+                const uint32_t acc = tmem + d * N;
+                if (leader) {
                     #pragma unroll
                     for (int k = 0; k < 2 * WORDS; ++k) {
                         const int kk = g * 2 * WORDS + k;    // 16 columns of the block: half kk / 4, 32 bytes each
-                        const uint64_t da = smem_desc(sa + (kk >> 2) * (128 * 128) + (kk & 3) * 32, 16, 1024);
                         #pragma unroll
                         for (int q = PLANES - 1; q >= 0; --q) {
-                            const uint64_t db = smem_desc(sb + q * N * 256 + (kk >> 2) * (N * 128) + (kk & 3) * 32, 16, 1024);
+                            const uint64_t db = da + ((128 * 256 + q * N * 256 + (kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4);
                             const bool more = k > 0 || q < PLANES - 1;
-                            mma_f16<1>(tmem + d * N, da, db, idesc, more);
-                            if (AFFINE) mma_f16<1>(tmem + (TC_BUFS + d) * N, one, db, idesc, more);
+                            mma_f16<1>(acc, da + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4), db, idesc, more);
+                            if (AFFINE) mma_f16<1>(acc + TC_BUFS * N, one, db, idesc, more);
                         }
                     }
                     mma_commit<1>(dfull0 + 8 * d);
+                    if (g == GROUPS - 1) mma_commit<1>(empty0 + 8 * s);
                 }
-                mma_commit<1>(empty0 + 8 * s);
+                __syncwarp();
+                if (++d == TC_BUFS) { d = 0; dphase ^= 1; }
             }
-            // the tensor memory is freed and the stages reused only when everything issued has ended
+            if (++s == STAGES) { s = 0; phase ^= 1; }
+        }
+        // the tensor memory is freed and the stages reused only when everything issued has ended
+        if (leader) {
             mma_commit<1>(drain);
             const uint64_t t0 = timer_ns();
             while (!mbar_try(drain, 0) && timer_ns() - t0 < WAIT_LIMIT_NS) {}
         }
+        __syncwarp();
     } else {
-        // ---- scaling: warp w holds rows 32 w .. 32 w + 31 of the tile
-        const int r = 32 * warp + lane;
+        // ---- scaling: warp w holds rows 32 (w % 4) .. + 31 of the tile and half w / 4 of the vectors
+        const int r = 32 * (warp & 3) + lane;
         const Mat4 w = NM == 2 && r >= 64 ? w1 : w0;
         const int64_t row = min(row0 + (NM == 2 ? r & 63 : r), m - 1);
         const __half* ps = w.scale + (int64_t)first * GROUPS * m + row;
         const __half* po = AFFINE && w.offset ? w.offset + (int64_t)first * GROUPS * m + row : nullptr;
         const int count = min(last * GROUPS, groups) - first * GROUPS, all = (last - first) * GROUPS;
         #pragma unroll
-        for (int t = 0; t < N; ++t) out[t] = 0.0f;
+        for (int t = 0; t < W; ++t) out[t] = 0.0f;
         // scales and offsets come from memory while seven groups are worked on: one group takes a fraction of the way
         constexpr int FAR = 8;
         __half sr[FAR], orr[FAR];
@@ -702,25 +715,22 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
                 const int d = i % TC_BUFS;
                 if (!mbar_wait(dfull0 + 8 * d, (g / TC_BUFS) & 1, quit)) { ok = false; break; }
                 fence_after();
-                const uint32_t at = tmem + ((uint32_t)(32 * warp) << 16) + d * N;
-                constexpr int CH = N < 32 ? N : 32;
+                const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + d * N + (warp >> 2) * W;
+                uint32_t v[W], x1[W];
+                if constexpr (W == 32) tmem_ld32(at, v); else if constexpr (W == 16) tmem_ld16(at, v); else tmem_ld8(at, v);
+                if constexpr (AFFINE) {
+                    const uint32_t ax = at + TC_BUFS * N;
+                    if constexpr (W == 32) tmem_ld32(ax, x1); else if constexpr (W == 16) tmem_ld16(ax, x1); else tmem_ld8(ax, x1);
+                }
+                tmem_wait_ld();
                 #pragma unroll
-                for (int t = 0; t < N; t += CH) {
-                    uint32_t v[CH];
-                    if constexpr (CH == 32) tmem_ld32(at + t, v); else tmem_ld16(at + t, v);
-                    tmem_wait_ld();
-                    #pragma unroll
-                    for (int e = 0; e < CH; ++e) out[t + e] = fmaf(s, __uint_as_float(v[e]), out[t + e]);
-                    if (AFFINE) {
-                        if constexpr (CH == 32) tmem_ld32(at + TC_BUFS * N + t, v); else tmem_ld16(at + TC_BUFS * N + t, v);
-                        tmem_wait_ld();
-                        #pragma unroll
-                        for (int e = 0; e < CH; ++e) out[t + e] = fmaf(o, __uint_as_float(v[e]), out[t + e]);
-                    }
+                for (int e = 0; e < W; ++e) {
+                    out[e] = fmaf(s, __uint_as_float(v[e]), out[e]);
+                    if constexpr (AFFINE) out[e] = fmaf(o, __uint_as_float(x1[e]), out[e]);
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(dempty0 + 8 * d);
+                if (lane == 0) mbar_arrive(dempty0 + 8 * d);
             }
         }
     }
@@ -732,29 +742,35 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
     if (warp < TC_EPI) {
         const bool bad = *quit != 0;                         // a wait gave up: NaN rather than a wrong number
         #pragma unroll
-        for (int t = 0; t < N; ++t) red[t * 128 + 32 * warp + lane] = bad ? __uint_as_float(0x7fffffffu) : out[t];
+        for (int t = 0; t < W; ++t) red[((warp >> 2) * W + t) * 128 + 32 * (warp & 3) + lane] = bad ? __uint_as_float(0x7fffffffu) : out[t];
     }
     if (warp == TC_EPI) tmem_free<1>(tmem, COLUMNS);
     if (splits > 1) cluster_sync();
     else __syncthreads();
-    // each CTA of the cluster adds and stores a share of the rows: neighbouring lanes, neighbouring rows, so that a
-    // warp's read of a peer is one piece
-    const int r0 = ROWS * split / splits, share = ROWS * (split + 1) / splits - r0;
+    // each CTA of the cluster adds and stores a share of the rows, four at a time: neighbouring lanes, neighbouring rows,
+    // so that a warp's read of a peer is one piece
+    const int q0 = ROWS / 4 * split / splits, share = ROWS / 4 * (split + 1) / splits - q0;
     for (int e = threadIdx.x; e < share * N; e += TC_THREADS) {
-        const int rr = r0 + e % share, cc = e / share;
+        const int cc = e / share, rr = 4 * (q0 + e - cc * share);
         if (row0 + rr >= m || col0 + cc >= batch) continue;
-        float v[NM] = {};
+        float v[NM][4] = {};
         #pragma unroll
         for (int j = 0; j < NM; ++j) {
-            const float* const p = red + cc * 128 + 64 * j + rr;
-            float part[8];
+            const uint32_t at = smem_u32(red + cc * 128 + 64 * j + rr);
+            float4 part[8];
             #pragma unroll
-            for (int q = 0; q < 8; ++q) part[q] = q < splits ? ld_cluster(map_rank(smem_u32(p), q)) : 0.0f;
+            for (int q = 0; q < 8; ++q) part[q] = q < splits ? ld_cluster4(map_rank(at, q)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             #pragma unroll
-            for (int q = 0; q < 8; ++q) v[j] += part[q];
+            for (int q = 0; q < 8; ++q) {
+                v[j][0] += part[q].x; v[j][1] += part[q].y; v[j][2] += part[q].z; v[j][3] += part[q].w;
+            }
         }
-        const float res = NM == 1 ? v[0] : act_rt<PLANES == 3>(act, v[0]) * v[NM - 1];
-        y[(col0 + cc) * ldy + row0 + rr] = from_f32<X>(res);
+        X* const o = y + (col0 + cc) * ldy + row0 + rr;
+        #pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float res = NM == 1 ? v[0][t] : act_rt<PLANES == 3>(act, v[0][t]) * v[NM - 1][t];
+            if (row0 + rr + t < m) o[t] = from_f32<X>(res);
+        }
     }
     if (splits > 1) cluster_sync();                          // peers may still read this CTA's sums
 }
@@ -797,11 +813,11 @@ cudaError_t launch_tile4(const Product& p) {
     const bool vec = aligned(p.x, 16) && p.ldx * sizeof(X) % 16 == 0;
     const int64_t tiles = (p.m + 128 / NM - 1) / (128 / NM), cols = (p.batch + N - 1) / N, blocks = (p.n + 127) / 128;
     // shares of the columns: the fewest rounds of CTAs times the blocks of a share, each CTA costing about
-    // three blocks' time to start, fill its stages and add up
+    // nine blocks' time (of 0.8 us) to start, fill its stages and add up
     int splits = 1;
     int64_t best = INT64_MAX;
     for (int c = 1; c <= 8 && c <= blocks; ++c) {
-        const int64_t cost = (tiles * cols * c + sm_count() - 1) / sm_count() * ((blocks + c - 1) / c + 3);
+        const int64_t cost = (tiles * cols * c + sm_count() - 1) / sm_count() * ((blocks + c - 1) / c + 9);
         if (cost < best) { best = cost; splits = c; }
     }
     cudaLaunchConfig_t cfg = {};
