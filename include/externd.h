@@ -281,6 +281,11 @@ typedef enum {
     EXTERND_ACT_RELU2 = 3
 } externd_act;
 
+/* Bytes of workspace for one operand (rows x n of type dtype) whose rows do not all start on 16-byte boundaries
+ * (pointer 16-byte aligned, and leading dimension times element size a multiple of 16, or one row): the products
+ * below copy such operands into `work` first where they need to. */
+size_t externd_aligned_bytes(int dtype, int64_t rows, int64_t n);
+
 /* Bytes of one row of n 4-bit codes: 64 ceil(n / 128).  0 for n < 1. */
 size_t externd_int4_row_bytes(int64_t n);
 
@@ -308,15 +313,20 @@ int externd_int4_dequantize(const uint8_t* q, const void* scale, const void* off
  * does nothing).  q as externd_int4_quantize lays it out, 16-byte aligned; offset NULL: b = 0.
  * The codes enter the products exactly and each group's sum is scaled in fp32; fp32 inputs are
  * split without loss.  |X| up to 2^115: beyond that, and for infinite entries, a sum may become
- * inf or NaN before it is scaled.  Rows of X do not influence one another. */
+ * inf or NaN before it is scaled.  Rows of X do not influence one another.
+ *   work       [tmp] NULL (work_bytes 0) for a batch of at most 8, or where the rows of X start on 16-byte
+ *                    boundaries; otherwise 256-byte aligned, externd_aligned_bytes(dtype, batch, n) bytes, owned
+ *                    by the caller. */
 int externd_int4_matvec(const uint8_t* q, const void* scale, const void* offset, int64_t m, int64_t n, int group,
-                        const void* X, int dtype, int64_t ldx, int64_t batch, void* Y, int64_t ldy, void* stream);
+                        const void* X, int dtype, int64_t ldx, int64_t batch, void* Y, int64_t ldy, void* work, size_t work_bytes,
+                        void* stream);
 
 /* H = act(X Wg^T) * (X Wu^T), elementwise product, both matrices m x n in 4 bits with one group
  * size; otherwise as externd_int4_matvec. */
 int externd_int4_gated(const uint8_t* qg, const void* scale_g, const void* offset_g, const uint8_t* qu,
                        const void* scale_u, const void* offset_u, int64_t m, int64_t n, int group, int act,
-                       const void* X, int dtype, int64_t ldx, int64_t batch, void* H, int64_t ldh, void* stream);
+                       const void* X, int dtype, int64_t ldx, int64_t batch, void* H, int64_t ldh, void* work, size_t work_bytes,
+                       void* stream);
 
 /* The gated feed-forward block with dense fp16 or bf16 weights (m x n, as a model stores its gate and up
  * projections): H = act(G) * U, G = X Wg^T, U = X Wu^T, for X tokens x n.  fp32 sums, one rounding of each
@@ -326,13 +336,11 @@ int externd_int4_gated(const uint8_t* qg, const void* scale_g, const void* offse
  *                    externd_gated_backward needs, of type save_dtype: EXTERND_F32, or dtype.  (16-bit ones
  *                    halve the memory held for the backward pass and add their rounding to its results.)
  *   work       [tmp] 256-byte aligned, owned by the caller; NULL (work_bytes 0) where the rows of X, Wg and
- *                    Wu start on 16-byte boundaries (pointer 16-byte aligned, leading dimension a multiple
- *                    of 8, or one row).  Otherwise externd_gated_work(rows, n) bytes for each of the three
- *                    that does not: it is copied there first.
+ *                    Wu start on 16-byte boundaries, otherwise externd_aligned_bytes(dtype, rows, n) bytes for
+ *                    each of the three whose rows do not.
  *   async_status  NULL, or a device int that receives EXTERND_OK, or EXTERND_ETIMEOUT if a device-side
  *                    wait gave up (2 s; the outputs are then unspecified), when the stream gets there.
  * tokens = 0 computes nothing. */
-size_t externd_gated_work(int64_t rows, int64_t n);
 int externd_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu, int dtype,
                   int64_t m, int64_t n, int64_t tokens, int act, void* H, int64_t ldh, void* G, void* U, int save_dtype,
                   int64_t ldgu, void* work, size_t work_bytes, int* async_status, void* stream);

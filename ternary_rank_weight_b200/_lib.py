@@ -37,7 +37,7 @@ EXPORTS = (
     "externd_int4_matvec",
     "externd_int4_gated",
     "externd_gated",
-    "externd_gated_work",
+    "externd_aligned_bytes",
     "externd_gated_backward_work",
     "externd_gated_backward",
 )
@@ -176,13 +176,14 @@ def load():
     L.externd_int4_quantize.restype = c_int
     L.externd_int4_dequantize.argtypes = [vp, vp, vp, i64, i64, c_int, vp, c_int, i64, vp]
     L.externd_int4_dequantize.restype = c_int
-    L.externd_int4_matvec.argtypes = [vp, vp, vp, i64, i64, c_int, vp, c_int, i64, i64, vp, i64, vp]
+    L.externd_int4_matvec.argtypes = [vp, vp, vp, i64, i64, c_int, vp, c_int, i64, i64, vp, i64, vp, ctypes.c_size_t, vp]
     L.externd_int4_matvec.restype = c_int
-    L.externd_int4_gated.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, c_int, c_int, vp, c_int, i64, i64, vp, i64, vp]
+    L.externd_int4_gated.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, c_int, c_int, vp, c_int, i64, i64, vp, i64, vp,
+                                     ctypes.c_size_t, vp]
     L.externd_int4_gated.restype = c_int
     sz = ctypes.c_size_t
-    L.externd_gated_work.argtypes = [i64, i64]
-    L.externd_gated_work.restype = sz
+    L.externd_aligned_bytes.argtypes = [c_int, i64, i64]
+    L.externd_aligned_bytes.restype = sz
     L.externd_gated.argtypes = [vp, i64, vp, i64, vp, i64, c_int, i64, i64, i64, c_int, vp, i64, vp, vp, c_int, i64, vp, sz, vp,
                                 vp]
     L.externd_gated.restype = c_int

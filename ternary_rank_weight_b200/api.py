@@ -607,6 +607,17 @@ def _result(out, rows: int, cols: int, like: torch.Tensor) -> torch.Tensor:
     return out
 
 
+def _align_bytes(*tensors) -> int:
+    """Workspace for the operands whose rows do not start on 16-byte boundaries (externd_aligned_bytes each)."""
+    total = 0
+    for t in tensors:
+        rows, cols = t.shape
+        size = t.element_size()
+        if t.data_ptr() % 16 or (rows > 1 and t.stride(0) * size % 16):
+            total += (rows * ((cols * size + 15) // 16 * 16) + 255) // 256 * 256
+    return total
+
+
 def _act(act: str) -> int:
     if act not in ACTS:
         raise ValueError(f"act must be one of {', '.join(ACTS)}")
@@ -721,7 +732,9 @@ def _int4_products(ws, X, act: int, out, stream) -> torch.Tensor:
             out = out.unsqueeze(0)
         batch = X2.shape[0]
         Y = _result(out, batch, w.m, X2)
-        tail = (X2.data_ptr(), _DTYPE[X2.dtype], _ld(X2), batch, Y.data_ptr(), _ld(Y), _handle_of(dev.index))
+        nbytes = _align_bytes(X2) if batch > 8 else 0
+        work = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
+        tail = (X2.data_ptr(), _DTYPE[X2.dtype], _ld(X2), batch, Y.data_ptr(), _ld(Y), _ptr(work), nbytes, _handle_of(dev.index))
         if len(ws) == 1:
             rc = _lib.load().externd_int4_matvec(*mats, w.m, w.n, w.group, *tail)
         else:
@@ -783,16 +796,6 @@ def _gated_inputs(X, Wg, Wu):
 
 def _flat(t: torch.Tensor) -> torch.Tensor:
     return t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
-
-
-def _align_bytes(*tensors) -> int:
-    """Workspace for the operands whose rows do not start on 16-byte boundaries (externd_gated_work each)."""
-    total = 0
-    for t in tensors:
-        rows, cols = t.shape
-        if t.data_ptr() % 16 or (rows > 1 and t.stride(0) % 8):
-            total += (rows * ((cols + 7) // 8 * 8) * 2 + 255) // 256 * 256
-    return total
 
 
 def _gated(X, Wg, Wu, act, save, out, async_status, stream):

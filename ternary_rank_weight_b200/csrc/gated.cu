@@ -556,24 +556,6 @@ cudaError_t launch_gemm(const Maps& maps, const GemmArgs& g, cudaStream_t s) {
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// ---- operands whose rows do not start on 16-byte boundaries ------------------------------------------
-
-// Up to three matrices are laid out in rows that do, in one launch: a warp a row, 8 columns a lane.  TMA needs that, and
-// such operands are odd-sized ones; a model's own sizes never come here.
-struct AlignJob { const unsigned short* src; int64_t lds; unsigned short* dst; int64_t ldd; int64_t rows, cols; };
-struct AlignJobs { AlignJob j[3]; int count; };
-
-__global__ void __launch_bounds__(256) align_rows_kernel(const AlignJobs jobs) {
-    const AlignJob& j = jobs.j[blockIdx.y];
-    const int lane = threadIdx.x & 31;
-    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < j.rows; r += (int64_t)gridDim.x * 8)
-        for (int64_t k = 8 * lane; k < j.cols; k += 256)
-            *reinterpret_cast<uint4*>(j.dst + r * j.ldd + k) = load8(j.src + r * j.lds, k, j.cols, false);
-}
-
-int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
-size_t plane_bytes(int64_t rows, int64_t cols) { return ((size_t)rows * (size_t)round8(cols) * 2 + 255) / 256 * 256; }
-
 // one call's arguments, with the operands' final places
 struct Call {
     const void* X; int64_t ldx;
@@ -591,34 +573,14 @@ struct Call {
     cudaStream_t stream;
 };
 
-bool row_aligned(const void* p, int64_t rows, int64_t ld) { return aligned(p, 16) && (rows < 2 || ld % 8 == 0); }
-
 // Move the operands that need it into `work` (consumed from its start).  Returns a status.
 int align_operands(Call& c, bool x, bool w) {
     AlignJobs jobs = {};
-    const auto place = [&](const void*& p, int64_t& ld, int64_t rows) {
-        if (row_aligned(p, rows, ld)) {
-            if (rows < 2) ld = round8(c.n);                         // one row: any leading dimension serves
-            return true;
-        }
-        const size_t bytes = plane_bytes(rows, c.n);
-        if (!c.work || c.work_bytes < bytes) return false;
-        jobs.j[jobs.count++] = {(const unsigned short*)p, ld, (unsigned short*)c.work, round8(c.n), rows, c.n};
-        p = c.work;
-        ld = round8(c.n);
-        c.work += bytes;
-        c.work_bytes -= bytes;
-        return true;
-    };
-    if (x && !place(c.X, c.ldx, c.tokens)) return EXTERND_EINVAL;
+    if (x && !place_rows(jobs, c.X, c.ldx, c.tokens, c.n, 2, c.work, c.work_bytes)) return EXTERND_EINVAL;
     if (w)
         for (int i = 0; i < 2; ++i)
-            if (!place(c.W[i], c.ldw[i], c.m)) return EXTERND_EINVAL;
-    if (jobs.count) {
-        align_rows_kernel<<<dim3((unsigned)sm_count() * 4, (unsigned)jobs.count), 256, 0, c.stream>>>(jobs);
-        if (cudaGetLastError() != cudaSuccess) return EXTERND_ECUDA;
-    }
-    return EXTERND_OK;
+            if (!place_rows(jobs, c.W[i], c.ldw[i], c.m, c.n, 2, c.work, c.work_bytes)) return EXTERND_EINVAL;
+    return align_rows(jobs, c.stream) == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
 }
 
 template <typename T, int CG>
@@ -753,7 +715,7 @@ int backward_tiles(const Call& c, const T* dg, const T* du, int64_t ldd, float* 
 template <typename T>
 int backward(const Call& c) {
     const int64_t ldd = round8(c.m);
-    const size_t plane = plane_bytes(c.tokens, c.m);
+    const size_t plane = plane_bytes(c.tokens, c.m, 2);
     const int splits = c.dX ? dx_splits(c.m, c.n, c.tokens) : 1;
     if (!c.work || c.work_bytes < 2 * plane + share_bytes(c.m, c.n, c.tokens)) return EXTERND_EINVAL;
     T* const dg = (T*)c.work;
@@ -814,7 +776,9 @@ using namespace externd_ffn;
 
 extern "C" {
 
-size_t externd_gated_work(int64_t rows, int64_t n) { return rows < 1 || n < 1 ? 0 : plane_bytes(rows, n); }
+size_t externd_aligned_bytes(int dtype, int64_t rows, int64_t n) {
+    return rows < 1 || n < 1 || !valid_dtype(dtype) ? 0 : plane_bytes(rows, n, dtype_bytes(dtype));
+}
 
 int externd_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu, int dtype, int64_t m, int64_t n,
                   int64_t tokens, int act, void* H, int64_t ldh, void* G, void* U, int save_dtype, int64_t ldgu, void* work,
@@ -841,7 +805,7 @@ int externd_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const
 }
 
 size_t externd_gated_backward_work(int64_t m, int64_t n, int64_t tokens) {
-    return m < 1 || n < 1 || tokens < 1 || too_large(m, n, tokens) ? 0 : 2 * plane_bytes(tokens, m) + share_bytes(m, n, tokens);
+    return m < 1 || n < 1 || tokens < 1 || too_large(m, n, tokens) ? 0 : 2 * plane_bytes(tokens, m, 2) + share_bytes(m, n, tokens);
 }
 
 int externd_gated_backward(const void* dH, int64_t lddh, const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu,
@@ -867,8 +831,8 @@ int externd_gated_backward(const void* dH, int64_t lddh, const void* X, int64_t 
         if (too_large(m, n, tokens)) return EXTERND_ELIMIT;
         size_t need = externd_gated_backward_work(m, n, tokens);
         if (dX)
-            for (int i = 0; i < 2; ++i) need += row_aligned(c.W[i], m, c.ldw[i]) ? 0 : plane_bytes(m, n);
-        if (dw) need += row_aligned(X, tokens, ldx) ? 0 : plane_bytes(tokens, n);
+            for (int i = 0; i < 2; ++i) need += row_aligned(c.W[i], m, c.ldw[i], 2) ? 0 : plane_bytes(m, n, 2);
+        if (dw) need += row_aligned(X, tokens, ldx, 2) ? 0 : plane_bytes(tokens, n, 2);
         if (!work || work_bytes < need) return EXTERND_EINVAL;
     }
     if (async_status && cudaMemsetAsync(async_status, 0, sizeof(int), c.stream) != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }

@@ -288,6 +288,12 @@ struct Mat4 {                       // one 4-bit matrix
     const __half* offset;           // nullptr: symmetric
 };
 
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+
 __device__ __forceinline__ uint32_t word_of(const uint4& q, int i) { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; }
 
 // d += (16 rows' codes of one word span) x (8 vectors' entries), all planes, least significant first
@@ -315,7 +321,7 @@ __device__ __forceinline__ void span_mma(float (&d)[4], const uint32_t (&a)[4], 
 // The offsets' part b sum(x) takes sum(x) from the lanes that hold x (products with ones would occupy the
 // tensor cores as long as the codes do, and those are nearly as busy as memory).
 // X element type, T product type (bf16 for fp32 X), NM matrices, WORDS = group / 32.
-constexpr int VEC_DEPTH = 4, VEC_WARPS = 8;
+constexpr int VEC_DEPTH = 4, VEC_WARPS = 8, VEC_BATCH = 8;
 
 __device__ __forceinline__ float sum8(const uint4& r, __half*) {
     const float2 a = unpack2<__half>(r.x), b = unpack2<__half>(r.y), c = unpack2<__half>(r.z), d = unpack2<__half>(r.w);
@@ -420,8 +426,7 @@ __global__ void __launch_bounds__(VEC_WARPS * 32) vec4_kernel(Mat4 w0, Mat4 w1, 
         for (int j = 0; j < NM; ++j)
             #pragma unroll
             for (int h = 0; h < 2; ++h)
-                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(code[j][h].x), "=r"(code[j][h].y), "=r"(code[j][h].z), "=r"(code[j][h].w)
-                             : "r"(mine + slot + (2 * j + h) * 512));
+                code[j][h] = lds128(mine + slot + (2 * j + h) * 512);
         float acc[NM][4] = {}, sum = 0.0f;
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -507,15 +512,16 @@ __global__ void __launch_bounds__(VEC_WARPS * 32) vec4_kernel(Mat4 w0, Mat4 w1, 
 // Bound by the codes' unpacking and staging at few vectors' worth of arithmetic a weight.
 constexpr int TC_EPI = 8, TC_PROD = 8, TC_THREADS = (TC_EPI + 1 + TC_PROD) * 32;
 template <int N> __host__ __device__ constexpr int tc_bufs() { return N == 64 ? 4 : 8; }     // accumulators in flight
-template <typename X> __host__ __device__ constexpr int tc_stages() { return Raw8<X>::PLANES == 3 ? 2 : 4; }
+template <typename X> __host__ __device__ constexpr int tc_stages() { return Raw8<X>::PLANES == 3 ? 2 : 3; }
+constexpr int TC_CODES = 6;                               // blocks of codes in flight, 32 bytes a thread each
 template <typename X, int N> __host__ __device__ constexpr int tc_stage() { return 128 * 256 + Raw8<X>::PLANES * N * 256; }
 template <typename X, int N> __host__ __device__ constexpr int tc_smem() {
-    return tc_stages<X>() * tc_stage<X, N>() + 128 * 128 + 1024;          // stages, the ones, alignment
+    return tc_stages<X>() * tc_stage<X, N>() + 128 * 128 + TC_CODES * TC_PROD * 32 * 32 + 1024;   // stages, the ones, codes, alignment
 }
 
 template <typename X, typename T, int N, int NM, int WORDS, bool AFFINE>
 __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, int64_t m, int64_t n, int act, const X* __restrict__ x,
-                                                             int64_t ldx, int vec, int64_t batch, X* __restrict__ y, int64_t ldy,
+                                                             int64_t ldx, int64_t batch, X* __restrict__ y, int64_t ldy,
                                                              int splits) {
     using Raw = typename Raw8<X>::type;
     constexpr int PLANES = Raw8<X>::PLANES;
@@ -572,12 +578,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
         const int p = threadIdx.x - (TC_EPI + 1) * 32, r = p & 127, h = p >> 7;
         const Mat4 w = NM == 2 && r >= 64 ? w1 : w0;
         const int64_t row = min(row0 + (NM == 2 ? r & 63 : r), m - 1);    // rows past the last one repeat it
-        const uint4* src = reinterpret_cast<const uint4*>(w.q + (row * blocks + first) * 64) + 2 * h;
+        const uint8_t* src = w.q + (row * blocks + first) * 64 + 32 * h;
         constexpr int PIECES = N * 16 / (TC_PROD * 32);      // pieces of 8 entries a thread: vectors col, col + 16, ..
-        constexpr int AHEAD = PLANES == 3 ? 1 : 2;           // blocks in flight
-        const int whole = vec ? (int)(n / 128) : 0;          // blocks whose entries load 16 bytes at a time, unchecked
+        constexpr int AHEAD = PLANES == 3 ? 1 : 2;           // blocks of entries in flight
+        const int whole = (int)(n / 128);          // blocks whose entries load 16 bytes at a time, unchecked
         const int col = p >> 4, piece = p & 15;
-        uint4 code[AHEAD][2];
         Raw ent[AHEAD][PIECES];
         // vectors past the last one repeat it: their sums are not stored
         const XE* xp[PIECES];
@@ -585,20 +590,30 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
         for (int e = 0; e < PIECES; ++e) xp[e] = reinterpret_cast<const XE*>(x + min(col0 + col + 16 * e, batch - 1) * ldx) + (int64_t)first * 128 + 8 * piece;
         const auto load = [&](int u, int blk) {
             if (blk >= last) return;
-            code[u][0] = __ldcs(src);
-            code[u][1] = __ldcs(src + 1);
-            src += 4;
             if (blk < whole) {
                 #pragma unroll
                 for (int e = 0; e < PIECES; ++e) ent[u][e] = *reinterpret_cast<const Raw*>(xp[e]);
             } else {
                 const int64_t k = (int64_t)blk * 128 + 8 * piece;
                 #pragma unroll
-                for (int e = 0; e < PIECES; ++e) ent[u][e] = load8(xp[e] - k, k, n, vec);
+                for (int e = 0; e < PIECES; ++e) ent[u][e] = load8(xp[e] - k, k, n, true);
             }
             #pragma unroll
             for (int e = 0; e < PIECES; ++e) xp[e] += 128;
         };
+        // codes ride a ring of their own, each thread copying what it will unpack: no barrier
+        const uint32_t cring = ones + 128 * 128 + p * 16;    // halves of the 32 bytes TC_PROD * 512 bytes apart
+        const auto issue = [&](int blk, uint32_t at) {
+            if (blk < last) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(cring + at), "l"(src) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(cring + at + TC_PROD * 512), "l"(src + 16) : "memory");
+                src += 64;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        #pragma unroll
+        for (int d = 0; d < TC_CODES; ++d) issue(first + d, d * (TC_PROD * 1024));
+        uint32_t slot = 0;
         // places within a stage: columns 32 i + 8 c (c = 2 h, 2 h + 1) of the block are 16-byte chunk 4 (i % 2) + c of half
         // i / 2, a row 128 bytes, chunks swizzled by the row; entries alike (vectors 16 apart share their swizzle)
         const uint32_t place = r * 128 + (((2 * h) ^ (r & 7)) << 4), xplace = 128 * 256 + (piece >> 3) * (N * 128) + col * 128 + (((piece & 7) ^ (col & 7)) << 4);
@@ -616,12 +631,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
                 if (blk >= last) break;
                 if (!mbar_wait(empty0 + 8 * s, phase, quit)) { ok = false; break; }
                 const uint32_t st = base + s * STAGE, at = st + place;
+                asm volatile("cp.async.wait_group %0;" ::"n"(TC_CODES - 1) : "memory");
+                const uint4 code[2] = {lds128(cring + slot), lds128(cring + slot + TC_PROD * 512)};
                 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     #pragma unroll
                     for (int cc = 0; cc < 2; ++cc) {
                         uint32_t v[4];
-                        codes8<T>(word_of(code[u][cc], i), v);
+                        codes8<T>(word_of(code[cc], i), v);
                         sts(((at ^ (16u * cc)) ^ (64u * (i & 1))) + (i >> 1) * (128 * 128), v);
                     }
                 #pragma unroll
@@ -632,11 +649,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
                     for (int q = 0; q < PLANES; ++q) sts(st + xplace + q * N * 256 + e * 2048, v[q]);
                 }
                 load(u, blk + AHEAD);
+                issue(blk + TC_CODES, slot);                 // the slot's codes have been used
+                slot = slot == (TC_CODES - 1) * (TC_PROD * 1024) ? 0 : slot + TC_PROD * 1024;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(full0 + 8 * s);
                 if (++s == STAGES) { s = 0; phase ^= 1; }
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == TC_EPI) {
         // ---- products
         const bool leader = elect_one();
@@ -798,8 +818,8 @@ cudaError_t launch_vec4(const Product& p) {
     constexpr int smem = VEC_WARPS * VEC_DEPTH * NM * 1024;
     const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    const bool vec = aligned(p.x, 16) && p.ldx * sizeof(X) % 16 == 0;
-    kernel<<<(unsigned)((p.m + 15) / 16), VEC_WARPS * 32, smem, p.stream>>>(p.w0, p.w1, p.m, p.n, p.act, (const X*)p.x, p.ldx, vec,
+    const bool vec = row_aligned(p.x, p.batch, p.ldx, sizeof(X));
+    kernel<<<(unsigned)((p.m + 15) / 16), VEC_WARPS * 32, smem, p.stream>>>(p.w0, p.w1, p.m, p.n, p.act, (const X*)p.x, p.ldx, (int)vec,
                                                                            (int)p.batch, (X*)p.y, p.ldy);
     return cudaGetLastError();
 }
@@ -810,7 +830,6 @@ cudaError_t launch_tile4(const Product& p) {
     constexpr int smem = tc_smem<X, N>();
     const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
-    const bool vec = aligned(p.x, 16) && p.ldx * sizeof(X) % 16 == 0;
     const int64_t tiles = (p.m + 128 / NM - 1) / (128 / NM), cols = (p.batch + N - 1) / N, blocks = (p.n + 127) / 128;
     // shares of the columns: the fewest rounds of CTAs times the blocks of a share, each CTA costing about
     // nine blocks' time (of 0.8 us) to start, fill its stages and add up
@@ -831,12 +850,12 @@ cudaError_t launch_tile4(const Product& p) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = splits > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p.w0, p.w1, p.m, p.n, p.act, (const X*)p.x, p.ldx, (int)vec, p.batch, (X*)p.y, p.ldy, splits);
+    return cudaLaunchKernelEx(&cfg, kernel, p.w0, p.w1, p.m, p.n, p.act, (const X*)p.x, p.ldx, p.batch, (X*)p.y, p.ldy, splits);
 }
 
 template <typename X, typename T, int NM, int WORDS, bool AFFINE>
 cudaError_t run_kernel(const Product& p) {
-    if (p.batch <= 8) return launch_vec4<X, T, NM, WORDS, AFFINE>(p);
+    if (p.batch <= VEC_BATCH) return launch_vec4<X, T, NM, WORDS, AFFINE>(p);
     if (p.batch <= 16) return launch_tile4<X, T, NM, WORDS, AFFINE, 16>(p);
     if (p.batch <= 32) return launch_tile4<X, T, NM, WORDS, AFFINE, 32>(p);
     return launch_tile4<X, T, NM, WORDS, AFFINE, 64>(p);
@@ -858,7 +877,7 @@ cudaError_t run_product(const Product& p) {
 
 template <int NM>
 int products(const Mat4& w0, const Mat4& w1, int64_t m, int64_t n, int group, int act, const void* X, int dtype, int64_t ldx,
-             int64_t batch, void* Y, int64_t ldy, void* stream) {
+             int64_t batch, void* Y, int64_t ldy, void* work, size_t work_bytes, void* stream) {
     if (m < 1 || n < 1 || batch < 0 || !valid_group(group) || !valid_dtype(dtype) || ldx < n || ldy < m) return EXTERND_EINVAL;
     if (NM == 2 && !valid_act(act)) return EXTERND_EINVAL;
     const Device dev;
@@ -872,8 +891,14 @@ int products(const Mat4& w0, const Mat4& w1, int64_t m, int64_t n, int group, in
     if (!X || !Y || !aligned(X, eb) || !aligned(Y, eb) || !dev.holds(X) || !dev.holds(Y)) return EXTERND_EINVAL;
     // grid dimensions, 32-bit column blocks
     if ((m + 15) / 16 > 0x7fffffff / 8 || (batch + 63) / 64 > 65535 || n > 0x7fffffff - 128) return EXTERND_ELIMIT;
-    const Product p = {w0, w1, m, n, group, act, X, ldx, batch, Y, ldy, reinterpret_cast<cudaStream_t>(stream)};
-    cudaError_t e;
+    if (work && (!aligned(work, 256) || !dev.holds(work))) return EXTERND_EINVAL;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    AlignJobs jobs = {};
+    unsigned char* place = (unsigned char*)work;
+    if (batch > VEC_BATCH && !place_rows(jobs, X, ldx, batch, n, eb, place, work_bytes)) return EXTERND_EINVAL;
+    const Product p = {w0, w1, m, n, group, act, X, ldx, batch, Y, ldy, s};
+    cudaError_t e = align_rows(jobs, s);
+    if (e != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
     switch (dtype) {
         case EXTERND_F32: e = run_product<float, __nv_bfloat16, NM>(p); break;
         case EXTERND_F16: e = run_product<__half, __half, NM>(p); break;
@@ -988,16 +1013,16 @@ int externd_int4_dequantize(const uint8_t* q, const void* scale, const void* off
 }
 
 int externd_int4_matvec(const uint8_t* q, const void* scale, const void* offset, int64_t m, int64_t n, int group, const void* X,
-                        int dtype, int64_t ldx, int64_t batch, void* Y, int64_t ldy, void* stream) {
+                        int dtype, int64_t ldx, int64_t batch, void* Y, int64_t ldy, void* work, size_t work_bytes, void* stream) {
     const Mat4 w = {q, (const __half*)scale, (const __half*)offset};
-    return products<1>(w, Mat4{}, m, n, group, 0, X, dtype, ldx, batch, Y, ldy, stream);
+    return products<1>(w, Mat4{}, m, n, group, 0, X, dtype, ldx, batch, Y, ldy, work, work_bytes, stream);
 }
 
 int externd_int4_gated(const uint8_t* qg, const void* scale_g, const void* offset_g, const uint8_t* qu, const void* scale_u,
                        const void* offset_u, int64_t m, int64_t n, int group, int act, const void* X, int dtype, int64_t ldx,
-                       int64_t batch, void* H, int64_t ldh, void* stream) {
+                       int64_t batch, void* H, int64_t ldh, void* work, size_t work_bytes, void* stream) {
     const Mat4 wg = {qg, (const __half*)scale_g, (const __half*)offset_g}, wu = {qu, (const __half*)scale_u, (const __half*)offset_u};
-    return products<2>(wg, wu, m, n, group, act, X, dtype, ldx, batch, H, ldh, stream);
+    return products<2>(wg, wu, m, n, group, act, X, dtype, ldx, batch, H, ldh, work, work_bytes, stream);
 }
 
 }  // extern "C"

@@ -233,6 +233,57 @@ __device__ __forceinline__ void planes8(const F8& r, uint32_t (&v)[3][4]) {
     }
 }
 
+// ---- operands whose rows do not start on 16-byte boundaries ---------------------------------------------
+
+// Up to three matrices are laid out in rows that do, in one launch: a warp a row, 16 bytes a lane.  TMA needs that,
+// and wide loads; such operands are odd-sized ones, a model's own sizes hardly ever come here.
+// Elements count as 16-bit ones (an fp32 as two).
+struct AlignJob { const unsigned short* src; int64_t lds; unsigned short* dst; int64_t ldd; int64_t rows, cols; };
+struct AlignJobs { AlignJob j[3]; int count; };
+
+static __global__ void __launch_bounds__(256) align_rows_kernel(const AlignJobs jobs) {
+    const AlignJob& j = jobs.j[blockIdx.y];
+    const int lane = threadIdx.x & 31;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < j.rows; r += (int64_t)gridDim.x * 8)
+        for (int64_t k = 8 * lane; k < j.cols; k += 256)
+            *reinterpret_cast<uint4*>(j.dst + r * j.ldd + k) = load8(j.src + r * j.lds, k, j.cols, false);
+}
+
+inline int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
+inline bool row_aligned(const void* p, int64_t rows, int64_t ld, size_t bytes) { return aligned(p, 16) && (rows < 2 || ld * bytes % 16 == 0); }
+// bytes of rows x cols elements laid out in aligned rows
+inline size_t plane_bytes(int64_t rows, int64_t cols, size_t bytes) {
+    return ((size_t)rows * (size_t)round8(cols * (int64_t)(bytes / 2)) * 2 + 255) / 256 * 256;
+}
+
+// Where p (rows x cols elements of `bytes` bytes) has misaligned rows: give it a place at the start of the workspace
+// and note the job.  false: the workspace is too small.
+inline bool place_rows(AlignJobs& jobs, const void*& p, int64_t& ld, int64_t rows, int64_t cols, size_t bytes, unsigned char*& work,
+                       size_t& work_bytes) {
+    const int64_t wide = round8(cols * (int64_t)(bytes / 2));           // in 16-bit elements
+    if (row_aligned(p, rows, ld, bytes)) {
+        if (rows < 2) ld = wide / (int64_t)(bytes / 2);                 // one row: any leading dimension serves
+        return true;
+    }
+    const size_t need = plane_bytes(rows, cols, bytes);
+    if (!work || work_bytes < need) return false;
+    jobs.j[jobs.count++] = {(const unsigned short*)p, ld * (int64_t)(bytes / 2), (unsigned short*)work, wide, rows, cols * (int64_t)(bytes / 2)};
+    p = work;
+    ld = wide / (int64_t)(bytes / 2);
+    work += need;
+    work_bytes -= need;
+    return true;
+}
+
+inline cudaError_t align_rows(const AlignJobs& jobs, cudaStream_t stream) {
+    if (jobs.count == 0) return cudaSuccess;
+    int64_t rows = 1;
+    for (int i = 0; i < jobs.count; ++i) rows = rows > jobs.j[i].rows ? rows : jobs.j[i].rows;
+    const int64_t want = (rows + 7) / 8, cap = (int64_t)sm_count() * 8;
+    align_rows_kernel<<<dim3((unsigned)(want < cap ? want : cap), (unsigned)jobs.count), 256, 0, stream>>>(jobs);
+    return cudaGetLastError();
+}
+
 // ---- clusters ------------------------------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }

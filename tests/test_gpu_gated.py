@@ -296,7 +296,7 @@ def test_library_refuses_bad_arguments():
     H, G, Up = ext.gated_forward(X, Wg, Wu)
     out = [torch.zeros(s, dtype=BF16, device="cuda") for s in ((t, n), (m, n), (m, n))]
     need = L.externd_gated_backward_work(m, n, t)
-    work = torch.zeros(need + 3 * L.externd_gated_work(m, n), dtype=torch.uint8, device="cuda")
+    work = torch.zeros(need + 3 * L.externd_aligned_bytes(2, m, n), dtype=torch.uint8, device="cuda")
     host = torch.zeros(1 << 16, dtype=torch.uint8)
     st = torch.cuda.current_stream().cuda_stream
     base = dict(x=X.data_ptr(), ldx=n, wg=Wg.data_ptr(), ldg=n, wu=Wu.data_ptr(), ldu=n, dt=2, m=m, n=n, t=t, act=0, h=H.data_ptr(),
@@ -326,9 +326,9 @@ def test_library_refuses_bad_arguments():
                dict(wb=need - 1), dict(work=work.data_ptr() + 16), dict(dwg=host.data_ptr())):
         assert bwd(**kw) == einval, kw
     # rows off the 16-byte boundaries take their place in work
-    over = (work.data_ptr(), L.externd_gated_work(t, n))
+    over = (work.data_ptr(), L.externd_aligned_bytes(2, t, n))
     assert fwd(x=X.data_ptr() + 2, t=t - 1, fw=over[0], fwb=over[1]) == 0
-    assert fwd(x=X.data_ptr() + 2, t=t - 1, fw=over[0], fwb=L.externd_gated_work(t - 1, n) - 1) == einval
+    assert fwd(x=X.data_ptr() + 2, t=t - 1, fw=over[0], fwb=L.externd_aligned_bytes(2, t - 1, n) - 1) == einval
     assert bwd(x=X.data_ptr() + 2, t=t - 1, wb=need + over[1]) == 0
     assert bwd(dx=None, wg=None, wu=None) == 0 and bwd(dwg=None, dwu=None, x=None) == 0
     with pytest.raises(ValueError):

@@ -254,14 +254,15 @@ def test_products_repeat_bit_for_bit_on_streams_and_in_graphs():
 def test_library_refuses_bad_arguments():
     L, einval = ext._lib.load(), ext.STATUS["EINVAL"]
     w = _random_weights(20, 100, 64, True, seed=1)
-    X, Y = _vectors(3, 100, 1, BF16), torch.zeros(3, 20, dtype=BF16, device="cuda")
-    base = dict(q=w.q.data_ptr(), s=w.scale.data_ptr(), b=w.offset.data_ptr(), m=20, n=100, group=64, x=X.data_ptr(), dt=2,
-                ldx=100, batch=3, y=Y.data_ptr(), ldy=20)
+    X, Y = _vectors(12, 104, 1, BF16), torch.zeros(12, 20, dtype=BF16, device="cuda")
+    work = torch.zeros(L.externd_aligned_bytes(2, 11, 100), dtype=torch.uint8, device="cuda")
+    base = dict(work=None, wb=0, q=w.q.data_ptr(), s=w.scale.data_ptr(), b=w.offset.data_ptr(), m=20, n=100, group=64, x=X.data_ptr(), dt=2,
+                ldx=104, batch=3, y=Y.data_ptr(), ldy=20)
 
     def call(**kw):
         a = dict(base, **kw)
         return L.externd_int4_matvec(a["q"], a["s"], a["b"], a["m"], a["n"], a["group"], a["x"], a["dt"], a["ldx"], a["batch"],
-                                     a["y"], a["ldy"], torch.cuda.current_stream().cuda_stream)
+                                     a["y"], a["ldy"], a["work"], a["wb"], torch.cuda.current_stream().cuda_stream)
 
     assert call() == 0
     host = torch.zeros(4096, dtype=torch.uint8)
@@ -270,3 +271,9 @@ def test_library_refuses_bad_arguments():
                dict(s=w.scale.data_ptr() + 1), dict(x=X.data_ptr() + 1), dict(x=host.data_ptr()), dict(q=host.data_ptr())):
         assert call(**kw) == einval, kw
     assert call(batch=0, x=None, y=None) == 0
+    # more than 8 rows off the 16-byte boundaries take their place in work
+    assert call(x=X.data_ptr() + 2) == 0
+    off = dict(x=X.data_ptr() + 2, batch=11)
+    assert call(**off) == einval and call(**off, work=work.data_ptr(), wb=work.numel() - 1) == einval
+    assert call(**off, work=host.data_ptr(), wb=work.numel()) == einval and call(**off, work=work.data_ptr() + 16, wb=work.numel()) == einval
+    assert call(**off, work=work.data_ptr(), wb=work.numel()) == 0

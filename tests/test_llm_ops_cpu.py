@@ -38,9 +38,9 @@ def test_int4_entry_points_reject_bad_arguments_before_device_work():
     assert L.externd_int4_quantize(p, 0, 1, 1, 1, 48, p, p, None, None, None) == EINVAL
     assert L.externd_int4_dequantize(p, p, None, 1, 1, 32, p, 0, 1, None) == EINVAL            # host memory
     assert L.externd_int4_dequantize(p, p, None, 1, 1, 32, None, 0, 1, None) == EINVAL
-    assert L.externd_int4_matvec(p, p, None, 1, 1, 32, p, 0, 1, 1, p, 1, None) == EINVAL       # host memory
-    assert L.externd_int4_matvec(p, p, None, 1, 1, 32, p, 0, 1, -1, p, 1, None) == EINVAL
-    assert L.externd_int4_gated(p, p, None, p, p, None, 1, 1, 32, 4, p, 0, 1, 1, p, 1, None) == EINVAL   # activation
+    assert L.externd_int4_matvec(p, p, None, 1, 1, 32, p, 0, 1, 1, p, 1, None, 0, None) == EINVAL       # host memory
+    assert L.externd_int4_matvec(p, p, None, 1, 1, 32, p, 0, 1, -1, p, 1, None, 0, None) == EINVAL
+    assert L.externd_int4_gated(p, p, None, p, p, None, 1, 1, 32, 4, p, 0, 1, 1, p, 1, None, 0, None) == EINVAL   # activation
 
 
 def test_int4_binding_rejects_bad_tensors():
@@ -74,8 +74,9 @@ def test_gated_entry_points_reject_bad_arguments_before_device_work():
     for kw in ({}, dict(w=None), dict(dt=0), dict(act=9), dict(m=0), dict(n=0), dict(t=-1), dict(h=None), dict(wb=256)):
         assert fwd(**kw) == EINVAL, kw                                       # {}: host memory
     assert L.externd_gated_backward(p, 1, p, 8, p, 8, p, 8, p, p, 0, 1, 2, 1, 1, 1, 0, p, 1, p, p, 1, p, 512, None, None) == EINVAL
-    assert L.externd_gated_work(0, 5) == 0 and L.externd_gated_work(5, 0) == 0
-    assert L.externd_gated_work(3, 9) == 256 and L.externd_gated_work(100, 9) == 3328
+    assert L.externd_aligned_bytes(1, 0, 5) == 0 and L.externd_aligned_bytes(1, 5, 0) == 0 and L.externd_aligned_bytes(7, 5, 5) == 0
+    assert L.externd_aligned_bytes(2, 3, 9) == 256 and L.externd_aligned_bytes(1, 100, 9) == 3328
+    assert L.externd_aligned_bytes(0, 100, 9) == 4864                       # fp32: rows of 48 bytes
     assert L.externd_gated_backward_work(0, 5, 5) == 0 and L.externd_gated_backward_work(5, 5, 0) == 0
     # two planes of 8-element rows on 256 bytes; besides, with few tokens, shares of dX
     assert L.externd_gated_backward_work(3, 3, 1) == 512
