@@ -267,7 +267,9 @@ int externd_pack_mask_sign(const uint8_t* T, int64_t rows, int64_t len, uint8_t*
  * dimension in ELEMENTS (at least the number of columns); element types are EXTERND_F32,
  * EXTERND_F16 or EXTERND_BF16.  Calls are stream-ordered and asynchronous unless noted; they
  * allocate nothing and keep nothing between calls, so they can be captured into CUDA graphs.
- * Outputs must not overlap inputs.  Sums are held in fp32.
+ * Outputs must not overlap inputs.  Sums are held in fp32.  The first call of an entry point on a device may
+ * load device code there: make it before any stream capture.  A device-side wait that gave up (2 s; it does
+ * not happen unless the device stops) leaves NaN in the results of the 4-bit products.
  * ------------------------------------------------------------------------- */
 
 typedef enum { EXTERND_F32 = 0, EXTERND_F16 = 1, EXTERND_BF16 = 2 } externd_dtype;

@@ -551,6 +551,7 @@ def pack_mask_sign(T: torch.Tensor, rows: int, length: int, *, stream=None):
 # ---------------------------------------------------------------------------
 
 _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_SIZE = {torch.float32: 4, torch.float16: 2, torch.bfloat16: 2}
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu2": 3}
 
 
@@ -558,8 +559,9 @@ _NOTHING = contextlib.nullcontext()
 
 
 def _guard(stream, device: torch.device):
-    """Make `device` current, and `stream` if one is given: torch's allocator may hand the memory of
-    temporaries and outputs to later work of the stream they were allocated on only."""
+    """Make `device` current, and `stream` if one is given: the memory of temporaries and outputs must belong
+    to the stream the kernels run on, for torch's allocator hands it to later work of that stream only.
+    Results of a call with `stream` are ready for, and belong to, that stream."""
     if stream is None:
         return _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     if not isinstance(stream, torch.cuda.Stream):
@@ -607,15 +609,25 @@ def _result(out, rows: int, cols: int, like: torch.Tensor) -> torch.Tensor:
     return out
 
 
-def _align_bytes(*tensors) -> int:
-    """Workspace for the operands whose rows do not start on 16-byte boundaries (externd_aligned_bytes each)."""
-    total = 0
-    for t in tensors:
-        rows, cols = t.shape
-        size = t.element_size()
-        if t.data_ptr() % 16 or (rows > 1 and t.stride(0) * size % 16):
-            total += (rows * ((cols * size + 15) // 16 * 16) + 255) // 256 * 256
-    return total
+def _operand(t, cols: int, name: str, dtype: torch.dtype, device: torch.device):
+    """A 2-D operand (copied where its columns are not of unit stride): the tensor, its address, its leading
+    dimension and the workspace it takes if its rows do not start on 16-byte boundaries
+    (externd_aligned_bytes)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor on {device}")
+    rows, width = t.shape
+    if width != cols:
+        raise ValueError(f"{name} must have {cols} columns, not {width}")
+    ld, step = t.stride()
+    if rows and ((step != 1 and cols > 1) or (rows > 1 and ld < cols)):
+        t = t.contiguous()
+        ld = cols
+    if rows < 2:
+        ld = cols
+    ptr, size = t.data_ptr(), _SIZE[dtype]
+    if ptr & 15 or (rows > 1 and ld * size & 15):
+        return t, ptr, ld, (rows * ((cols * size + 15) // 16 * 16) + 255) // 256 * 256
+    return t, ptr, ld, 0
 
 
 def _act(act: str) -> int:
@@ -650,6 +662,8 @@ def _check_int4(w: Int4Weights, device: torch.device):
     if m < 1 or n < 1 or group not in (32, 64, 128):
         raise ValueError("Int4Weights need m, n >= 1 and groups of 32, 64 or 128 columns")
     q, scale, offset = w.q, w.scale, w.offset
+    if not isinstance(q, torch.Tensor) or not isinstance(scale, torch.Tensor) or not (offset is None or isinstance(offset, torch.Tensor)):
+        raise ValueError("q, scale and offset must be tensors (offset may be None)")
     scales = ((n + group - 1) // group, m)
     if q.dtype != torch.uint8 or q.shape != (m, (n + 127) // 128 * 64) or q.device != device or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous uint8 tensor of {m} rows of int4_row_bytes({n}) on {device}")
@@ -689,7 +703,7 @@ def int4_quantize(A: torch.Tensor, group: int = 128, *, affine: bool = True, asy
 
 def int4_dequantize(w: Int4Weights, dtype: torch.dtype = torch.float32, *, stream=None) -> torch.Tensor:
     """The m x n matrix that the 4 bits stand for, rounded once to dtype (externd_int4_dequantize)."""
-    if not isinstance(w, Int4Weights) or not w.q.is_cuda:
+    if not isinstance(w, Int4Weights) or not isinstance(w.q, torch.Tensor) or not w.q.is_cuda:
         raise ValueError("w must be Int4Weights on the GPU")
     if dtype not in _DTYPE:
         raise ValueError("dtype must be float32, float16 or bfloat16")
@@ -718,23 +732,25 @@ def int4_gated(wg: Int4Weights, wu: Int4Weights, X: torch.Tensor, act: str = "si
 
 
 def _int4_products(ws, X, act: int, out, stream) -> torch.Tensor:
-    if not isinstance(X, torch.Tensor) or not X.is_cuda:
-        raise ValueError("X must be a CUDA tensor")
-    dev = X.device
+    if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dtype not in _DTYPE:
+        raise ValueError("X must be a float32, float16 or bfloat16 CUDA tensor")
+    dev, dtype = X.device, X.dtype
     mats = []
     for w in ws:
         _check_int4(w, dev)
         mats += (w.q.data_ptr(), w.scale.data_ptr(), None if w.offset is None else w.offset.data_ptr())
     squeeze = X.dim() == 1
     with _guard(stream, dev):
-        X2 = _rows_in(X.unsqueeze(0) if squeeze else X, w.n, "X")
+        X2, x, ldx, nbytes = _operand(X.unsqueeze(0) if squeeze else X, w.n, "X", dtype, dev)
         if out is not None and squeeze:
             out = out.unsqueeze(0)
         batch = X2.shape[0]
         Y = _result(out, batch, w.m, X2)
-        nbytes = _align_bytes(X2) if batch > 8 else 0
-        work = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
-        tail = (X2.data_ptr(), _DTYPE[X2.dtype], _ld(X2), batch, Y.data_ptr(), _ld(Y), _ptr(work), nbytes, _handle_of(dev.index))
+        work = None
+        if nbytes and batch > 8:
+            work = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        tail = (x, _DTYPE[dtype], ldx, batch, Y.data_ptr(), w.m if out is None else _ld(Y), _ptr(work),
+                0 if work is None else nbytes, _handle_of(dev.index))
         if len(ws) == 1:
             rc = _lib.load().externd_int4_matvec(*mats, w.m, w.n, w.group, *tail)
         else:
@@ -785,13 +801,13 @@ def _gated_inputs(X, Wg, Wu):
     if not isinstance(Wg, torch.Tensor) or Wg.dim() != 2 or Wg.numel() == 0:
         raise ValueError("Wg must be a 2-D float16 or bfloat16 CUDA tensor")
     m, n = Wg.shape
-    if not isinstance(X, torch.Tensor) or X.dim() < 1 or X.shape[-1] != n or not X.is_cuda:
+    if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dim() < 1 or X.shape[-1] != n:
         raise ValueError(f"X must be a CUDA tensor whose last dimension is {n}")
-    if X.dtype not in (torch.float16, torch.bfloat16):
+    if X.dtype != torch.bfloat16 and X.dtype != torch.float16:
         raise ValueError("X, Wg and Wu must be float16 or bfloat16")
     if not isinstance(Wu, torch.Tensor) or Wu.shape != Wg.shape:
         raise ValueError("Wg and Wu must have the same shape")
-    return m, n
+    return m, n, X.device, X.dtype
 
 
 def _flat(t: torch.Tensor) -> torch.Tensor:
@@ -799,31 +815,33 @@ def _flat(t: torch.Tensor) -> torch.Tensor:
 
 
 def _gated(X, Wg, Wu, act, save, out, async_status, stream):
-    m, n = _gated_inputs(X, Wg, Wu)
+    m, n, dev, dtype = _gated_inputs(X, Wg, Wu)
     code = _act(act)
-    dev = X.device
     _check_status(async_status, dev)
-    shape = (*X.shape[:-1], m)
-    if out is not None and (not isinstance(out, torch.Tensor) or out.shape != shape):
-        raise ValueError(f"out must have shape {shape}")
-    if save is not None and save not in (torch.float32, X.dtype):
+    two = X.dim() == 2
+    shape = (X.shape[0], m) if two else (*X.shape[:-1], m)
+    if out is not None and (not isinstance(out, torch.Tensor) or out.shape != shape or (out.dim() > 2 and not out.is_contiguous())):
+        raise ValueError(f"out must have shape {shape} (and be contiguous with more than two dimensions)")
+    if save is not None and save != torch.float32 and save != dtype:
         raise ValueError("the projections can be saved in float32 or in X's type")
     with _guard(stream, dev):
-        X2 = _rows_in(_flat(X), n, "X")
-        Wg, Wu = _rows_in(Wg, n, "Wg", X2), _rows_in(Wu, n, "Wu", X2)
+        X2, x, ldx, bx = _operand(_flat(X), n, "X", dtype, dev)
+        Wg, wg, ldg, bg = _operand(Wg, n, "Wg", dtype, dev)
+        Wu, wu, ldu, bu = _operand(Wu, n, "Wu", dtype, dev)
         t = X2.shape[0]
         H = _result(None if out is None else out.view(-1, m), t, m, X2)
         G = U = None
         if save is not None:
             G, U = X2.new_empty(shape, dtype=save), X2.new_empty(shape, dtype=save)
-        nbytes = _align_bytes(X2, Wg, Wu)
+        nbytes = bx + bg + bu
         work = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
-        rc = _lib.load().externd_gated(X2.data_ptr(), _ld(X2), Wg.data_ptr(), _ld(Wg), Wu.data_ptr(), _ld(Wu), _DTYPE[X2.dtype],
-                                       m, n, t, code, H.data_ptr(), _ld(H), G.data_ptr() if t and save else None,
-                                       U.data_ptr() if t and save else None, _DTYPE[save or X2.dtype], m, _ptr(work), nbytes,
+        kept = t and save is not None
+        rc = _lib.load().externd_gated(x, ldx, wg, ldg, wu, ldu, _DTYPE[dtype], m, n, t, code, H.data_ptr(),
+                                       m if out is None else _ld(H), G.data_ptr() if kept else None,
+                                       U.data_ptr() if kept else None, _DTYPE[save or dtype], m, _ptr(work), nbytes,
                                        _ptr(async_status), _handle_of(dev.index))
     _check(rc, "externd_gated")
-    return (H if X.dim() == 2 else H.view(shape)), G, U
+    return (H if two else H.view(shape)), G, U
 
 
 def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", *, out: Optional[torch.Tensor] = None,
@@ -848,37 +866,38 @@ def gated_backward(dH: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torc
                    act: str = "silu", *, need=(True, True, True), async_status=None, stream=None):
     """(dX, dWg, dWu) from the gradient dH of gated_forward's H and the G and U it returned
     (externd_gated_backward); need: which of the three to compute (None in place of the others)."""
-    m, n = _gated_inputs(X, Wg, Wu)
+    m, n, dev, dtype = _gated_inputs(X, Wg, Wu)
     code = _act(act)
-    dev = X.device
     _check_status(async_status, dev)
-    shape = (*X.shape[:-1], m)
+    two = X.dim() == 2
+    shape = (X.shape[0], m) if two else (*X.shape[:-1], m)
     for name, v in (("dH", dH), ("G", G), ("U", U)):
         if not isinstance(v, torch.Tensor) or v.shape != shape:
             raise ValueError(f"{name} must have shape {shape}")
-    if G.dtype != U.dtype or G.dtype not in (torch.float32, X.dtype):
+    saved = G.dtype
+    if saved != torch.float32 and saved != dtype:
         raise ValueError("G and U must both be float32 or both of X's type")
     with _guard(stream, dev):
-        X2 = _rows_in(_flat(X), n, "X")
-        Wg, Wu = _rows_in(Wg, n, "Wg", X2), _rows_in(Wu, n, "Wu", X2)
-        dH2, G2 = _rows_in(_flat(dH), m, "dH", X2), _rows_in(_flat(G), m, "G")
-        U2 = _rows_in(_flat(U), m, "U", G2)
-        if G2.device != dev:
-            raise ValueError("G and U must be on X's device")
-        if _ld(G2) != _ld(U2):
+        X2, x, ldx, bx = _operand(_flat(X), n, "X", dtype, dev)
+        Wg, wg, ldg, bg = _operand(Wg, n, "Wg", dtype, dev)
+        Wu, wu, ldu, bu = _operand(Wu, n, "Wu", dtype, dev)
+        dH2, dh, lddh, _ = _operand(_flat(dH), m, "dH", dtype, dev)
+        G2, g, lds, _ = _operand(_flat(G), m, "G", saved, dev)
+        U2, u, ldu2, _ = _operand(_flat(U), m, "U", saved, dev)
+        if lds != ldu2:
             G2, U2 = G2.contiguous(), U2.contiguous()
+            g, u, lds = G2.data_ptr(), U2.data_ptr(), m
         t = X2.shape[0]
         dX = X2.new_empty((t, n)) if need[0] else None
         dWg = X2.new_empty((m, n)) if need[1] else None
         dWu = X2.new_empty((m, n)) if need[2] else None
         nbytes = 0
         if t and (need[0] or need[1] or need[2]):
-            used = ([Wg, Wu] if need[0] else []) + ([X2] if need[1] or need[2] else [])
-            nbytes = _lib.load().externd_gated_backward_work(m, n, t) + _align_bytes(*used)
+            nbytes = (_lib.load().externd_gated_backward_work(m, n, t) + (bg + bu if need[0] else 0)
+                      + (bx if need[1] or need[2] else 0))
         work = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
-        rc = _lib.load().externd_gated_backward(
-            dH2.data_ptr(), _ld(dH2), X2.data_ptr(), _ld(X2), Wg.data_ptr(), _ld(Wg), Wu.data_ptr(), _ld(Wu), G2.data_ptr(),
-            U2.data_ptr(), _DTYPE[G2.dtype], _ld(G2), _DTYPE[X2.dtype], m, n, t, code, _ptr(dX), n, _ptr(dWg), _ptr(dWu), n,
-            _ptr(work), nbytes, _ptr(async_status), _handle_of(dev.index))
+        rc = _lib.load().externd_gated_backward(dh, lddh, x, ldx, wg, ldg, wu, ldu, g, u, _DTYPE[saved], lds, _DTYPE[dtype], m, n,
+                                                t, code, _ptr(dX), n, _ptr(dWg), _ptr(dWu), n, _ptr(work), nbytes,
+                                                _ptr(async_status), _handle_of(dev.index))
     _check(rc, "externd_gated_backward")
-    return (dX if dX is None or X.dim() == 2 else dX.view(X.shape)), dWg, dWu
+    return (dX if two or dX is None else dX.view(X.shape)), dWg, dWu

@@ -377,7 +377,11 @@ template <typename T> struct Saved8 {
 template <typename T, typename S, int ACT, bool VEC>
 __global__ void __launch_bounds__(256) gate_grad_kernel(const T* __restrict__ dh, int64_t lddh, const S* __restrict__ gs,
                                                         const S* __restrict__ us, int64_t ldgu, int64_t rows, int64_t m,
-                                                        T* __restrict__ dg, T* __restrict__ du, int64_t ldw) {
+                                                        T* __restrict__ dg, T* __restrict__ du, int64_t ldw, const AlignJobs jobs) {
+    if (blockIdx.y > 0) {                                  // copies of operands with misaligned rows ride along
+        align_rows(jobs.j[blockIdx.y - 1], blockIdx.x, gridDim.x);
+        return;
+    }
     const int64_t per = VEC ? m / 8 : m;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / per, c = i - r * per;
@@ -537,8 +541,14 @@ bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64
 
 template <typename T, int MODE, int CG>
 cudaError_t launch_gemm(const Maps& maps, const GemmArgs& g, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(gemm_kernel<T, MODE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<CG>::SMEM);
-    if (e != cudaSuccess) return e;
+    static bool attr[64] = {};   // set once per device of the process
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
+    if (dev < 0 || dev >= 64 || !attr[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<T, MODE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<CG>::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr[dev] = true;
+    }
     const int tiles = g.main.tiles_r * g.main.tiles_c * g.main.splits + g.grad.tiles_r * g.grad.tiles_c, slots = sm_count() / CG;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((tiles < slots ? tiles : slots) * CG));
@@ -573,14 +583,13 @@ struct Call {
     cudaStream_t stream;
 };
 
-// Move the operands that need it into `work` (consumed from its start).  Returns a status.
-int align_operands(Call& c, bool x, bool w) {
-    AlignJobs jobs = {};
-    if (x && !place_rows(jobs, c.X, c.ldx, c.tokens, c.n, 2, c.work, c.work_bytes)) return EXTERND_EINVAL;
+// Give the operands that need it a place in `work` (consumed from its start).  false: it is too small.
+bool place_operands(Call& c, bool x, bool w, AlignJobs& jobs) {
+    if (x && !place_rows(jobs, c.X, c.ldx, c.tokens, c.n, 2, c.work, c.work_bytes)) return false;
     if (w)
         for (int i = 0; i < 2; ++i)
-            if (!place_rows(jobs, c.W[i], c.ldw[i], c.m, c.n, 2, c.work, c.work_bytes)) return EXTERND_EINVAL;
-    return align_rows(jobs, c.stream) == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
+            if (!place_rows(jobs, c.W[i], c.ldw[i], c.m, c.n, 2, c.work, c.work_bytes)) return false;
+    return true;
 }
 
 template <typename T, int CG>
@@ -633,34 +642,34 @@ int forward(const Call& c) {
 }
 
 template <typename T, typename S, bool VEC>
-cudaError_t launch_gate_grad(const Call& c, T* dg, T* du, int64_t ldd) {
+cudaError_t launch_gate_grad(const Call& c, T* dg, T* du, int64_t ldd, const AlignJobs& jobs) {
     const int64_t items = c.tokens * (VEC ? c.m / 8 : c.m), cap = (int64_t)sm_count() * 32;
-    const unsigned grid = (unsigned)((items + 255) / 256 < cap ? (items + 255) / 256 : cap);
+    const dim3 grid((unsigned)((items + 255) / 256 < cap ? (items + 255) / 256 : cap), 1 + jobs.count);
     const T* h = (const T*)c.dH;
     const S *g = (const S*)c.S[0], *u = (const S*)c.S[1];
     switch (c.act) {
         case EXTERND_ACT_SILU:
-            gate_grad_kernel<T, S, EXTERND_ACT_SILU, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd);
+            gate_grad_kernel<T, S, EXTERND_ACT_SILU, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd, jobs);
             break;
         case EXTERND_ACT_GELU:
-            gate_grad_kernel<T, S, EXTERND_ACT_GELU, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd);
+            gate_grad_kernel<T, S, EXTERND_ACT_GELU, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd, jobs);
             break;
         case EXTERND_ACT_GELU_TANH:
-            gate_grad_kernel<T, S, EXTERND_ACT_GELU_TANH, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd);
+            gate_grad_kernel<T, S, EXTERND_ACT_GELU_TANH, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd, jobs);
             break;
         default:
-            gate_grad_kernel<T, S, EXTERND_ACT_RELU2, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd);
+            gate_grad_kernel<T, S, EXTERND_ACT_RELU2, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd, jobs);
             break;
     }
     return cudaGetLastError();
 }
 
 template <typename T, typename S>
-cudaError_t gate_grad(const Call& c, T* dg, T* du, int64_t ldd) {
+cudaError_t gate_grad(const Call& c, T* dg, T* du, int64_t ldd, const AlignJobs& jobs) {
     // whole vectors of 8 only where every row starts on a 16-byte boundary and ends with one
     const bool vec = c.m % 8 == 0 && c.lddh % 8 == 0 && c.lds % (16 / sizeof(S)) == 0 && aligned(c.dH, 16) && aligned(c.S[0], 16) &&
                      aligned(c.S[1], 16);
-    return vec ? launch_gate_grad<T, S, true>(c, dg, du, ldd) : launch_gate_grad<T, S, false>(c, dg, du, ldd);
+    return vec ? launch_gate_grad<T, S, true>(c, dg, du, ldd, jobs) : launch_gate_grad<T, S, false>(c, dg, du, ldd, jobs);
 }
 
 // Shares of the depth of dX's 2 m terms: with few tokens its tiles are few and long, and a tile is left to as many
@@ -713,7 +722,7 @@ int backward_tiles(const Call& c, const T* dg, const T* du, int64_t ldd, float* 
 }
 
 template <typename T>
-int backward(const Call& c) {
+int backward(const Call& c, const AlignJobs& jobs) {
     const int64_t ldd = round8(c.m);
     const size_t plane = plane_bytes(c.tokens, c.m, 2);
     const int splits = c.dX ? dx_splits(c.m, c.n, c.tokens) : 1;
@@ -721,7 +730,7 @@ int backward(const Call& c) {
     T* const dg = (T*)c.work;
     T* const du = (T*)(c.work + plane);
     float* const part = (float*)(c.work + 2 * plane);
-    const cudaError_t e = c.save_dtype == EXTERND_F32 ? gate_grad<T, float>(c, dg, du, ldd) : gate_grad<T, T>(c, dg, du, ldd);
+    const cudaError_t e = c.save_dtype == EXTERND_F32 ? gate_grad<T, float>(c, dg, du, ldd, jobs) : gate_grad<T, T>(c, dg, du, ldd, jobs);
     if (e != cudaSuccess) return EXTERND_ECUDA;
     // as for the forward pass: the stages the busiest worker goes through, weighted with a stage's measured time
     // (4096 x 6912 x 2560, whole pass: pairs 478 us, single CTAs 560, half as wide 795 with twice the stages)
@@ -798,7 +807,8 @@ int externd_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const
     }
     if (async_status && cudaMemsetAsync(async_status, 0, sizeof(int), c.stream) != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
     if (tokens == 0) return EXTERND_OK;
-    int rc = align_operands(c, true, true);
+    AlignJobs jobs = {};
+    int rc = !place_operands(c, true, true, jobs) ? EXTERND_EINVAL : launch_align(jobs, c.stream) != cudaSuccess ? EXTERND_ECUDA : EXTERND_OK;
     if (rc == EXTERND_OK) rc = dtype == EXTERND_F16 ? forward<__half>(c) : forward<__nv_bfloat16>(c);
     if (rc != EXTERND_OK) cudaGetLastError();
     return rc;
@@ -842,8 +852,9 @@ int externd_gated_backward(const void* dH, int64_t lddh, const void* X, int64_t 
         return EXTERND_OK;
     }
     if (!dX && !dw) return EXTERND_OK;
-    int rc = align_operands(c, dw, dX != nullptr);
-    if (rc == EXTERND_OK) rc = dtype == EXTERND_F16 ? backward<__half>(c) : backward<__nv_bfloat16>(c);
+    AlignJobs jobs = {};
+    int rc = place_operands(c, dw, dX != nullptr, jobs) ? EXTERND_OK : EXTERND_EINVAL;
+    if (rc == EXTERND_OK) rc = dtype == EXTERND_F16 ? backward<__half>(c, jobs) : backward<__nv_bfloat16>(c, jobs);
     if (rc != EXTERND_OK) cudaGetLastError();
     return rc;
 }

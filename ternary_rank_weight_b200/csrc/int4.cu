@@ -806,17 +806,23 @@ struct Product {
     cudaStream_t stream;
 };
 
-// dynamic shared memory beside at most 32 KB of static: what the 48 KB every kernel has do not hold
+// dynamic shared memory of a kernel, once per device of the process
 template <typename K>
-cudaError_t allow_smem(K kernel, int bytes) {
-    return bytes > 16 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) : cudaSuccess;
+cudaError_t allow_smem(K kernel, int bytes, bool (&done)[64]) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
+    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
 }
 
 template <typename X, typename T, int NM, int WORDS, bool AFFINE>
 cudaError_t launch_vec4(const Product& p) {
     const auto kernel = vec4_kernel<X, T, NM, WORDS, AFFINE>;
     constexpr int smem = VEC_WARPS * VEC_DEPTH * NM * 1024;
-    const cudaError_t e = allow_smem(kernel, smem);
+    static bool done[64] = {};
+    const cudaError_t e = allow_smem(kernel, smem, done);
     if (e != cudaSuccess) return e;
     const bool vec = row_aligned(p.x, p.batch, p.ldx, sizeof(X));
     kernel<<<(unsigned)((p.m + 15) / 16), VEC_WARPS * 32, smem, p.stream>>>(p.w0, p.w1, p.m, p.n, p.act, (const X*)p.x, p.ldx, (int)vec,
@@ -828,7 +834,8 @@ template <typename X, typename T, int NM, int WORDS, bool AFFINE, int N>
 cudaError_t launch_tile4(const Product& p) {
     const auto kernel = tile4_kernel<X, T, N, NM, WORDS, AFFINE>;
     constexpr int smem = tc_smem<X, N>();
-    const cudaError_t e = allow_smem(kernel, smem);
+    static bool done[64] = {};
+    const cudaError_t e = allow_smem(kernel, smem, done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.m + 128 / NM - 1) / (128 / NM), cols = (p.batch + N - 1) / N, blocks = (p.n + 127) / 128;
     // shares of the columns: the fewest rounds of CTAs times the blocks of a share, each CTA costing about
@@ -897,7 +904,7 @@ int products(const Mat4& w0, const Mat4& w1, int64_t m, int64_t n, int group, in
     unsigned char* place = (unsigned char*)work;
     if (batch > VEC_BATCH && !place_rows(jobs, X, ldx, batch, n, eb, place, work_bytes)) return EXTERND_EINVAL;
     const Product p = {w0, w1, m, n, group, act, X, ldx, batch, Y, ldy, s};
-    cudaError_t e = align_rows(jobs, s);
+    cudaError_t e = launch_align(jobs, s);
     if (e != cudaSuccess) { cudaGetLastError(); return EXTERND_ECUDA; }
     switch (dtype) {
         case EXTERND_F32: e = run_product<float, __nv_bfloat16, NM>(p); break;

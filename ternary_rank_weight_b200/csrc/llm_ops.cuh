@@ -241,13 +241,14 @@ __device__ __forceinline__ void planes8(const F8& r, uint32_t (&v)[3][4]) {
 struct AlignJob { const unsigned short* src; int64_t lds; unsigned short* dst; int64_t ldd; int64_t rows, cols; };
 struct AlignJobs { AlignJob j[3]; int count; };
 
-static __global__ void __launch_bounds__(256) align_rows_kernel(const AlignJobs jobs) {
-    const AlignJob& j = jobs.j[blockIdx.y];
+// a block of 256 threads, `block` of `count`
+__device__ __forceinline__ void align_rows(const AlignJob& j, int64_t block, int64_t count) {
     const int lane = threadIdx.x & 31;
-    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < j.rows; r += (int64_t)gridDim.x * 8)
+    for (int64_t r = block * 8 + (threadIdx.x >> 5); r < j.rows; r += count * 8)
         for (int64_t k = 8 * lane; k < j.cols; k += 256)
             *reinterpret_cast<uint4*>(j.dst + r * j.ldd + k) = load8(j.src + r * j.lds, k, j.cols, false);
 }
+static __global__ void __launch_bounds__(256) align_rows_kernel(const AlignJobs jobs) { align_rows(jobs.j[blockIdx.y], blockIdx.x, gridDim.x); }
 
 inline int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
 inline bool row_aligned(const void* p, int64_t rows, int64_t ld, size_t bytes) { return aligned(p, 16) && (rows < 2 || ld * bytes % 16 == 0); }
@@ -275,7 +276,7 @@ inline bool place_rows(AlignJobs& jobs, const void*& p, int64_t& ld, int64_t row
     return true;
 }
 
-inline cudaError_t align_rows(const AlignJobs& jobs, cudaStream_t stream) {
+inline cudaError_t launch_align(const AlignJobs& jobs, cudaStream_t stream) {
     if (jobs.count == 0) return cudaSuccess;
     int64_t rows = 1;
     for (int i = 0; i < jobs.count; ++i) rows = rows > jobs.j[i].rows ? rows : jobs.j[i].rows;
