@@ -198,6 +198,54 @@ def test_shapes_strides_and_partial_gradients():
     assert torch.all(out == 5.0)
 
 
+@pytest.mark.parametrize("t,m,n", [(40, 2000, 300), (100, 640, 128), (200, 3000, 40), (130, 513, 1000)])
+def test_split_depth_of_few_tokens(t, m, n):
+    """With few tokens the 2 m terms of dX are summed in shares."""
+    X, Wg, Wu, dH = _make(t, m, n, BF16, seed=4)
+    _, G, Up = ext.gated_forward(X, Wg, Wu, "gelu")
+    got = ext.gated_backward(dH, X, Wg, Wu, G, Up, "gelu")
+    _check_backward(X, Wg, Wu, dH, "gelu", G, Up, got)
+    again = ext.gated_backward(dH, X, Wg, Wu, G, Up, "gelu", need=(True, False, False))
+    assert torch.equal(again[0], got[0])
+
+
+def test_one_vector_and_broadcast_gradient():
+    X, Wg, Wu, _ = _make(1, 70, 40, BF16, seed=5)
+    H, G, Up = ext.gated_forward(X[0], Wg, Wu)
+    assert H.shape == G.shape == (70,)
+    dH = torch.ones(1, dtype=BF16, device="cuda").expand(70)
+    dX, dWg, dWu = ext.gated_backward(dH, X[0], Wg, Wu, G, Up)
+    assert dX.shape == (40,)
+    _check_backward(X, Wg, Wu, dH.contiguous()[None], "silu", G[None], Up[None], (dX[None], dWg, dWu))
+
+
+def test_calls_on_two_streams_at_once():
+    a, b = _make(300, 700, 400, BF16, seed=6), _make(20, 900, 640, BF16, seed=7)
+    refs = [ext.gated_forward(*v[:3]) for v in (a, b)]
+    grads = [ext.gated_backward(v[3], *v[:3], *r[1:]) for v, r in zip((a, b), refs)]
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = []
+    for _ in range(10):
+        for i, v in enumerate((a, b)):
+            f = ext.gated_forward(*v[:3], stream=s[i])
+            outs.append((i, f, ext.gated_backward(v[3], *v[:3], *f[1:], stream=s[i])))
+    torch.cuda.synchronize()
+    for i, f, g in outs:
+        assert all(torch.equal(p, q) for p, q in zip((*f, *g), (*refs[i], *grads[i])))
+
+
+def test_results_past_32_bit_offsets():
+    """2.4 G entries of H: the last tokens' are those of a call of their own."""
+    t, m, n = 40100, 60000, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    X = torch.randn(t, n, generator=g, device="cuda").to(BF16)
+    Wg, Wu = (torch.randn(m, n, generator=g, device="cuda").to(BF16) * 0.125 for _ in range(2))
+    H = ext.gated(X, Wg, Wu)
+    assert torch.equal(H[-100:], ext.gated(X[-100:], Wg, Wu)) and torch.equal(H[:100], ext.gated(X[:100], Wg, Wu))
+
+
 def test_no_tokens():
     X, Wg, Wu, dH = _make(4, 40, 24, F16)
     H, G, Up = ext.gated_forward(X[:0], Wg, Wu)

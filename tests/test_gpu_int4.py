@@ -251,6 +251,52 @@ def test_products_repeat_bit_for_bit_on_streams_and_in_graphs():
         assert torch.equal(v, ext.int4_dequantize(ext.int4_quantize(A, 64)))
 
 
+@pytest.mark.parametrize("blocks", range(1, 12))
+def test_every_share_of_the_columns(blocks):
+    """More than 8 vectors split a tile's columns over 1 to 8 CTAs, whose sums meet in a fixed order."""
+    n = 128 * blocks - 5
+    w, X = _random_weights(150, n, 32, True, seed=blocks), _vectors(20, n, blocks, F16)
+    W, mag = _values64(w)
+    y = X.double() @ W.t()
+    got = ext.int4_matvec(w, X)
+    assert torch.all((got.double() - y).abs() <= _sum_bound(w, mag, X) * (1 + 2.0 ** -8) + half_step(F16, y))
+    assert torch.equal(got, ext.int4_matvec(w, X))
+
+
+def test_calls_on_two_streams_at_once():
+    w, big = _random_weights(700, 2000, 64, True, seed=1), _random_weights(3000, 1024, 128, False, seed=2)
+    X, Z = _vectors(30, 2000, 1, BF16), _vectors(5, 1024, 2, F32)
+    ref, ref2 = ext.int4_matvec(w, X), ext.int4_matvec(big, Z)
+    torch.cuda.synchronize()
+    s, r = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(20):
+        outs.append((ext.int4_matvec(w, X, stream=s), ext.int4_matvec(big, Z, stream=r), ext.int4_gated(w, w, X, stream=r)))
+    torch.cuda.synchronize()
+    h = ext.int4_gated(w, w, X)
+    assert all(torch.equal(a, ref) and torch.equal(b, ref2) and torch.equal(c, h) for a, b, c in outs)
+
+
+def test_matrices_past_32_bit_offsets():
+    """Codes of more than 4 GiB: the last rows are the last rows."""
+    m, n, group = 70001, 131072, 128
+    q = torch.randint(0, 256, (m, ext.int4_row_bytes(n)), dtype=torch.uint8, device="cuda")
+    s = torch.rand(n // group, m, device="cuda").half() * 0.01
+    w = ext.Int4Weights(q, s, None, m, n, group)
+    tail = ext.Int4Weights(q[-40:].clone(), s[:, -40:].contiguous(), None, 40, n, group)
+    for t in (1, 12):
+        X = _vectors(t, n, t, F16)
+        assert torch.equal(ext.int4_matvec(w, X)[:, -40:], ext.int4_matvec(tail, X))
+    del q, w
+    A = torch.zeros(40001, 65536, dtype=F16, device="cuda")          # 2.6 G entries, 5 GB
+    A[-3:] = _matrix(3, 65536, 1, F16)
+    w = ext.int4_quantize(A, 128)
+    ref = ext.int4_quantize(A[-3:].clone(), 128)
+    assert torch.equal(w.q[-3:], ref.q) and torch.equal(w.scale[:, -3:], ref.scale) and torch.equal(w.offset[:, -3:], ref.offset)
+    v = ext.int4_dequantize(w, F16)
+    assert torch.equal(v[-3:], ext.int4_dequantize(ref, F16)) and not v[:-3].any()
+
+
 def test_library_refuses_bad_arguments():
     L, einval = ext._lib.load(), ext.STATUS["EINVAL"]
     w = _random_weights(20, 100, 64, True, seed=1)
