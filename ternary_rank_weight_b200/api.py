@@ -831,17 +831,24 @@ def _gated(X, Wg, Wu, act, save, out, async_status, stream):
         t = X2.shape[0]
         H = _result(None if out is None else out.view(-1, m), t, m, X2)
         G = U = None
+        lds = m
         if save is not None:
-            G, U = X2.new_empty(shape, dtype=save), X2.new_empty(shape, dtype=save)
+            # rows on 16-byte boundaries: the kernels store and load them whole
+            lds = (m + 7) // 8 * 8
+            G, U = X2.new_empty((t, lds), dtype=save), X2.new_empty((t, lds), dtype=save)
+            if lds != m:
+                G, U = G[:, :m], U[:, :m]
         nbytes = bx + bg + bu
         work = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if nbytes else None
         kept = t and save is not None
         rc = _lib.load().externd_gated(x, ldx, wg, ldg, wu, ldu, _DTYPE[dtype], m, n, t, code, H.data_ptr(),
                                        m if out is None else _ld(H), G.data_ptr() if kept else None,
-                                       U.data_ptr() if kept else None, _DTYPE[save or dtype], m, _ptr(work), nbytes,
+                                       U.data_ptr() if kept else None, _DTYPE[save or dtype], lds, _ptr(work), nbytes,
                                        _ptr(async_status), _handle_of(dev.index))
     _check(rc, "externd_gated")
-    return (H if two else H.view(shape)), G, U
+    if two:
+        return H, G, U
+    return H.view(shape), None if G is None else G.view(shape), None if U is None else U.view(shape)
 
 
 def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", *, out: Optional[torch.Tensor] = None,
@@ -856,7 +863,8 @@ def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu"
 def gated_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", *,
                   save_dtype: torch.dtype = torch.float32, async_status=None, stream=None):
     """(H, G, U): gated() with the projections G = X Wg^T and U = X Wu^T that gated_backward needs, in
-    float32, or in X's type (half the memory; their rounding then adds to the gradients' errors)."""
+    float32, or in X's type (half the memory; their rounding then adds to the gradients' errors).  G's and
+    U's rows start on 16-byte boundaries: with m not a multiple of 8 they are not contiguous."""
     if save_dtype is None:
         raise ValueError("the projections can be saved in float32 or in X's type")
     return _gated(X, Wg, Wu, act, save_dtype, None, async_status, stream)

@@ -99,35 +99,39 @@ __device__ __forceinline__ bool tile_of(const GemmArgs& g, int worker, int worke
     return true;
 }
 
+// piece i of a staged row r sits at piece i ^ (r / 2 % 4)
+__device__ __forceinline__ int staged(int r, int i) { return r * STG_ROW + ((i ^ (r >> 1 & 3)) << 4); }
+
+// the warp's staged rows to global memory, as units of U: neighbouring lanes write neighbouring units
+template <typename U, typename T>
+__device__ __forceinline__ void store_units(const unsigned char* stg_ptr, T* out, int64_t ld, int rows, int cols, int lane) {
+    constexpr int LANES = 64 / sizeof(U), STEP = 32 / LANES;       // lanes of a row, rows at a time
+    const int r0 = lane / LANES, byte = lane % LANES * (int)sizeof(U);
+    const int last = byte < cols * (int)sizeof(T) ? rows : 0;      // units lie inside the columns: all of them, or units of one
+    unsigned char* o = reinterpret_cast<unsigned char*>(out + r0 * ld) + byte;
+    #pragma unroll 8
+    for (int r = r0; r < 32; r += STEP, o += STEP * ld * sizeof(T))
+        if (r < last) *reinterpret_cast<U*>(o) = *reinterpret_cast<const U*>(stg_ptr + staged(r, byte >> 4) + (byte & 15));
+}
+
 // 64 bytes of each of a warp's 32 rows (a row per lane, 16 registers) to global memory through the warp's staging
-// buffer, so that neighbouring lanes write neighbouring 16 bytes
+// buffer, in the widest units that the rows' starts allow
 template <typename T>
 __device__ __forceinline__ void store64(const uint32_t* v, uint32_t stg, const unsigned char* stg_ptr, T* out, int64_t ld, int row0, int rows,
                                         int col0, int cols, int lane) {
-    constexpr int E = 16 / sizeof(T);         // outputs of a 16-byte piece
-    // piece i of row r sits at piece i ^ (r / 2 % 4)
-    const auto at = [](int r, int i) { return r * STG_ROW + ((i ^ (r >> 1 & 3)) << 4); };
     #pragma unroll
     for (int i = 0; i < 4; ++i)
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(stg + at(lane, i)), "r"(v[4 * i]), "r"(v[4 * i + 1]), "r"(v[4 * i + 2]),
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(stg + staged(lane, i)), "r"(v[4 * i]), "r"(v[4 * i + 1]), "r"(v[4 * i + 2]),
                      "r"(v[4 * i + 3]) : "memory");
     __syncwarp();
-    const bool vec = col0 + 4 * E <= cols && ld % E == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-    if (vec) {
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2), c = lane & 3;
-            const uint4 w = *reinterpret_cast<const uint4*>(stg_ptr + at(r, c));
-            if (row0 + r < rows) *reinterpret_cast<uint4*>(out + (int64_t)(row0 + r) * ld + col0 + E * c) = w;
-        }
-    } else {
-        #pragma unroll 4
-        for (int r = 0; r < 32; r += 32 / (4 * E)) {
-            const int rr = 4 * E == 32 ? r : r + (lane >> 4), c = 4 * E == 32 ? lane : lane & 15;
-            const T w = *reinterpret_cast<const T*>(stg_ptr + at(rr, c / E) + (int)sizeof(T) * (c % E));
-            if (row0 + rr < rows && col0 + c < cols) out[(int64_t)(row0 + rr) * ld + col0 + c] = w;
-        }
-    }
+    T* const o = out + (int64_t)row0 * ld + col0;
+    const int nr = min(32, rows - row0), nc = min((int)(64 / sizeof(T)), cols - col0);
+    const uint32_t starts = (uint32_t)(reinterpret_cast<uintptr_t>(out) | (uintptr_t)(ld * sizeof(T)));
+    if (nc < (int)(64 / sizeof(T))) store_units<T>(stg_ptr, o, ld, nr, nc, lane);
+    else if ((starts & 15) == 0) store_units<uint4>(stg_ptr, o, ld, nr, nc, lane);
+    else if ((starts & 7) == 0) store_units<uint2>(stg_ptr, o, ld, nr, nc, lane);
+    else if ((starts & 3) == 0) store_units<uint32_t>(stg_ptr, o, ld, nr, nc, lane);
+    else store_units<T>(stg_ptr, o, ld, nr, nc, lane);
     __syncwarp();
 }
 
@@ -363,53 +367,37 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
 // tensor cores need.  Against a step that keeps everything in 32 bits this rounding makes the gradients' error
 // 1.4 times theirs (the output's rounding alone); G and U saved in 16 bits (S = T) make it 1.8 times, with
 // relu2, which doubles their relative error, 2.5 times.
-template <typename S> struct Saved8;                                       // 8 saved values
-template <> struct Saved8<float> {
-    float4 a, b;
-    __device__ __forceinline__ explicit Saved8(const float* p) {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    }
-    __device__ __forceinline__ float2 pair(int e) const {
-        return e == 0 ? make_float2(a.x, a.y) : e == 1 ? make_float2(a.z, a.w) : e == 2 ? make_float2(b.x, b.y) : make_float2(b.z, b.w);
-    }
-};
-template <typename T> struct Saved8 {
-    uint4 a;
-    __device__ __forceinline__ explicit Saved8(const T* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ float2 pair(int e) const { return unpack2<T>(e == 0 ? a.x : e == 1 ? a.y : e == 2 ? a.z : a.w); }
-};
+template <typename T> __device__ __forceinline__ float2 pair_of(const uint4& v, int e) {
+    return unpack2<T>(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
+}
+template <typename T> __device__ __forceinline__ float2 pair_of(const F8& v, int e) {
+    return e == 0 ? make_float2(v.a.x, v.a.y) : e == 1 ? make_float2(v.a.z, v.a.w) : e == 2 ? make_float2(v.b.x, v.b.y) : make_float2(v.b.z, v.b.w);
+}
 
-template <typename T, typename S, int ACT, bool VEC>
-__global__ void __launch_bounds__(256) gate_grad_kernel(const T* __restrict__ dh, int64_t lddh, const S* __restrict__ gs,
-                                                        const S* __restrict__ us, int64_t ldgu, int64_t rows, int64_t m,
+// 8 columns a thread; hvec, svec: dH's rows, G's and U's, start on 16-byte boundaries.  S: float, or the operands' 16 bits.
+template <typename T, typename S, int ACT>
+__global__ void __launch_bounds__(256) gate_grad_kernel(const T* __restrict__ dh, int64_t lddh, int hvec, const S* __restrict__ gs,
+                                                        const S* __restrict__ us, int64_t ldgu, int svec, int64_t rows, int64_t m,
                                                         T* __restrict__ dg, T* __restrict__ du, int64_t ldw, const AlignJobs jobs) {
     if (blockIdx.y > 0) {                                  // copies of operands with misaligned rows ride along
         align_rows(jobs.j[blockIdx.y - 1], blockIdx.x, gridDim.x);
         return;
     }
-    const int64_t per = VEC ? m / 8 : m;
+    const int64_t per = ldw / 8;                           // ldw: m rounded up to 8
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / per, c = i - r * per;
-        if (VEC) {
-            const Saved8<T> h8(dh + r * lddh + 8 * c);
-            const Saved8<S> g8(gs + r * ldgu + 8 * c), u8(us + r * ldgu + 8 * c);
-            uint32_t og[4], ou[4];
-            #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 h = h8.pair(e), g = g8.pair(e), u = u8.pair(e);
-                const float2 a = act_both<ACT, false>(g.x), b = act_both<ACT, false>(g.y);
-                og[e] = pack2<T>(h.x * u.x * a.y, h.y * u.y * b.y);
-                ou[e] = pack2<T>(h.x * a.x, h.y * b.x);
-            }
-            *(reinterpret_cast<uint4*>(dg + r * ldw) + c) = make_uint4(og[0], og[1], og[2], og[3]);
-            *(reinterpret_cast<uint4*>(du + r * ldw) + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
-        } else {
-            const float h = to_f32(dh[r * lddh + c]), g = to_f32(gs[r * ldgu + c]), u = to_f32(us[r * ldgu + c]);
-            const float2 a = act_both<ACT, false>(g);
-            dg[r * ldw + c] = from_f32<T>(h * u * a.y);
-            du[r * ldw + c] = from_f32<T>(h * a.x);
+        const int64_t r = i / per, k = 8 * (i - r * per);
+        const uint4 h8 = load8(reinterpret_cast<const unsigned short*>(dh + r * lddh), k, m, hvec);
+        const auto g8 = load8(gs + r * ldgu, k, m, svec), u8 = load8(us + r * ldgu, k, m, svec);
+        uint32_t og[4], ou[4];
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 h = pair_of<T>(h8, e), g = pair_of<T>(g8, e), u = pair_of<T>(u8, e);
+            const float2 a = act_both<ACT, false>(g.x), b = act_both<ACT, false>(g.y);
+            og[e] = pack2<T>(h.x * u.x * a.y, h.y * u.y * b.y);
+            ou[e] = pack2<T>(h.x * a.x, h.y * b.x);
         }
+        *reinterpret_cast<uint4*>(dg + r * ldw + k) = make_uint4(og[0], og[1], og[2], og[3]);
+        *reinterpret_cast<uint4*>(du + r * ldw + k) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
     }
 }
 
@@ -647,35 +635,29 @@ int forward(const Call& c) {
     return forward_tiles<T>(c);
 }
 
-template <typename T, typename S, bool VEC>
-cudaError_t launch_gate_grad(const Call& c, T* dg, T* du, int64_t ldd, const AlignJobs& jobs) {
-    const int64_t items = c.tokens * (VEC ? c.m / 8 : c.m), cap = (int64_t)sm_count() * 32;
-    const dim3 grid((unsigned)((items + 255) / 256 < cap ? (items + 255) / 256 : cap), 1 + jobs.count);
-    const T* h = (const T*)c.dH;
-    const S *g = (const S*)c.S[0], *u = (const S*)c.S[1];
-    switch (c.act) {
-        case EXTERND_ACT_SILU:
-            gate_grad_kernel<T, S, EXTERND_ACT_SILU, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd, jobs);
-            break;
-        case EXTERND_ACT_GELU:
-            gate_grad_kernel<T, S, EXTERND_ACT_GELU, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd, jobs);
-            break;
-        case EXTERND_ACT_GELU_TANH:
-            gate_grad_kernel<T, S, EXTERND_ACT_GELU_TANH, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd, jobs);
-            break;
-        default:
-            gate_grad_kernel<T, S, EXTERND_ACT_RELU2, VEC><<<grid, 256, 0, c.stream>>>(h, c.lddh, g, u, c.lds, c.tokens, c.m, dg, du, ldd, jobs);
-            break;
+template <typename T, typename S, int ACT>
+void launch_gate_grad(const Call& c, T* dg, T* du, int64_t ldd, const AlignJobs& jobs) {
+    const int64_t items = c.tokens * (ldd / 8), cap = (int64_t)sm_count() * 32;
+    int64_t want = (items + 255) / 256;
+    for (int i = 0; i < jobs.count; ++i) {
+        const int64_t n = (jobs.j[i].rows * ((jobs.j[i].cols + 255) / 256) + 7) / 8;
+        want = want > n ? want : n;
     }
-    return cudaGetLastError();
+    const dim3 grid((unsigned)(want < cap ? want : cap), 1 + jobs.count);
+    gate_grad_kernel<T, S, ACT><<<grid, 256, 0, c.stream>>>(
+        (const T*)c.dH, c.lddh, row_aligned(c.dH, c.tokens, c.lddh, 2), (const S*)c.S[0], (const S*)c.S[1], c.lds,
+        row_aligned(c.S[0], c.tokens, c.lds, sizeof(S)) && row_aligned(c.S[1], c.tokens, c.lds, sizeof(S)), c.tokens, c.m, dg, du, ldd, jobs);
 }
 
 template <typename T, typename S>
 cudaError_t gate_grad(const Call& c, T* dg, T* du, int64_t ldd, const AlignJobs& jobs) {
-    // whole vectors of 8 only where every row starts on a 16-byte boundary and ends with one
-    const bool vec = c.m % 8 == 0 && c.lddh % 8 == 0 && c.lds % (16 / sizeof(S)) == 0 && aligned(c.dH, 16) && aligned(c.S[0], 16) &&
-                     aligned(c.S[1], 16);
-    return vec ? launch_gate_grad<T, S, true>(c, dg, du, ldd, jobs) : launch_gate_grad<T, S, false>(c, dg, du, ldd, jobs);
+    switch (c.act) {
+        case EXTERND_ACT_SILU: launch_gate_grad<T, S, EXTERND_ACT_SILU>(c, dg, du, ldd, jobs); break;
+        case EXTERND_ACT_GELU: launch_gate_grad<T, S, EXTERND_ACT_GELU>(c, dg, du, ldd, jobs); break;
+        case EXTERND_ACT_GELU_TANH: launch_gate_grad<T, S, EXTERND_ACT_GELU_TANH>(c, dg, du, ldd, jobs); break;
+        default: launch_gate_grad<T, S, EXTERND_ACT_RELU2>(c, dg, du, ldd, jobs); break;
+    }
+    return cudaGetLastError();
 }
 
 // Shares of the depth of dX's 2 m terms: with few tokens its tiles are few and long, and a tile is left to as many
@@ -736,7 +718,7 @@ int backward(const Call& c, const AlignJobs& jobs) {
     T* const dg = (T*)c.work;
     T* const du = (T*)(c.work + plane);
     float* const part = (float*)(c.work + 2 * plane);
-    const cudaError_t e = c.save_dtype == EXTERND_F32 ? gate_grad<T, float>(c, dg, du, ldd, jobs) : gate_grad<T, T>(c, dg, du, ldd, jobs);
+    const cudaError_t e = c.save_dtype == EXTERND_F32 ? gate_grad<T, float>(c, dg, du, ldd, jobs) : gate_grad<T, unsigned short>(c, dg, du, ldd, jobs);
     if (e != cudaSuccess) return EXTERND_ECUDA;
     // as for the forward pass: the stages the busiest worker goes through, weighted with a stage's measured time
     // (4096 x 6912 x 2560, whole pass: pairs 478 us, single CTAs 560, half as wide 795 with twice the stages)

@@ -104,6 +104,11 @@ __global__ void __launch_bounds__(256) quantize_kernel(const T* __restrict__ A, 
                 #pragma unroll
                 for (int h = 0; h < (int)sizeof(T) / 2; ++h)
                     reinterpret_cast<uint4*>(w[u])[h] = __ldcs(reinterpret_cast<const uint4*>(arow + j0) + h);
+            } else if (j0 + 8 <= n) {
+                using E = typename std::conditional<sizeof(T) == 4, float, unsigned short>::type;
+                const auto v = load8(reinterpret_cast<const E*>(arow), j0, n, false);
+                static_assert(sizeof(v) == sizeof(w[u]), "eight entries");
+                memcpy(w[u], &v, sizeof(v));
             } else {
                 // columns past the last one repeat the group's first: they change no extreme
                 const int64_t g0 = j0 >> LG << LG;

@@ -235,18 +235,20 @@ __device__ __forceinline__ void planes8(const F8& r, uint32_t (&v)[3][4]) {
 
 // ---- operands whose rows do not start on 16-byte boundaries ---------------------------------------------
 
-// Up to three matrices are laid out in rows that do, in one launch: a warp a row, 16 bytes a lane.  TMA needs that,
+// Up to three matrices are laid out in rows that do, in one launch, 16 bytes a lane.  TMA needs that,
 // and wide loads; such operands are odd-sized ones, a model's own sizes hardly ever come here.
 // Elements count as 16-bit ones (an fp32 as two).
 struct AlignJob { const unsigned short* src; int64_t lds; unsigned short* dst; int64_t ldd; int64_t rows, cols; };
 struct AlignJobs { AlignJob j[3]; int count; };
 
-// a block of 256 threads, `block` of `count`
+// a block of 256 threads, `block` of `count`: a warp takes 256 columns of a row at a time
 __device__ __forceinline__ void align_rows(const AlignJob& j, int64_t block, int64_t count) {
     const int lane = threadIdx.x & 31;
-    for (int64_t r = block * 8 + (threadIdx.x >> 5); r < j.rows; r += count * 8)
-        for (int64_t k = 8 * lane; k < j.cols; k += 256)
-            *reinterpret_cast<uint4*>(j.dst + r * j.ldd + k) = load8(j.src + r * j.lds, k, j.cols, false);
+    const int64_t per = (j.cols + 255) / 256;
+    for (int64_t i = block * 8 + (threadIdx.x >> 5); i < j.rows * per; i += count * 8) {
+        const int64_t r = i / per, k = 256 * (i - r * per) + 8 * lane;
+        if (k < j.cols) *reinterpret_cast<uint4*>(j.dst + r * j.ldd + k) = load8(j.src + r * j.lds, k, j.cols, false);
+    }
 }
 static __global__ void __launch_bounds__(256) align_rows_kernel(const AlignJobs jobs) { align_rows(jobs.j[blockIdx.y], blockIdx.x, gridDim.x); }
 
@@ -278,9 +280,12 @@ inline bool place_rows(AlignJobs& jobs, const void*& p, int64_t& ld, int64_t row
 
 inline cudaError_t launch_align(const AlignJobs& jobs, cudaStream_t stream) {
     if (jobs.count == 0) return cudaSuccess;
-    int64_t rows = 1;
-    for (int i = 0; i < jobs.count; ++i) rows = rows > jobs.j[i].rows ? rows : jobs.j[i].rows;
-    const int64_t want = (rows + 7) / 8, cap = (int64_t)sm_count() * 8;
+    int64_t items = 1;
+    for (int i = 0; i < jobs.count; ++i) {
+        const int64_t n = jobs.j[i].rows * ((jobs.j[i].cols + 255) / 256);
+        items = items > n ? items : n;
+    }
+    const int64_t want = (items + 7) / 8, cap = (int64_t)sm_count() * 8;
     align_rows_kernel<<<dim3((unsigned)(want < cap ? want : cap), (unsigned)jobs.count), 256, 0, stream>>>(jobs);
     return cudaGetLastError();
 }
