@@ -301,11 +301,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
 
 __device__ __forceinline__ uint32_t word_of(const uint4& q, int i) { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; }
 
-// d += (16 rows' codes of one word span) x (8 vectors' entries), all planes, least significant first
+// (16 rows' codes of one word span) x (8 vectors' entries): the most significant plane into hi, the others into lo,
+// whose roundings are then 2^-8 as large
 template <typename T, int PLANES>
-__device__ __forceinline__ void span_mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[4], const uint32_t (&x)[PLANES][4]) {
+__device__ __forceinline__ void span_mma(float (&hi)[4], float (&lo)[4], const uint32_t (&a)[4], const uint32_t (&b)[4], const uint32_t (&x)[PLANES][4]) {
     #pragma unroll
     for (int p = PLANES - 1; p >= 0; --p) {
+        float(&d)[4] = p == 0 ? hi : lo;
         mma16816<T>(d, a[0], b[0], a[1], b[1], x[p][0], x[p][1]);
         mma16816<T>(d, a[2], b[2], a[3], b[3], x[p][2], x[p][3]);
     }
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(VEC_WARPS * 32) vec4_kernel(Mat4 w0, Mat4 w1, 
             #pragma unroll
             for (int h = 0; h < 2; ++h)
                 code[j][h] = lds128(mine + slot + (2 * j + h) * 512);
-        float acc[NM][4] = {}, sum = 0.0f;
+        float acc[NM][4] = {}, low[NM][4] = {}, sum = 0.0f;      // low: planes 1 and 2 of fp32 entries
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t xv[PLANES][4];
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(VEC_WARPS * 32) vec4_kernel(Mat4 w0, Mat4 w1, 
                 uint32_t a[4], b[4];
                 codes8<T>(word_of(code[j][0], i), a);
                 codes8<T>(word_of(code[j][1], i), b);
-                span_mma<T, PLANES>(acc[j], a, b, xv);
+                span_mma<T, PLANES>(acc[j], low[j], a, b, xv);
             }
             if (AFFINE) sum += sum8(xs[i], (T*)nullptr);
             if ((i + 1) % WORDS == 0) {                  // the group ends here
@@ -458,6 +460,13 @@ __global__ void __launch_bounds__(VEC_WARPS * 32) vec4_kernel(Mat4 w0, Mat4 w1, 
                 #pragma unroll
                 for (int j = 0; j < NM; ++j) {
                     const float sa = __half2float(sg[j * FAR * GROUPS * 16]), sb = __half2float(sg[j * FAR * GROUPS * 16 + 8]);
+                    if (PLANES > 1) {
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            acc[j][e] += low[j][e];
+                            low[j][e] = 0.0f;
+                        }
+                    }
                     out[j][0] = fmaf(sa, acc[j][0], out[j][0]);
                     out[j][1] = fmaf(sa, acc[j][1], out[j][1]);
                     out[j][2] = fmaf(sb, acc[j][2], out[j][2]);
@@ -679,17 +688,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
                 fence_after();
                 const uint32_t acc = tmem + d * N;
                 if (leader) {
+                    // the least significant plane first: only the last one's sums are rounded at the result's magnitude
                     #pragma unroll
-                    for (int k = 0; k < 2 * WORDS; ++k) {
-                        const int kk = g * 2 * WORDS + k;    // 16 columns of the block: half kk / 4, 32 bytes each
+                    for (int q = PLANES - 1; q >= 0; --q)
                         #pragma unroll
-                        for (int q = PLANES - 1; q >= 0; --q) {
+                        for (int k = 0; k < 2 * WORDS; ++k) {
+                            const int kk = g * 2 * WORDS + k;    // 16 columns of the block: half kk / 4, 32 bytes each
                             const uint64_t db = da + ((128 * 256 + q * N * 256 + (kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4);
                             const bool more = k > 0 || q < PLANES - 1;
                             mma_f16<1>(acc, da + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4), db, idesc, more);
                             if (AFFINE) mma_f16<1>(acc + TC_BUFS * N, one, db, idesc, more);
                         }
-                    }
                     mma_commit<1>(dfull0 + 8 * d);
                     if (g == GROUPS - 1) mma_commit<1>(empty0 + 8 * s);
                 }
