@@ -4,7 +4,7 @@
 //
 // Few tokens: the weights stream once through the warp-level products (dense_stream_kernel).  Otherwise one
 // persistent kernel on the 5th-generation tensor cores (gemm_kernel): TMA brings 64-deep operand slabs into
-// a ring of swizzled shared-memory stages, one thread issues tcgen05.mma into tensor memory, four warps drain
+// a ring of swizzled shared-memory stages, one thread issues tcgen05.mma into tensor memory, eight warps drain
 // a finished accumulator while the next one fills.  It runs as
 //   FWD  both projections of a tile in one accumulator, activation and product in the epilogue;
 //   BWD  two lists of tiles: dX = dG Wg + dU Wu as one sum of 2 m terms (weights read along their columns, as
@@ -14,7 +14,6 @@
 #include <type_traits>
 
 #include "sm100.cuh"
-
 
 namespace externd_ffn {
 
@@ -91,11 +90,11 @@ __device__ __forceinline__ bool tile_of(const GemmArgs& g, int worker, int worke
         return true;
     }
     const int more = nm % workers, few = workers - more;
-    const int round = i - mine + (worker < more ? g.skip : 0);
-    const int t = round < g.skip ? round * few + worker - more : g.skip * few + (round - g.skip) * workers + worker;
+    const int64_t round = (int64_t)i - mine + (worker < more ? g.skip : 0);
+    const int64_t t = round < g.skip ? round * few + worker - more : (int64_t)g.skip * few + (round - g.skip) * workers + worker;
     if (t >= ng) return false;
     o.grad = true;
-    tile_at(t, g.grad, o);
+    tile_at((int)t, g.grad, o);
     return true;
 }
 
@@ -661,14 +660,16 @@ cudaError_t gate_grad(const Call& c, T* dg, T* du, int64_t ldd, const AlignJobs&
 }
 
 // Shares of the depth of dX's 2 m terms: with few tokens its tiles are few and long, and a tile is left to as many
-// workers as there are for each (64 tokens x 6912 x 2560: 88 us without).  For the widest tiles; narrower ones have
-// no fewer workers each.
+// workers as there are for each (the backward pass of 64 tokens x 6912 x 2560 took 88 us without).  Below 64 stages (24 us)
+// the launch that adds the shares up would take back what they save.  For the widest tiles; narrower ones have no
+// fewer workers each.
 constexpr int MAX_SPLITS = 16;
 int dx_splits(int64_t m, int64_t n, int64_t tokens) {
-    const int64_t tiles = (int64_t)ceil_div(tokens, 128) * ceil_div(n, 256), most = ceil_div(m, BK) / 4;
+    const int64_t tiles = (int64_t)ceil_div(tokens, 128) * ceil_div(n, 256), stages = 2 * (int64_t)ceil_div(m, BK);
+    if (stages < 64) return 1;
     int64_t s = sm_count() / tiles;
     s = s < MAX_SPLITS ? s : MAX_SPLITS;
-    s = s < most ? s : most;
+    s = s < stages / 8 ? s : stages / 8;
     return s < 1 ? 1 : (int)s;
 }
 size_t share_bytes(int64_t m, int64_t n, int64_t tokens) {

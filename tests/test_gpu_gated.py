@@ -198,7 +198,7 @@ def test_shapes_strides_and_partial_gradients():
     assert torch.all(out == 5.0)
 
 
-@pytest.mark.parametrize("t,m,n", [(40, 2000, 300), (100, 640, 128), (200, 3000, 40), (130, 513, 1000)])
+@pytest.mark.parametrize("t,m,n", [(40, 2100, 300), (100, 2560, 128), (200, 3000, 40), (130, 4095, 1000)])
 def test_split_depth_of_few_tokens(t, m, n):
     """With few tokens the 2 m terms of dX are summed in shares."""
     X, Wg, Wu, dH = _make(t, m, n, BF16, seed=4)
