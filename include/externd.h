@@ -25,7 +25,8 @@
  *   the work finished, because the return code carries the device status --
  *   except the factorizations given an async_status int (externd_options,
  *   externd_batch_options), which return once their work is queued and deliver
- *   the status through that int, and externd_matvec.
+ *   the status through that int, externd_matvec, and the 4-bit and gated
+ *   feed-forward operators (see there).
  * - The library keeps no pointer after return (an asynchronous call's queued
  *   work still uses the caller's buffers until the stream reaches its end).
  *   Workspace (the residual in two layouts, each entry an fp32 pair hi + lo;
@@ -266,7 +267,8 @@ int externd_pack_mask_sign(const uint8_t* T, int64_t rows, int64_t len, uint8_t*
  * current device (EXTERND_EINVAL otherwise).  Matrices are row-major with an explicit leading
  * dimension in ELEMENTS (at least the number of columns); element types are EXTERND_F32,
  * EXTERND_F16 or EXTERND_BF16.  Calls are stream-ordered and asynchronous unless noted; they
- * allocate nothing and keep nothing between calls, so they can be captured into CUDA graphs.
+ * allocate nothing (the synchronous externd_int4_quantize: 4 bytes, in stream order) and keep
+ * nothing between calls, so they can be captured into CUDA graphs.
  * Outputs must not overlap inputs.  Sums are held in fp32.  The first call of an entry point on a device may
  * load device code there: make it before any stream capture.  A device-side wait that gave up (2 s; it does
  * not happen unless the device stops) leaves NaN in the results of the 4-bit products.

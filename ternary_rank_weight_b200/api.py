@@ -576,7 +576,7 @@ _handle_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _rows_in(t, cols: int, name: str, like: Optional[torch.Tensor] = None) -> torch.Tensor:
+def _rows_in(t, cols: int, name: str) -> torch.Tensor:
     """A 2-D CUDA tensor with `cols` columns of unit stride (copied otherwise) and one of the element
     types; rows may be strided."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda or t.dtype not in _DTYPE:
@@ -584,8 +584,6 @@ def _rows_in(t, cols: int, name: str, like: Optional[torch.Tensor] = None) -> to
     rows, width = t.shape
     if width != cols:
         raise ValueError(f"{name} must have {cols} columns, not {width}")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must have the element type and device of the other tensors")
     if rows:
         ld, step = t.stride()
         if (step != 1 and cols > 1) or (rows > 1 and ld < cols):
