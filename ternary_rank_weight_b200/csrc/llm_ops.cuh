@@ -73,7 +73,7 @@ __device__ __forceinline__ float act_fn(float g) {
     } else if constexpr (ACT == EXTERND_ACT_GELU_TANH) {
         return g * sigmoid<PRECISE>(1.5957691216057308f * g * fmaf(0.044715f * g, g, 1.0f));
     } else {
-        const float r = g > 0.0f ? g : g * 0.0f;   // 0 for g <= 0, NaN stays
+        const float r = g <= 0.0f ? 0.0f : g;      // NaN stays
         return r * r;
     }
 }
@@ -92,7 +92,7 @@ __device__ __forceinline__ float2 act_both(float g) {
         const float s = sigmoid<PRECISE>(1.5957691216057308f * g * (1.0f + c)), a = g * s;
         return make_float2(a, fmaf(a * (1.0f - s), 1.5957691216057308f * fmaf(3.0f, c, 1.0f), s));
     } else {
-        const float r = g > 0.0f ? g : g * 0.0f;
+        const float r = g <= 0.0f ? 0.0f : g;
         return make_float2(r * r, 2.0f * r);
     }
 }

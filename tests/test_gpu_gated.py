@@ -165,6 +165,17 @@ def test_large_magnitudes_of_the_gate():
             assert not torch.isnan(g).any()
 
 
+def test_relu2_of_an_overflowed_gate():
+    """A projection past the 16-bit range: relu2 and its gradient are 0 on the negative side."""
+    X = torch.full((1, 64), 60000.0, dtype=F16, device="cuda")
+    Wg, Wu = torch.full((16, 64), -60000.0, dtype=F16, device="cuda"), torch.ones(16, 64, dtype=F16, device="cuda")
+    for t in (1, 20):
+        H, G, Up = ext.gated_forward(X.expand(t, 64), Wg, Wu * 1e-4, "relu2", save_dtype=F16)
+        assert not H.any() and torch.isinf(G).all()
+        for g in ext.gated_backward(torch.ones_like(H), X.expand(t, 64), Wg, Wu * 1e-4, G, Up, "relu2"):
+            assert not g.any()
+
+
 def test_shapes_strides_and_partial_gradients():
     t, m, n = 60, 130, 100
     X, Wg, Wu, dH = _make(t, m, n, BF16)
