@@ -350,11 +350,12 @@ int externd_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const
                   int64_t ldgu, void* work, size_t work_bytes, int* async_status, void* stream);
 
 /* Gradients of the gated block: with dG = dH * U * act'(G) and dU = dH * act(G) (rounded to dtype, for the
- * tensor cores),
+ * tensor cores: in fp16 one past 65504 becomes infinite, and one below 2^-25 zero),
  *   dX = dG Wg + dU Wu (tokens x n),   dWg = dG^T X,   dWu = dU^T X (m x n, leading dimension lddw).
  *   dX, dWg, dWu  [out] any of them may be NULL: it is then not computed.  The inputs are needed (and
  *                       checked) only for what is computed: X for dWg and dWu, Wg and Wu for dX.
- *   G, U, save_dtype, ldgu  as externd_gated returned them.
+ *   G, U, save_dtype, ldgu  as externd_gated returned them.  An infinite entry (a projection past 65504 saved in
+ *                       fp16, say) counts as the largest finite value of save_dtype with its sign; NaN stays NaN.
  *   work          [tmp] as for externd_gated, with externd_gated_backward_work(m, n, tokens) bytes besides.
  * tokens = 0 sets dWg and dWu to 0.  The same call gives the same bits (no atomics). */
 size_t externd_gated_backward_work(int64_t m, int64_t n, int64_t tokens);

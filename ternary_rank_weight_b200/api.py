@@ -871,7 +871,8 @@ def gated_forward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str 
 def gated_backward(dH: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, G: torch.Tensor, U: torch.Tensor,
                    act: str = "silu", *, need=(True, True, True), async_status=None, stream=None):
     """(dX, dWg, dWu) from the gradient dH of gated_forward's H and the G and U it returned
-    (externd_gated_backward); need: which of the three to compute (None in place of the others)."""
+    (externd_gated_backward); need: which of the three to compute (None in place of the others).  Infinite entries of
+    G and U (projections past 65504 saved in float16) count as the type's largest value."""
     m, n, dev, dtype = _gated_inputs(X, Wg, Wu)
     code = _act(act)
     _check_status(async_status, dev)

@@ -374,6 +374,13 @@ template <typename T> __device__ __forceinline__ float2 pair_of(const F8& v, int
     return e == 0 ? make_float2(v.a.x, v.a.y) : e == 1 ? make_float2(v.a.z, v.a.w) : e == 2 ? make_float2(v.b.x, v.b.y) : make_float2(v.b.z, v.b.w);
 }
 
+// A projection that was saved as infinite (fp16: past 65504) counts as the type's largest value: act and act' are at their
+// limits there (silu, gelu, gelu_tanh: 0 or g, and 0 or 1), where infinity itself would meet them as 0 * inf.  NaN stays.
+template <typename S> struct Largest { static constexpr float value = FLT_MAX; };
+template <> struct Largest<__half> { static constexpr float value = 65504.0f; };
+template <> struct Largest<__nv_bfloat16> { static constexpr float value = 3.38953139e38f; };
+template <typename S> __device__ __forceinline__ float finite(float v) { return fabsf(v) > Largest<S>::value ? copysignf(Largest<S>::value, v) : v; }
+
 // 8 columns a thread; hvec, svec: dH's rows, G's and U's, start on 16-byte boundaries.  S: float, or the operands' 16 bits.
 template <typename T, typename S, int ACT>
 __global__ void __launch_bounds__(256) gate_grad_kernel(const T* __restrict__ dh, int64_t lddh, int hvec, const S* __restrict__ gs,
@@ -384,6 +391,7 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const T* __restrict__ dh
         return;
     }
     const int64_t per = ldw / 8;                           // ldw: m rounded up to 8
+    using Saved = typename std::conditional<std::is_same<S, float>::value, float, T>::type;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / per, k = 8 * (i - r * per);
         const uint4 h8 = load8(reinterpret_cast<const unsigned short*>(dh + r * lddh), k, m, hvec);
@@ -392,8 +400,9 @@ __global__ void __launch_bounds__(256) gate_grad_kernel(const T* __restrict__ dh
         #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float2 h = pair_of<T>(h8, e), g = pair_of<T>(g8, e), u = pair_of<T>(u8, e);
-            const float2 a = act_both<ACT, false>(g.x), b = act_both<ACT, false>(g.y);
-            og[e] = pack2<T>(h.x * u.x * a.y, h.y * u.y * b.y);
+            const float2 a = act_both<ACT, false>(finite<Saved>(g.x)), b = act_both<ACT, false>(finite<Saved>(g.y));
+            // dH act' first: a derivative of 0 makes 0 of any U, where dH U may be past the fp32 range
+            og[e] = pack2<T>(h.x * a.y * finite<Saved>(u.x), h.y * b.y * finite<Saved>(u.y));
             ou[e] = pack2<T>(h.x * a.x, h.y * b.x);
         }
         *reinterpret_cast<uint4*>(dg + r * ldw + k) = make_uint4(og[0], og[1], og[2], og[3]);

@@ -92,8 +92,9 @@ __device__ __forceinline__ float2 act_both(float g) {
         const float s = sigmoid<PRECISE>(1.5957691216057308f * g * (1.0f + c)), a = g * s;
         return make_float2(a, fmaf(a * (1.0f - s), 1.5957691216057308f * fmaf(3.0f, c, 1.0f), s));
     } else {
-        const float r = g <= 0.0f ? 0.0f : g;
-        return make_float2(r * r, 2.0f * r);
+        // finite where the square leaves the fp32 range, so that a gradient of 0 stays 0
+        const float r = g <= 0.0f ? 0.0f : g, a = r * r, d = 2.0f * r;
+        return make_float2(a > FLT_MAX ? FLT_MAX : a, d > FLT_MAX ? FLT_MAX : d);
     }
 }
 

@@ -176,6 +176,50 @@ def test_relu2_of_an_overflowed_gate():
             assert not g.any()
 
 
+@pytest.mark.parametrize("dtype,save", [(F16, F16), (F16, torch.float32), (BF16, BF16), (BF16, torch.float32)])
+@pytest.mark.parametrize("act", ACTS)
+def test_gradients_of_infinite_projections(act, dtype, save):
+    """Saved projections that are infinite count as the type's largest value: act is then 0 or g (relu2 0 or g^2), act'
+    0 or 1 (relu2 0 or 2 g), and nothing becomes NaN.  Where the products leave the range, dH is 0 and so are they."""
+    inf, big = float("inf"), torch.finfo(save).max
+    for t in (1, 20):
+        m, n = 24, 40
+        X, Wg, Wu, _ = _make(t, m, n, dtype, seed=9)
+        gv = torch.tensor([inf, -inf, inf, -inf, 1.0, 1.0] * 4, dtype=torch.float64, device="cuda")
+        uv = torch.tensor([0.5, 0.5, inf, -inf, inf, 0.5] * 4, dtype=torch.float64, device="cuda")
+        dH = torch.full((t, m), 2.0 ** -22, dtype=dtype, device="cuda")
+        if save != F16:                                 # past every 16-bit product: gradients of 0
+            dH[:, (gv > 0) & (torch.isinf(gv) | torch.isinf(uv))] = 0
+        elif act == "relu2":
+            dH[:, 2::6] = 0                             # 2 65504^2 of it
+        G, Up = gv.to(save).expand(t, m).contiguous(), uv.to(save).expand(t, m).contiguous()
+        g, u = gv.clamp(-big, big), uv.clamp(-big, big)
+        f, df = act64(act, torch.where(g.abs() > 1, g.sign(), g))
+        far = g.abs() > 1
+        pos = (g > 0).double()
+        f = torch.where(far, pos * (g * g if act == "relu2" else g), f)
+        df = torch.where(far, pos * (2 * g if act == "relu2" else 1.0), df)
+        r = dH.double()
+        dg, du = r * df * u, r * f
+        assert max(dg.abs().max(), du.abs().max()) < (65000 if dtype == F16 else 3e38)
+        # the limits are exact, the activation at 1 has its error (as in _check_backward); products and one rounding
+        edf, ef = (torch.where(far, 0.0, act_eps(g) * v) for v in ((df.abs() + 1 + f.abs()) * 4, f.abs()))
+        eg, eu = (r * u).abs() * edf + 4 * U * dg.abs(), r.abs() * ef + 4 * U * du.abs()
+        eg, eu = (e * (1 + 2.0 ** -8) + half_step(dtype, v) * (1 + 2.0 ** -8) for e, v in ((eg, dg), (eu, du)))
+        got = ext.gated_backward(dH, X, Wg, Wu, G, Up, act)
+        x, wg, wu = X.double(), Wg.double(), Wu.double()
+        want = (dg @ wg + du @ wu, dg.t() @ x, du.t() @ x)
+        err = (eg @ wg.abs() + eu @ wu.abs(), eg.t() @ x.abs(), eu.t() @ x.abs())
+        mag = (dg.abs() @ wg.abs() + du.abs() @ wu.abs(), dg.abs().t() @ x.abs(), du.abs().t() @ x.abs())
+        for a, v, e, s in zip(got, want, err, mag):
+            assert torch.all((a.double() - v).abs() <= (e + (2 * m + 24) * U * (s + e)) * (1 + 2.0 ** -8) + half_step(dtype, v))
+        G[-1, 3] = float("nan")                         # NaN is passed on
+        dX, dWg, dWu = ext.gated_backward(dH, X, Wg, Wu, G, Up, act)
+        assert torch.isnan(dX[-1]).all() and torch.isnan(dWg[3]).all() and torch.isnan(dWu[3]).all()
+        keep = [i for i in range(m) if i != 3]
+        assert not torch.isnan(dX[:-1]).any() and torch.equal(dWg[keep], got[1][keep]) and torch.equal(dWu[keep], got[2][keep])
+
+
 def test_shapes_strides_and_partial_gradients():
     t, m, n = 60, 130, 100
     X, Wg, Wu, dH = _make(t, m, n, BF16)
