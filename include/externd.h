@@ -364,6 +364,11 @@ int externd_gated_backward(const void* dH, int64_t lddh, const void* X, int64_t 
                            int dtype, int64_t m, int64_t n, int64_t tokens, int act, void* dX, int64_t lddx, void* dWg,
                            void* dWu, int64_t lddw, void* work, size_t work_bytes, int* async_status, void* stream);
 
+/* Test hook: the gated block's and the 4-bit products' tile kernels, in the calls of this thread from now on.  Each
+ * device-side wait gives up after wait_limit_s seconds (0.001 to 2; 0 = 2), and the products of worker `withhold` (a
+ * CTA or a pair of CTAs, counted from 1; 0 = none) are not made, so that the waits for them run out. */
+int externd_debug_wait_fault(double wait_limit_s, int withhold);
+
 /* Human-readable message for a status code (static storage). */
 const char* externd_strerror(int status);
 

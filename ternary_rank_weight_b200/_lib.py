@@ -40,6 +40,7 @@ EXPORTS = (
     "externd_aligned_bytes",
     "externd_gated_backward_work",
     "externd_gated_backward",
+    "externd_debug_wait_fault",
 )
 
 
@@ -192,5 +193,7 @@ def load():
     L.externd_gated_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, c_int, i64, c_int, i64, i64, i64, c_int,
                                          vp, i64, vp, vp, i64, vp, sz, vp, vp]
     L.externd_gated_backward.restype = c_int
+    L.externd_debug_wait_fault.argtypes = [ctypes.c_double, c_int]
+    L.externd_debug_wait_fault.restype = c_int
     _lib = L
     return L

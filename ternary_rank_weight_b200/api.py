@@ -466,6 +466,18 @@ def debug_start_trits(m: int, k: int, tau: float, seed: int, device="cuda", *, s
     return out
 
 
+@contextlib.contextmanager
+def debug_wait_fault(withhold: int, wait_limit_s: float = 0.05):
+    """Within: the gated block's and the 4-bit products' tile kernels, called from this thread, do not make the products
+    of worker `withhold` (counted from 1), so that the waits for them run out (externd_debug_wait_fault)."""
+    L = _lib.load()
+    _check(L.externd_debug_wait_fault(float(wait_limit_s), int(withhold)), "externd_debug_wait_fault")
+    try:
+        yield
+    finally:
+        L.externd_debug_wait_fault(0.0, 0)
+
+
 # ---------------------------------------------------------------------------
 # host codecs of the packed 2-bit format: 00 = 0, 01 = +1, 11 = -1
 # ---------------------------------------------------------------------------

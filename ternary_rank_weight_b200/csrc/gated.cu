@@ -62,6 +62,7 @@ struct GemmArgs {
     float* part;             // BWD, main.splits > 1: the shares' sums (splits x tokens x ldp) instead of dX
     int64_t ldp;
     int* status;             // may be null
+    WaitFault fault;
 };
 
 struct Tile { bool grad; int r, c, split, first, last; };    // stages first .. last - 1
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
     __shared__ __align__(8) uint64_t bars[2 * C::STAGES + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ int quit_flag;
+    __shared__ uint32_t issued[2];                                  // stages that each CTA of the pair sent loads for
     const uint32_t base = (smem_u32(raw) + 1023) & ~1023u;          // swizzle atoms are 1024-byte aligned
     unsigned char* const stg_base = raw + (base - smem_u32(raw)) + C::STAGES * C::STAGE;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -190,6 +192,11 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
     const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
     const uint32_t b_bytes = (uint32_t)(g.width / CG) * (BK * 2);     // a CTA's share of a stage's B
 
+    // wait until the loads of stage i have landed
+    const auto land = [&](int i) {
+        const uint64_t t0 = timer_ns();
+        while (!mbar_try(full0 + 8 * (i % C::STAGES), (i / C::STAGES) & 1) && timer_ns() - t0 < WAIT_LIMIT_NS) {}
+    };
     if (warp == 0 && lane == 0) {
         // ---- loads: each CTA fetches its 128 rows of A and its share of B; both complete on the leader's barrier
         int it = 0;
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         for (int i = 0; ok && tile_of(g, worker, workers, i, t); ++i) {
             for (int kb = t.first; kb < t.last; ++kb, ++it) {
                 const int s = it % C::STAGES;
-                if (!mbar_wait(empty0 + 8 * s, ((it / C::STAGES) & 1) ^ 1, quit)) { ok = false; break; }
+                if (!mbar_wait(empty0 + 8 * s, ((it / C::STAGES) & 1) ^ 1, quit, g.fault.limit_ns)) { ok = false; break; }
                 const uint32_t sa = base + s * C::STAGE, sb = sa + 128 * BK * 2;
                 uint32_t bar = full0 + 8 * s;
                 if (rank == 0) mbar_expect(bar, CG * (128 * BK * 2 + b_bytes));
@@ -229,21 +236,21 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         }
         if (rank == 0) {
             // leave only when every issued load has landed (with a limit each)
-            const int last = it < C::STAGES ? it : C::STAGES;
-            for (int i = it - last; i < it; ++i) {
-                const uint64_t t0 = timer_ns();
-                while (!mbar_try(full0 + 8 * (i % C::STAGES), (i / C::STAGES) & 1) && timer_ns() - t0 < WAIT_LIMIT_NS) {}
-            }
+            for (int i = max(0, it - C::STAGES); i < it; ++i) land(i);
+        }
+        if constexpr (CG == 2) {
+            issued[rank] = it;
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_rank(smem_u32(&issued[rank]), rank ^ 1)), "r"(it) : "memory");
         }
     } else if (warp == 1 && rank == 0) {
-        // ---- products
+        // ---- products.  (Nothing in the loop needs the whole warp: where a wait runs out, lanes may leave it one by one)
         const bool leader = elect_one();
         constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
         // along K: 8-row groups 1024 bytes apart, 32 bytes per 16 elements of depth.  Along M or N: 64-element
         // boxes BK * 128 bytes apart, 8-deep groups 1024 bytes apart, 2048 bytes per 16 elements of depth.
         constexpr uint32_t box = 64 * BK * 2;
         int s = 0, phase = 0, n = 0;
-        bool ok = true;
+        bool ok = worker + 1 != g.fault.withhold;
         Tile t;
         for (; ok && tile_of(g, worker, workers, n, t); ++n) {
             const bool a_mn = MODE == BWD && t.grad, b_mn = MODE == BWD;
@@ -251,10 +258,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
             const uint32_t a_lbo = a_mn ? box : 16, b_lbo = b_mn ? box : 16, a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
             const int kbs = t.last - t.first;
             const uint32_t acc = tmem + (n & 1) * ACC;
-            if (!mbar_wait(tempty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, quit)) break;
+            if (!mbar_wait(tempty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, quit, g.fault.limit_ns)) break;
             fence_after();
             for (int kb = 0; kb < kbs; ++kb) {
-                if (!mbar_wait(full0 + 8 * s, phase, quit)) { ok = false; break; }
+                if (!mbar_wait(full0 + 8 * s, phase, quit, g.fault.limit_ns)) { ok = false; break; }
                 fence_after();
                 const uint32_t sa = base + s * C::STAGE, sb = sa + 128 * BK * 2;
                 const uint64_t da = smem_desc(sa, a_lbo, 1024), db = smem_desc(sb, b_lbo, 1024);
@@ -264,13 +271,12 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
                     mma_commit<CG>(empty0 + 8 * s);
                     if (kb == kbs - 1) mma_commit<CG>(tfull0 + 8 * (n & 1));
                 }
-                __syncwarp();
                 if (++s == C::STAGES) { s = 0; phase ^= 1; }
             }
         }
-        if (*quit && leader) {
+        if (leader) {
             // issued products end before the tensor memory is freed
-            mma_commit<CG>(drain);
+            mma_commit<CG>(drain, 1);
             const uint64_t t0 = timer_ns();
             while (!mbar_try(drain, 0) && timer_ns() - t0 < WAIT_LIMIT_NS) {}
         }
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         const unsigned char* stg_ptr = stg_base + (warp - 4) * 32 * STG_ROW;
         Tile t;
         for (int n = 0; tile_of(g, worker, workers, n, t); ++n) {
-            if (!mbar_wait(tfull0 + 8 * (n & 1), (n >> 1) & 1, quit)) break;
+            if (!mbar_wait_warp(tfull0 + 8 * (n & 1), (n >> 1) & 1, quit, g.fault.limit_ns)) break;
             fence_after();
             const uint32_t acc = tmem + (n & 1) * ACC + ((uint32_t)(32 * w) << 16);
             if constexpr (MODE == FWD) {
@@ -351,7 +357,19 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
     }
     __syncthreads();
     if (threadIdx.x == 0 && quit_flag && g.status) atomicExch(g.status, EXTERND_ETIMEOUT);
-    if constexpr (CG == 2) cluster_sync();
+    if constexpr (CG == 2) {
+        cluster_sync();
+        if (issued[0] != issued[1]) {
+            // The CTAs gave up at different stages.  Loads complete on CTA 0's barriers, which do not yet expect what CTA 1
+            // alone sent: its own 128 rows of A and share of B
+            if (rank == 0 && threadIdx.x == 0)
+                for (int i = (int)issued[0]; i < (int)issued[1]; ++i) {
+                    mbar_expect(full0 + 8 * (i % C::STAGES), 128 * BK * 2 + b_bytes);
+                    land(i);
+                }
+            cluster_sync();
+        }
+    }
     if (warp == 1) {
         fence_after();
         tmem_free<CG>(tmem, 512);
@@ -606,6 +624,7 @@ int forward_tiles(const Call& c, int width) {
     g.grad.splits = 1;
     g.width = width;
     g.act = c.act;
+    g.fault = wait_fault();
     g.h = c.H; g.ldh = c.ldh; g.s[0] = c.S[0]; g.s[1] = c.S[1]; g.lds = c.lds; g.save32 = c.save_dtype == EXTERND_F32;
     g.status = c.status;
     return launch_gemm<T, FWD, CG>(maps, g, c.stream) == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
@@ -694,6 +713,7 @@ int backward_tiles(const Call& c, const T* dg, const T* du, int64_t ldd, float* 
     Maps maps = {};
     g.width = width;
     g.status = c.status;
+    g.fault = wait_fault();
     g.main.splits = g.grad.splits = 1;
     if (c.dX) {
         if (!make_map(&maps.a[0], dg, c.tokens, c.m, ldd, 128, c.dtype) || !make_map(&maps.a[1], du, c.tokens, c.m, ldd, 128, c.dtype) ||
@@ -780,9 +800,25 @@ bool good_saved(const Device& dev, const Call& c) {
 
 }  // namespace externd_ffn
 
+namespace externd_llm {
+
+WaitFault& wait_fault() {
+    thread_local WaitFault f;
+    return f;
+}
+
+}  // namespace externd_llm
+
 using namespace externd_ffn;
 
 extern "C" {
+
+int externd_debug_wait_fault(double wait_limit_s, int withhold) {
+    if (!(wait_limit_s == 0.0 || (wait_limit_s >= 0.001 && wait_limit_s <= 2.0)) || withhold < 0) return EXTERND_EINVAL;
+    wait_fault().limit_ns = wait_limit_s == 0.0 ? WAIT_LIMIT_NS : (uint64_t)(wait_limit_s * 1e9);
+    wait_fault().withhold = withhold;
+    return EXTERND_OK;
+}
 
 size_t externd_aligned_bytes(int dtype, int64_t rows, int64_t n) {
     return rows < 1 || n < 1 || !valid_dtype(dtype) ? 0 : plane_bytes(rows, n, dtype_bytes(dtype));

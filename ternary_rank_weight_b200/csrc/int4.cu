@@ -548,7 +548,7 @@ template <typename X, int N> __host__ __device__ constexpr int tc_smem() {
 template <typename X, typename T, int N, int NM, int WORDS, bool AFFINE>
 __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, int64_t m, int64_t n, int act, const X* __restrict__ x,
                                                              int64_t ldx, int64_t batch, X* __restrict__ y, int64_t ldy,
-                                                             int splits) {
+                                                             int splits, const WaitFault fault) {
     using Raw = typename Raw8<X>::type;
     constexpr int PLANES = Raw8<X>::PLANES;
     using XE = typename std::conditional<PLANES == 3, float, unsigned short>::type;
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
             for (int u = 0; u < AHEAD; ++u) {
                 const int blk = b0 + u;
                 if (blk >= last) break;
-                if (!mbar_wait(empty0 + 8 * s, phase, quit)) { ok = false; break; }
+                if (!mbar_wait(empty0 + 8 * s, phase, quit, fault.limit_ns)) { ok = false; break; }
                 const uint32_t st = base + s * STAGE, at = st + place;
                 asm volatile("cp.async.wait_group %0;" ::"n"(TC_CODES - 1) : "memory");
                 const uint4 code[2] = {lds128(cring + slot), lds128(cring + slot + TC_PROD * 512)};
@@ -684,19 +684,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == TC_EPI) {
-        // ---- products
+        // ---- products.  (Nothing in the loop needs the whole warp: where a wait runs out, lanes may leave it one by one)
         const bool leader = elect_one();
         constexpr uint32_t idesc = f16_idesc(std::is_same<T, __half>::value ? 0 : 1, false, false, 128, N);
         const uint64_t a0 = smem_desc(base, 16, 1024), one = smem_desc(ones, 16, 1024);
         int s = 0, phase = 0, d = 0, dphase = 1;
-        bool ok = true;
+        bool ok = (int)blockIdx.x + 1 != fault.withhold;
         for (int blk = first; blk < last && ok; ++blk) {
-            if (!mbar_wait(full0 + 8 * s, phase, quit)) break;
+            if (!mbar_wait(full0 + 8 * s, phase, quit, fault.limit_ns)) break;
             fence_after();
             const uint64_t da = a0 + (uint32_t)(s * (STAGE >> 4));   // the address field counts 16 bytes
             #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
-                if (!mbar_wait(dempty0 + 8 * d, dphase, quit)) { ok = false; break; }
+                if (!mbar_wait(dempty0 + 8 * d, dphase, quit, fault.limit_ns)) { ok = false; break; }
                 fence_after();
                 const uint32_t acc = tmem + d * N;
                 if (leader) {
@@ -714,7 +714,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
                     mma_commit<1>(dfull0 + 8 * d);
                     if (g == GROUPS - 1) mma_commit<1>(empty0 + 8 * s);
                 }
-                __syncwarp();
                 if (++d == TC_BUFS) { d = 0; dphase ^= 1; }
             }
             if (++s == STAGES) { s = 0; phase ^= 1; }
@@ -759,7 +758,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
                 ps += m;
                 if (AFFINE && po) po += m;
                 const int d = i % TC_BUFS;
-                if (!mbar_wait(dfull0 + 8 * d, (g / TC_BUFS) & 1, quit)) { ok = false; break; }
+                if (!mbar_wait_warp(dfull0 + 8 * d, (g / TC_BUFS) & 1, quit, fault.limit_ns)) { ok = false; break; }
                 fence_after();
                 const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + d * N + (warp >> 2) * W;
                 uint32_t v[W], x1[W];
@@ -883,7 +882,7 @@ cudaError_t launch_tile4(const Product& p) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = splits > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p.w0, p.w1, p.m, p.n, p.act, (const X*)p.x, p.ldx, p.batch, (X*)p.y, p.ldy, splits);
+    return cudaLaunchKernelEx(&cfg, kernel, p.w0, p.w1, p.m, p.n, p.act, (const X*)p.x, p.ldx, p.batch, (X*)p.y, p.ldy, splits, wait_fault());
 }
 
 template <typename X, typename T, int NM, int WORDS, bool AFFINE>

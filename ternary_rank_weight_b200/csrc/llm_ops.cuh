@@ -137,6 +137,15 @@ inline int sm_count() {
     return v;
 }
 
+// ---- waits -----------------------------------------------------------------------------------------
+
+constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;   // per wait, as for the factorizations
+
+// The limit of the tile kernels' waits, and the worker whose products are withheld (counted from 1; 0: none), so that
+// the waits for them run out: externd_debug_wait_fault sets both for the calls of its thread.
+struct WaitFault { uint64_t limit_ns = WAIT_LIMIT_NS; int withhold = 0; };
+WaitFault& wait_fault();                            // gated.cu
+
 // ---- warp-level matrix product ---------------------------------------------------------------------
 //
 // d += a b for a 16 x 16 and b 16 x 8, fp32 accumulation.  Lane 4 r + c holds a's rows r and r + 8 and b's

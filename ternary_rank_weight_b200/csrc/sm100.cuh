@@ -43,11 +43,9 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-constexpr uint64_t WAIT_LIMIT_NS = 2000000000ull;   // per wait, as for the factorizations
-
-// Wait for a phase.  Gives up after WAIT_LIMIT_NS, or when another warp of the CTA gave up: the CTA then
-// leaves its loops and the launch reports EXTERND_ETIMEOUT.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* quit) {
+// One thread waits for a phase.  It gives up after limit ns, or when another warp of the CTA gave up: the CTA then leaves
+// its loops and the launch reports EXTERND_ETIMEOUT.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* quit, uint64_t limit) {
     if (mbar_try(bar, parity)) return true;
     uint64_t t0 = 0;
     for (;;) {
@@ -57,7 +55,22 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         if (*quit) return false;
         const uint64_t t = timer_ns();
         if (t0 == 0) t0 = t;
-        else if (t - t0 > WAIT_LIMIT_NS) { *quit = 1; return false; }
+        else if (t - t0 > limit) { *quit = 1; return false; }
+    }
+}
+
+// A warp waits for a phase, and goes on or gives up as one: what follows are instructions of whole warps, which lanes
+// that saw `quit` and lanes that saw the phase complete must not meet apart.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* quit, uint64_t limit) {
+    if (__all_sync(FULL, mbar_try(bar, parity))) return true;
+    uint64_t t0 = 0;
+    for (;;) {
+        #pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (__all_sync(FULL, mbar_try(bar, parity))) return true;
+        const uint64_t t = timer_ns();
+        if (t0 == 0) t0 = t;
+        if (__any_sync(FULL, *quit != 0 || t - t0 > limit)) { *quit = 1; return false; }
     }
 }
 
@@ -82,14 +95,14 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
                      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate) : "memory");
 }
 
-// arrive on `bar` (in both CTAs of a pair) when the MMAs issued so far have finished
+// arrive on `bar` (of the CTAs in `ctas` of a pair) when the MMAs issued so far have finished
 template <int CG>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t ctas = 3) {
     if constexpr (CG == 1)
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
     else
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                     ::"r"(bar), "h"((uint16_t)3) : "memory");
+                     ::"r"(bar), "h"(ctas) : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {

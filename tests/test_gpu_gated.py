@@ -220,6 +220,28 @@ def test_gradients_of_infinite_projections(act, dtype, save):
         assert not torch.isnan(dX[:-1]).any() and torch.equal(dWg[keep], got[1][keep]) and torch.equal(dWu[keep], got[2][keep])
 
 
+# tokens, m, n: single CTAs; pairs; a split dX on pairs; several tiles a worker, pairs
+@pytest.mark.parametrize("t,m,n", [(20, 100, 72), (300, 1111, 777), (130, 4095, 1000), (1100, 6900, 500)])
+def test_waits_that_run_out_end_with_a_status(t, m, n):
+    """The products of one worker are withheld (a host-set flag): every wait for them gives up, the status says so, and
+    the next call is as ever."""
+    X, Wg, Wu, dH = _make(t, m, n, BF16, seed=11)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ref = ext.gated_forward(X, Wg, Wu, async_status=st)
+    gref = ext.gated_backward(dH, X, Wg, Wu, *ref[1:], async_status=st)
+    assert int(st.item()) == 0
+    for worker in (1, 2):
+        with ext.debug_wait_fault(worker):
+            ext.gated_forward(X, Wg, Wu, async_status=st)
+            late = int(st.item())
+            ext.gated_backward(dH, X, Wg, Wu, *ref[1:], async_status=st)
+        assert late == ext.STATUS["ETIMEOUT"] and int(st.item()) == ext.STATUS["ETIMEOUT"]
+        again = ext.gated_forward(X, Wg, Wu, async_status=st)
+        assert int(st.item()) == 0 and all(torch.equal(a, b) for a, b in zip(again, ref))
+        again = ext.gated_backward(dH, X, Wg, Wu, *ref[1:], async_status=st)
+        assert int(st.item()) == 0 and all(torch.equal(a, b) for a, b in zip(again, gref))
+
+
 def test_shapes_strides_and_partial_gradients():
     t, m, n = 60, 130, 100
     X, Wg, Wu, dH = _make(t, m, n, BF16)

@@ -263,6 +263,20 @@ def test_every_share_of_the_columns(blocks):
     assert torch.equal(got, ext.int4_matvec(w, X))
 
 
+@pytest.mark.parametrize("t,m,n", [(9, 100, 100), (20, 300, 2000), (64, 1000, 1500)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_waits_that_run_out_leave_nan(t, m, n, dtype):
+    """The products of one CTA are withheld (a host-set flag): its waits give up and its tile is NaN, the others' tiles
+    are right, and so is the next call."""
+    w, X = _random_weights(m, n, 64, True, seed=t), _vectors(t, n, t, dtype)
+    ref, href = ext.int4_matvec(w, X), ext.int4_gated(w, w, X)
+    with ext.debug_wait_fault(1):
+        y, h = ext.int4_matvec(w, X), ext.int4_gated(w, w, X)
+    for got, want, rows in ((y, ref, 128), (h, href, 64)):
+        assert torch.isnan(got[:, :rows]).all() and torch.equal(got[:, rows:], want[:, rows:])
+    assert torch.equal(ext.int4_matvec(w, X), ref) and torch.equal(ext.int4_gated(w, w, X), href)
+
+
 def test_calls_on_two_streams_at_once():
     w, big = _random_weights(700, 2000, 64, True, seed=1), _random_weights(3000, 1024, 128, False, seed=2)
     X, Z = _vectors(30, 2000, 1, BF16), _vectors(5, 1024, 2, F32)

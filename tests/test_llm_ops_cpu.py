@@ -84,6 +84,15 @@ def test_gated_entry_points_reject_bad_arguments_before_device_work():
     assert L.externd_gated_backward_work(6912, 2560, 64) > 2 * 64 * 6912 * 2
 
 
+def test_wait_fault_hook_checks_its_arguments():
+    L = _lib.load()
+    for limit, worker in ((-1.0, 0), (float("nan"), 0), (1e-6, 0), (2.5, 0), (float("inf"), 0), (0.1, -1)):
+        assert L.externd_debug_wait_fault(limit, worker) == EINVAL
+    with ext.debug_wait_fault(3):
+        pass
+    assert L.externd_debug_wait_fault(0.0, 0) == 0
+
+
 def test_gated_binding_rejects_bad_tensors():
     x, w = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(8, 16, dtype=torch.bfloat16)
     for args in ((x, w, w), (x[:, :8], w, w), (x, w, w[:4]), (None, w, w), (x, None, w), (x.float(), w.float(), w.float())):
