@@ -271,7 +271,7 @@ int externd_pack_mask_sign(const uint8_t* T, int64_t rows, int64_t len, uint8_t*
  * nothing between calls, so they can be captured into CUDA graphs.
  * Outputs must not overlap inputs.  Sums are held in fp32.  The first call of an entry point on a device may
  * load device code there: make it before any stream capture.  A device-side wait that gave up (2 s; it does
- * not happen unless the device stops) leaves NaN in the results of the 4-bit products.
+ * not happen unless the device stops) leaves NaN in the results that depended on it.
  * ------------------------------------------------------------------------- */
 
 typedef enum { EXTERND_F32 = 0, EXTERND_F16 = 1, EXTERND_BF16 = 2 } externd_dtype;
@@ -343,7 +343,7 @@ int externd_int4_gated(const uint8_t* qg, const void* scale_g, const void* offse
  *                    Wu start on 16-byte boundaries, otherwise externd_aligned_bytes(dtype, rows, n) bytes for
  *                    each of the three whose rows do not.
  *   async_status  NULL, or a device int that receives EXTERND_OK, or EXTERND_ETIMEOUT if a device-side
- *                    wait gave up (2 s; the outputs are then unspecified), when the stream gets there.
+ *                    wait gave up (2 s; outputs that were not reached are then NaN), when the stream gets there.
  * tokens = 0 computes nothing. */
 int externd_gated(const void* X, int64_t ldx, const void* Wg, int64_t ldg, const void* Wu, int64_t ldu, int dtype,
                   int64_t m, int64_t n, int64_t tokens, int act, void* H, int64_t ldh, void* G, void* U, int save_dtype,

@@ -135,6 +135,18 @@ __device__ __forceinline__ void store64(const uint32_t* v, uint32_t stg, const u
     __syncwarp();
 }
 
+// NaN in a warp's share of a tile: 32 rows, every other 32 of the columns col0 + turn .. end - 1
+template <typename T>
+__device__ __noinline__ void store_nan(uint32_t stg, const unsigned char* stg_ptr, T* out, int64_t ld, int row0, int rows, int col0, int turn,
+                                       int end, int cols, int lane) {
+    uint32_t v[16];
+    for (int i = 0; i < 16; ++i) v[i] = 0x7fff7fffu;                    // NaN in fp32, fp16 and bf16
+    if (row0 >= rows) return;
+    for (int c = turn; c < end; c += 64)
+        for (int e = c; e < c + 32; e += 64 / (int)sizeof(T))
+            if (col0 + e < cols) store64<T>(v, stg, stg_ptr, out, ld, row0, rows, col0 + e, cols, lane);
+}
+
 template <typename T, int ACT>
 __device__ __forceinline__ void gate_chunk(const uint32_t (&g)[32], const uint32_t (&u)[32], uint32_t (&h)[16]) {
     #pragma unroll
@@ -287,8 +299,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         const uint32_t stg = smem_u32(stg_base) + (warp - 4) * 32 * STG_ROW;
         const unsigned char* stg_ptr = stg_base + (warp - 4) * 32 * STG_ROW;
         Tile t;
-        for (int n = 0; tile_of(g, worker, workers, n, t); ++n) {
-            if (!mbar_wait_warp(tfull0 + 8 * (n & 1), (n >> 1) & 1, quit, g.fault.limit_ns)) break;
+        int n = 0;
+        bool late = false;
+        for (; tile_of(g, worker, workers, n, t); ++n) {
+            if (!mbar_wait_warp(tfull0 + 8 * (n & 1), (n >> 1) & 1, quit, g.fault.limit_ns)) { late = true; break; }
             fence_after();
             const uint32_t acc = tmem + (n & 1) * ACC + ((uint32_t)(32 * w) << 16);
             if constexpr (MODE == FWD) {
@@ -352,6 +366,24 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
                 uint32_t bar = tempty0 + 8 * (n & 1);
                 bar = map_rank(bar, 0);
                 mbar_arrive_cluster(bar);
+            }
+        }
+        // a wait gave up: NaN instead of what the outputs' memory held, whether or not the caller looks at a status
+        for (; late && tile_of(g, worker, workers, n, t); ++n) {
+            const int which = MODE == BWD && t.grad && t.r >= g.half_r;
+            const int row0 = (t.r - (which ? g.half_r : 0)) * C::BM + 128 * (int)rank + 32 * w;
+            const TileList& l = MODE == BWD && t.grad ? g.grad : g.main;
+            const int wide = MODE == FWD ? g.width / 2 : g.width, col0 = t.c * wide;
+            if (MODE == BWD && !t.grad && g.part) {
+                store_nan<float>(stg, stg_ptr, g.part + (int64_t)t.split * l.rows * g.ldp, g.ldp, row0, l.rows, col0, turn, wide, l.cols, lane);
+            } else if (MODE == BWD && t.grad) {
+                store_nan<T>(stg, stg_ptr, (T*)g.s[which], g.lds, row0, l.rows, col0, turn, wide, l.cols, lane);
+            } else {
+                store_nan<T>(stg, stg_ptr, (T*)g.h, g.ldh, row0, l.rows, col0, turn, wide, l.cols, lane);
+                for (int i = 0; MODE == FWD && g.s[0] && i < 2; ++i) {
+                    if (g.save32) store_nan<float>(stg, stg_ptr, (float*)g.s[i], g.lds, row0, l.rows, col0, turn, wide, l.cols, lane);
+                    else store_nan<T>(stg, stg_ptr, (T*)g.s[i], g.lds, row0, l.rows, col0, turn, wide, l.cols, lane);
+                }
             }
         }
     }

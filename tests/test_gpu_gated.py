@@ -242,6 +242,25 @@ def test_waits_that_run_out_end_with_a_status(t, m, n):
         assert int(st.item()) == 0 and all(torch.equal(a, b) for a, b in zip(again, gref))
 
 
+@pytest.mark.parametrize("save", [torch.float32, BF16])
+@pytest.mark.parametrize("t,m,n", [(20, 100, 72), (300, 1111, 777), (130, 4095, 1000), (1100, 6900, 500)])
+def test_waits_that_run_out_leave_nan(t, m, n, save):
+    """Without a status the outputs themselves show it: what the withheld worker did not reach is NaN, all else is right."""
+    X, Wg, Wu, dH = _make(t, m, n, BF16, seed=12)
+    ref = ext.gated_forward(X, Wg, Wu, save_dtype=save)
+    gref = ext.gated_backward(dH, X, Wg, Wu, *ref[1:])
+    torch.full((8, *gref[1].shape), 7.0, device="cuda")              # memory that the next outputs may get
+    with ext.debug_wait_fault(1):
+        got = ext.gated_forward(X, Wg, Wu, save_dtype=save)
+        ggot = ext.gated_backward(dH, X, Wg, Wu, *ref[1:])
+        alone = ext.gated_backward(dH, X, Wg, Wu, *ref[1:], need=(False, True, True))
+    nan = [torch.isnan(v) for v in got]
+    assert nan[0].any() and not nan[0].all() and torch.equal(nan[0], nan[1]) and torch.equal(nan[0], nan[2])
+    assert any(torch.isnan(v).any() for v in ggot) and any(torch.isnan(v).any() for v in alone[1:])
+    for a, b in zip((*got, *ggot, *alone[1:]), (*ref, *gref, *gref[1:])):
+        assert torch.equal(torch.where(torch.isnan(a), b, a), b)
+
+
 def test_shapes_strides_and_partial_gradients():
     t, m, n = 60, 130, 100
     X, Wg, Wu, dH = _make(t, m, n, BF16)
