@@ -594,14 +594,9 @@ bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64
 
 template <typename T, int MODE, int CG>
 cudaError_t launch_gemm(const Maps& maps, const GemmArgs& g, cudaStream_t s) {
-    static bool attr[64] = {};   // set once per device of the process
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
-    if (dev < 0 || dev >= 64 || !attr[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<T, MODE, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<CG>::SMEM);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) attr[dev] = true;
-    }
+    static PerDevice done;
+    const cudaError_t e = allow_smem(gemm_kernel<T, MODE, CG>, Cfg<CG>::SMEM, done);
+    if (e != cudaSuccess) return e;
     const int tiles = g.main.tiles_r * g.main.tiles_c * g.main.splits + g.grad.tiles_r * g.grad.tiles_c, slots = sm_count() / CG;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((tiles < slots ? tiles : slots) * CG));

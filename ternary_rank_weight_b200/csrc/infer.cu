@@ -17,6 +17,7 @@
 // trits of its 16-byte chunks and reads the vector through L1 (rowdot_kernel).
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <vector>
 
@@ -506,7 +507,7 @@ template <int NB, int R>
 cudaError_t launch_tdot(const uint8_t* T, int64_t rows, int64_t len, int64_t tb, const float* V, int64_t vstride,
                         const float* scale, float* out, int64_t ostride, bool dependent, cudaStream_t s) {
     const size_t smem = tdot_smem_bytes(NB, tb);
-    static bool attr[64] = {};   // set once per device of the process
+    static std::atomic<bool> attr[64];   // set once per device of the process; several host threads may be the first
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
     if (dev < 0 || dev >= 64 || !attr[dev]) {

@@ -831,22 +831,11 @@ struct Product {
     cudaStream_t stream;
 };
 
-// dynamic shared memory of a kernel, once per device of the process
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, bool (&done)[64]) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
-    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
-    return e;
-}
-
 template <typename X, typename T, int NM, int WORDS, bool AFFINE>
 cudaError_t launch_vec4(const Product& p) {
     const auto kernel = vec4_kernel<X, T, NM, WORDS, AFFINE>;
     constexpr int smem = VEC_WARPS * VEC_DEPTH * NM * 1024;
-    static bool done[64] = {};
+    static PerDevice done;
     const cudaError_t e = allow_smem(kernel, smem, done);
     if (e != cudaSuccess) return e;
     const bool vec = row_aligned(p.x, p.batch, p.ldx, sizeof(X));
@@ -859,7 +848,7 @@ template <typename X, typename T, int NM, int WORDS, bool AFFINE, int N>
 cudaError_t launch_tile4(const Product& p) {
     const auto kernel = tile4_kernel<X, T, N, NM, WORDS, AFFINE>;
     constexpr int smem = tc_smem<X, N>();
-    static bool done[64] = {};
+    static PerDevice done;
     const cudaError_t e = allow_smem(kernel, smem, done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.m + 128 / NM - 1) / (128 / NM), cols = (p.batch + N - 1) / N, blocks = (p.n + 127) / 128;

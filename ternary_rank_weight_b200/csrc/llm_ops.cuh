@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
 #include <cstdint>
 
@@ -135,6 +136,19 @@ inline int sm_count() {
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
     cudaGetLastError();
     return v;
+}
+
+// Dynamic shared memory of a kernel, set once per device of the process.  Several host threads may be the first.
+using PerDevice = std::atomic<bool>[64];
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, PerDevice& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
+    const bool known = dev >= 0 && dev < 64;
+    if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_release);
+    return e;
 }
 
 // ---- waits -----------------------------------------------------------------------------------------

@@ -331,6 +331,26 @@ def test_calls_on_two_streams_at_once():
         assert all(torch.equal(p, q) for p, q in zip((*f, *g), (*refs[i], *grads[i])))
 
 
+def test_host_threads_at_once():
+    """Several host threads, each on a stream of its own, through every kernel whose launch keeps something per device."""
+    from concurrent.futures import ThreadPoolExecutor
+    X, Wg, Wu, dH = _make(200, 256, 384, F16, seed=13)
+    w = ext.int4_quantize(Wg, 64)
+
+    def calls(stream):
+        f = ext.gated_forward(X, Wg, Wu, stream=stream)
+        return (*f, *ext.gated_backward(dH, X, Wg, Wu, *f[1:], stream=stream), ext.int4_matvec(w, X[:3], stream=stream),
+                ext.int4_matvec(w, X[:30], stream=stream), ext.int4_gated(w, w, X[:64], stream=stream))
+
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(8)]
+    with ThreadPoolExecutor(8) as pool:
+        got = list(pool.map(calls, streams))
+    torch.cuda.synchronize()
+    ref = calls(None)
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, ref))
+
+
 def test_results_past_32_bit_offsets():
     """2.4 G entries of H: the last tokens' are those of a call of their own."""
     t, m, n = 40100, 60000, 64
