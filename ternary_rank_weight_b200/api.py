@@ -624,7 +624,7 @@ def _operand(t, cols: int, name: str, dtype: torch.dtype, device: torch.device):
     dimension and the workspace it takes if its rows do not start on 16-byte boundaries
     (externd_aligned_bytes)."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor on {device}")
+        raise ValueError(f"{name} must be a 2-D {dtype} tensor on {device}")
     rows, width = t.shape
     if width != cols:
         raise ValueError(f"{name} must have {cols} columns, not {width}")
@@ -638,6 +638,15 @@ def _operand(t, cols: int, name: str, dtype: torch.dtype, device: torch.device):
     if ptr & 15 or (rows > 1 and ld * size & 15):
         return t, ptr, ld, (rows * ((cols * size + 15) // 16 * 16) + 255) // 256 * 256
     return t, ptr, ld, 0
+
+
+def _flat(t: torch.Tensor) -> torch.Tensor:
+    return t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
+
+
+def _check_out(out, shape):
+    if out is not None and (not isinstance(out, torch.Tensor) or out.shape != shape or (out.dim() > 2 and not out.is_contiguous())):
+        raise ValueError(f"out must have shape {shape} (and be contiguous with more than two dimensions)")
 
 
 def _act(act: str) -> int:
@@ -728,13 +737,13 @@ def int4_dequantize(w: Int4Weights, dtype: torch.dtype = torch.float32, *, strea
 
 
 def int4_matvec(w: Int4Weights, X: torch.Tensor, *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Y = X W^T for X of shape (batch, n) or (n,), in X's element type (externd_int4_matvec)."""
+    """Y = X W^T for X of shape (..., n), in X's element type (externd_int4_matvec)."""
     return _int4_products((w,), X, 0, out, stream)
 
 
 def int4_gated(wg: Int4Weights, wu: Int4Weights, X: torch.Tensor, act: str = "silu", *,
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """H = act(X Wg^T) * (X Wu^T) for X of shape (batch, n) or (n,), in X's element type
+    """H = act(X Wg^T) * (X Wu^T) for X of shape (..., n), in X's element type
     (externd_int4_gated); act: "silu", "gelu", "gelu_tanh" or "relu2"."""
     if isinstance(wg, Int4Weights) and isinstance(wu, Int4Weights) and (wg.m, wg.n, wg.group) != (wu.m, wu.n, wu.group):
         raise ValueError("both matrices must have the same shape and group")
@@ -744,18 +753,20 @@ def int4_gated(wg: Int4Weights, wu: Int4Weights, X: torch.Tensor, act: str = "si
 def _int4_products(ws, X, act: int, out, stream) -> torch.Tensor:
     if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dtype not in _DTYPE:
         raise ValueError("X must be a float32, float16 or bfloat16 CUDA tensor")
-    dev, dtype = X.device, X.dtype
+    dev, dtype, w = X.device, X.dtype, ws[0]
     mats = []
     for w in ws:
         _check_int4(w, dev)
         mats += (w.q.data_ptr(), w.scale.data_ptr(), None if w.offset is None else w.offset.data_ptr())
-    squeeze = X.dim() == 1
+    if X.dim() < 1 or X.shape[-1] != w.n:
+        raise ValueError(f"X's last dimension must be {w.n}")
+    two = X.dim() == 2
+    shape = (X.shape[0], w.m) if two else (*X.shape[:-1], w.m)
+    _check_out(out, shape)
     with _guard(stream, dev):
-        X2, x, ldx, nbytes = _operand(X.unsqueeze(0) if squeeze else X, w.n, "X", dtype, dev)
-        if out is not None and squeeze:
-            out = out.unsqueeze(0)
+        X2, x, ldx, nbytes = _operand(_flat(X), w.n, "X", dtype, dev)
         batch = X2.shape[0]
-        Y = _result(out, batch, w.m, X2)
+        Y = _result(None if out is None else out.view(-1, w.m), batch, w.m, X2)
         work = None
         if nbytes and batch > 8:
             work = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
@@ -766,7 +777,7 @@ def _int4_products(ws, X, act: int, out, stream) -> torch.Tensor:
         else:
             rc = _lib.load().externd_int4_gated(*mats, w.m, w.n, w.group, act, *tail)
     _check(rc, "externd_int4_matvec" if len(ws) == 1 else "externd_int4_gated")
-    return Y[0] if squeeze else Y
+    return Y if two else Y.view(shape)
 
 
 def _int4_places(n: int):
@@ -820,18 +831,13 @@ def _gated_inputs(X, Wg, Wu):
     return m, n, X.device, X.dtype
 
 
-def _flat(t: torch.Tensor) -> torch.Tensor:
-    return t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
-
-
 def _gated(X, Wg, Wu, act, save, out, async_status, stream):
     m, n, dev, dtype = _gated_inputs(X, Wg, Wu)
     code = _act(act)
     _check_status(async_status, dev)
     two = X.dim() == 2
     shape = (X.shape[0], m) if two else (*X.shape[:-1], m)
-    if out is not None and (not isinstance(out, torch.Tensor) or out.shape != shape or (out.dim() > 2 and not out.is_contiguous())):
-        raise ValueError(f"out must have shape {shape} (and be contiguous with more than two dimensions)")
+    _check_out(out, shape)
     if save is not None and save != torch.float32 and save != dtype:
         raise ValueError("the projections can be saved in float32 or in X's type")
     with _guard(stream, dev):

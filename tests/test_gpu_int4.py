@@ -202,6 +202,28 @@ def test_products_shapes_strides_and_outputs():
     assert ext.int4_gated(w, w, big[:0, 8:208]).shape == (0, 70)
 
 
+def test_products_take_any_leading_dimensions():
+    """(batch, sequence, n) and more, as the dense block does; each row as in a call with two dimensions."""
+    w = _random_weights(70, 200, 64, True, seed=4)
+    X = _vectors(24, 200, 2, BF16)
+    y, h = ext.int4_matvec(w, X), ext.int4_gated(w, w, X)
+    for lead in ((4, 6), (2, 3, 4), (1, 24)):
+        assert torch.equal(ext.int4_matvec(w, X.view(*lead, 200)), y.view(*lead, 70))
+        assert torch.equal(ext.int4_gated(w, w, X.view(*lead, 200)), h.view(*lead, 70))
+    out = torch.zeros(4, 6, 70, dtype=BF16, device="cuda")
+    got = ext.int4_matvec(w, X.view(6, 4, 200).transpose(0, 1), out=out)
+    assert got.data_ptr() == out.data_ptr() and torch.equal(out, y.view(6, 4, 70).transpose(0, 1))
+    one = torch.zeros(70, dtype=BF16, device="cuda")
+    assert ext.int4_matvec(w, X[0], out=one).shape == (70,) and torch.equal(one, ext.int4_matvec(w, X[0]))
+    assert ext.int4_matvec(w, X.view(4, 6, 200)[:0]).shape == (0, 6, 70)
+    for bad, kw in ((X[:, :199], {}), (X[0, 0], {}), (X, dict(out=out)), (X.view(4, 6, 200), dict(out=out[:, :5])), (X[0], dict(out=[0])),
+                    (X[0], dict(out=torch.zeros(140, dtype=BF16, device="cuda")[::2])), (X, dict(out=y.float()))):
+        with pytest.raises(ValueError):
+            ext.int4_matvec(w, bad, **kw)
+    with pytest.raises(ValueError, match="last dimension must be 200"):
+        ext.int4_matvec(w, X.view(4, 6, 200)[..., :100])
+
+
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 def test_rows_do_not_influence_one_another(dtype):
     w = _random_weights(40, 300, 64, True, seed=9)
