@@ -619,6 +619,26 @@ def _result(out, rows: int, cols: int, like: torch.Tensor) -> torch.Tensor:
     return out
 
 
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two matrices with unit column stride may share memory.  Side by side in the rows of one buffer (equal
+    row strides) they do not."""
+    if a.numel() == 0 or b.numel() == 0 or a.device != b.device:
+        return False
+    (pa, ra, la, wa), (pb, rb, lb, wb) = ((t.data_ptr(), t.shape[0], _ld(t) * t.element_size(), t.shape[1] * t.element_size())
+                                          for t in (a, b))
+    if pa + (ra - 1) * la + wa <= pb or pb + (rb - 1) * lb + wb <= pa:
+        return False
+    if ra > 1 and rb > 1 and la == lb:
+        d = (pb - pa) % la                       # where b's rows start within a's period
+        return d < wa or d + wb > la
+    return True
+
+
+def _check_apart(out, *inputs):
+    if any(_overlap(out, t) for t in inputs):
+        raise ValueError("out must not share memory with the inputs: they are still read while it is written")
+
+
 def _operand(t, cols: int, name: str, dtype: torch.dtype, device: torch.device):
     """A 2-D operand (copied where its columns are not of unit stride): the tensor, its address, its leading
     dimension and the workspace it takes if its rows do not start on 16-byte boundaries
@@ -737,14 +757,15 @@ def int4_dequantize(w: Int4Weights, dtype: torch.dtype = torch.float32, *, strea
 
 
 def int4_matvec(w: Int4Weights, X: torch.Tensor, *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Y = X W^T for X of shape (..., n), in X's element type (externd_int4_matvec)."""
+    """Y = X W^T for X of shape (..., n), in X's element type (externd_int4_matvec); out must not share memory with
+    X."""
     return _int4_products((w,), X, 0, out, stream)
 
 
 def int4_gated(wg: Int4Weights, wu: Int4Weights, X: torch.Tensor, act: str = "silu", *,
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """H = act(X Wg^T) * (X Wu^T) for X of shape (..., n), in X's element type
-    (externd_int4_gated); act: "silu", "gelu", "gelu_tanh" or "relu2"."""
+    (externd_int4_gated); act: "silu", "gelu", "gelu_tanh" or "relu2"; out must not share memory with X."""
     if isinstance(wg, Int4Weights) and isinstance(wu, Int4Weights) and (wg.m, wg.n, wg.group) != (wu.m, wu.n, wu.group):
         raise ValueError("both matrices must have the same shape and group")
     return _int4_products((wg, wu), X, _act(act), out, stream)
@@ -767,6 +788,8 @@ def _int4_products(ws, X, act: int, out, stream) -> torch.Tensor:
         X2, x, ldx, nbytes = _operand(_flat(X), w.n, "X", dtype, dev)
         batch = X2.shape[0]
         Y = _result(None if out is None else out.view(-1, w.m), batch, w.m, X2)
+        if out is not None:
+            _check_apart(Y, X2)
         work = None
         if nbytes and batch > 8:
             work = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
@@ -846,6 +869,8 @@ def _gated(X, Wg, Wu, act, save, out, async_status, stream):
         Wu, wu, ldu, bu = _operand(Wu, n, "Wu", dtype, dev)
         t = X2.shape[0]
         H = _result(None if out is None else out.view(-1, m), t, m, X2)
+        if out is not None:
+            _check_apart(H, X2, Wg, Wu)
         G = U = None
         lds = m
         if save is not None:
@@ -871,7 +896,7 @@ def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu"
           async_status=None, stream=None) -> torch.Tensor:
     """H = act(X Wg^T) * (X Wu^T) for X of shape (..., n) and Wg, Wu of shape (m, n), float16 or bfloat16
     (externd_gated); act: "silu", "gelu", "gelu_tanh" or "relu2".  Operands whose rows do not start on 16-byte
-    boundaries are copied first.  The call is asynchronous; autograd does not record it (gated_forward and
+    boundaries are copied first; out must not share memory with them.  The call is asynchronous; autograd does not record it (gated_forward and
     gated_backward are the training pair).  async_status: an int32 CUDA tensor that receives the status."""
     return _gated(X, Wg, Wu, act, None, out, async_status, stream)[0]
 

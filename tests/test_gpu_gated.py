@@ -305,6 +305,25 @@ def test_split_depth_of_few_tokens(t, m, n):
     assert torch.equal(again[0], got[0])
 
 
+def test_outputs_that_share_memory_with_inputs_are_refused():
+    """In place, a row's results would be written while other CTAs still read the row."""
+    X, Wg, Wu, _ = _make(40, 64, 64, BF16, seed=14)
+    w = ext.int4_quantize(Wg, 64)
+    ref, y, h = ext.gated(X, Wg, Wu), ext.int4_matvec(w, X), ext.int4_gated(w, w, X)
+    for call in (lambda o: ext.gated(X, Wg, Wu, out=o), lambda o: ext.int4_matvec(w, X, out=o), lambda o: ext.int4_gated(w, w, X, out=o)):
+        with pytest.raises(ValueError, match="share memory"):
+            call(X)
+    with pytest.raises(ValueError, match="share memory"):
+        ext.gated(X, Wg, Wu, out=Wg[:40])
+    # side by side in one buffer is fine
+    both = torch.zeros(40, 128, dtype=BF16, device="cuda")
+    both[:, :64] = X
+    for call, want in ((lambda x, o: ext.gated(x, Wg, Wu, out=o), ref), (lambda x, o: ext.int4_matvec(w, x, out=o), y),
+                       (lambda x, o: ext.int4_gated(w, w, x, out=o), h)):
+        call(both[:, :64], both[:, 64:])
+        assert torch.equal(both[:, 64:], want) and torch.equal(both[:, :64], X)
+
+
 def test_one_vector_and_broadcast_gradient():
     X, Wg, Wu, _ = _make(1, 70, 40, BF16, seed=5)
     H, G, Up = ext.gated_forward(X[0], Wg, Wu)

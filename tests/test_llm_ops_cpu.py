@@ -84,6 +84,17 @@ def test_gated_entry_points_reject_bad_arguments_before_device_work():
     assert L.externd_gated_backward_work(6912, 2560, 64) > 2 * 64 * 6912 * 2
 
 
+def test_shared_memory_of_outputs_and_inputs_is_seen():
+    from ternary_rank_weight_b200.api import _overlap
+    buf = torch.zeros(20, 64, dtype=torch.bfloat16)
+    for a, b, want in [(buf[:, :30], buf[:, 30:], False), (buf[:, 30:], buf[:, :30], False), (buf[:, :31], buf[:, 30:], True),
+                       (buf[:, 30:], buf[:, :31], True), (buf, buf, True), (buf[:10], buf[10:], False), (buf[:11], buf[10:], True),
+                       (buf[:10, 40:], buf[9:, :41], True), (buf[:10, 40:], buf[9:, :40], False), (buf[:9, 40:], buf[9:, :41], False),
+                       (buf[3:4], buf[3:4, :5], True), (buf[3:4, :5], buf[3:4, 5:], False), (buf[::2], buf[1::2], False),   # rows in turn
+                       (buf[:0], buf, False), (buf, torch.zeros_like(buf), False), (buf[2:3, :8], buf[:, 8:], True)]:
+        assert _overlap(a, b) == want and _overlap(b, a) == want, (a.shape, b.shape)
+
+
 def test_wait_fault_hook_checks_its_arguments():
     L = _lib.load()
     for limit, worker in ((-1.0, 0), (float("nan"), 0), (1e-6, 0), (2.5, 0), (float("inf"), 0), (0.1, -1)):
