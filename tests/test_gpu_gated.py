@@ -117,6 +117,91 @@ def test_small_integers_are_exact(dtype):
         assert want.abs().max() < 256 and torch.equal(got.double(), want)
 
 
+# The shapes of tiles the host picks with 148 SMs: single CTAs 128, 192 and 256 columns wide, pairs 192 and 256 (pairs 128
+# wide serve all the small shapes above); the tall ones several tiles a worker.  n is several rings of stages deep, and ragged.
+FORWARD_PLANS = [(40, 5501, 453), (17, 9477, 453), (301, 5503, 453), (600, 6903, 453), (301, 6901, 453), (1101, 6905, 453)]
+# tokens, m, n, which gradients.  Pairs, dX unsplit, all workers with one dX tile or none, then some with two; single CTAs 256
+# wide, dX unsplit and split; dX alone on pairs and on single CTAs; dWg and dWu alone on pairs; split dX and dWg on pairs
+BACKWARD_PLANS = [(1101, 6901, 2503, (1, 1, 1)), (2101, 1301, 2507, (1, 1, 1)), (500, 101, 3501, (1, 1, 1)), (3, 5501, 1901, (1, 1, 1)),
+                  (901, 101, 2501, (1, 0, 0)), (9, 2003, 2501, (1, 0, 0)), (17, 1001, 131, (0, 1, 1)), (200, 4501, 1003, (1, 1, 0))]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("t,m,n", FORWARD_PLANS)
+def test_every_forward_plan(t, m, n, dtype):
+    for act, save in (("silu", torch.float32), ("relu2", dtype)):
+        X, Wg, Wu, _ = _make(t, m, n, dtype, seed=21)
+        H, G, Up = ext.gated_forward(X, Wg, Wu, act, save_dtype=save)
+        _check_forward(X, Wg, Wu, act, H, G, Up)
+        assert torch.equal(ext.gated(X, Wg, Wu, act), H)
+    # whole numbers whose sums are exact (as in test_small_integers_are_exact): a term lost or doubled shows
+    X = (X > 1.5).to(dtype)
+    Wg, Wu = ((w * n ** 0.5).round().clamp(-1, 1) for w in (Wg, Wu))
+    H, G, Up = ext.gated_forward(X, Wg, Wu, "relu2")
+    g64, u64 = X.double() @ Wg.double().t(), X.double() @ Wu.double().t()
+    assert 16 < g64.abs().max() < 128 and torch.equal(G.double(), g64) and torch.equal(Up.double(), u64)
+    assert torch.equal(H, (g64.clamp(min=0) ** 2 * u64).float().to(dtype))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("t,m,n,need", BACKWARD_PLANS)
+def test_every_backward_plan(t, m, n, need, dtype):
+    X, Wg, Wu, dH = _make(t, m, n, dtype, seed=22)
+    _, G, Up = ext.gated_forward(X, Wg, Wu)
+    got = ext.gated_backward(dH, X, Wg, Wu, G, Up, need=need)
+    assert [v is not None for v in got] == [bool(v) for v in need]
+    _check_backward(X, Wg, Wu, dH, "silu", G, Up, got)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(23)
+    X = (X > 1.5).to(dtype)
+    Wg, Wu = ((w * n ** 0.5).round().clamp(-1, 1) for w in (Wg, Wu))
+    G, Up = (torch.randint(-1, 2, (t, m), generator=gen, device="cuda").to(dtype) for _ in range(2))
+    dH = (torch.rand(t, m, generator=gen, device="cuda") < 0.1).to(dtype)
+    got = ext.gated_backward(dH, X, Wg, Wu, G, Up, "relu2", need=need)
+    dg, du = dH.double() * Up.double() * 2 * G.double().clamp(min=0), dH.double() * G.double().clamp(min=0) ** 2
+    for a, want in zip(got, (dg @ Wg.double() + du @ Wu.double(), dg.t() @ X.double(), du.t() @ X.double())):
+        assert a is None or (want.abs().max() < 256 and want.any() and torch.equal(a.double(), want))
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_gradients_match_differences_closely(act, dtype):
+    """As test_gradients_match_differences, along V = the sign of the exact gradient: every entry then adds its magnitude,
+    and the kernels' errors (one rounding of dG or dU, none of G and U, one of the result) stay a small fraction of the
+    sum, which is asserted: a gradient of zeros, or of another sign, fails."""
+    t, m, n = 40, 96, 72
+    X, Wg, Wu, dH = _make(t, m, n, dtype, seed=24)
+    _, G, Up = ext.gated_forward(X, Wg, Wu, act)
+    grads = ext.gated_backward(dH, X, Wg, Wu, G, Up, act)
+    x = [v.double() for v in (X, Wg, Wu)]
+
+    def f(a, b, c):
+        return (dH.double() * act64(act, a @ b.t())[0] * (a @ c.t())).sum()
+
+    g, u = x[0] @ x[1].t(), x[0] @ x[2].t()
+    a, da = act64(act, g)
+    dg, du = dH.double() * u * da, dH.double() * a
+    exact = [dg @ x[1] + du @ x[2], dg.t() @ x[0], du.t() @ x[0]]
+    terms = [dg.abs() @ x[1].abs() + du.abs() @ x[2].abs(), dg.abs().t() @ x[0].abs(), du.abs().t() @ x[0].abs()]
+    # the activation's and its derivative's fp32 errors, as in _check_backward
+    ea, eda = act_eps(g) * a.abs(), act_eps(g) * (da.abs() + 1 + a.abs()) * 4
+    eg, eu = (dH.double() * u).abs() * eda, dH.double().abs() * ea
+    fp32 = [eg @ x[1].abs() + eu @ x[2].abs(), eg.t() @ x[0].abs(), eu.t() @ x[0].abs()]
+    half = torch.finfo(dtype).eps / 2
+    for i in range(3):
+        V = exact[i].sign()
+        h = 1e-5
+        hi, lo = [v.clone() for v in x], [v.clone() for v in x]
+        hi[i] += h * V
+        lo[i] -= h * V
+        diff = (f(*hi) - f(*lo)) / (2 * h)
+        # dG's or dU's rounding in every term, the result's in every entry, sums of 2 m or t terms in fp32; the difference
+        # itself is off by the third derivative times (h sum |V W|)^2, below 1e-8, and by 2^-53 / h of the terms
+        bound = ((half * 1.01 + (2 * m + 24) * U + 1e-6) * terms[i] + 1.01 * fp32[i] + half * 1.01 * exact[i].abs()).sum()
+        assert bound < 0.1 * diff, (bound, diff)
+        assert (diff - (grads[i].double() * V).sum()).abs() <= bound
+
+
 def test_gradients_match_differences():
     """d/ds of sum(dH H(X + s V)) in 64 bits, by central differences of the formula, against the kernels'
     gradients contracted with V: the gradients' bound of one rounding chain (4 roundings of fp16, 2^-11 each,
