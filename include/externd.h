@@ -277,7 +277,7 @@ int externd_pack_mask_sign(const uint8_t* T, int64_t rows, int64_t len, uint8_t*
 typedef enum { EXTERND_F32 = 0, EXTERND_F16 = 1, EXTERND_BF16 = 2 } externd_dtype;
 
 /* act(g): silu g / (1 + e^-g); gelu g Phi(g) (Phi the normal distribution function); gelu_tanh
- * 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))); relu2 max(g, 0)^2. */
+ * 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))); relu2 max(g, 0)^2.  act(-inf) = 0. */
 typedef enum {
     EXTERND_ACT_SILU = 0,
     EXTERND_ACT_GELU = 1,

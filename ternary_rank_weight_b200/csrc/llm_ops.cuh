@@ -65,8 +65,16 @@ __device__ __forceinline__ float sigmoid(float v) {
     return __fdividef(1.0f, 1.0f + __expf(-v));
 }
 
+// -inf (a sum below the fp32 range) -> the least finite value, where the activations are at their limit 0; NaN stays
+__device__ __forceinline__ float not_minus_inf(float g) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(g), "f"(-FLT_MAX));
+    return r;
+}
+
 template <int ACT, bool PRECISE>
 __device__ __forceinline__ float act_fn(float g) {
+    g = not_minus_inf(g);
     if constexpr (ACT == EXTERND_ACT_SILU) {
         return g * sigmoid<PRECISE>(g);
     } else if constexpr (ACT == EXTERND_ACT_GELU) {

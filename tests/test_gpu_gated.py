@@ -261,6 +261,28 @@ def test_relu2_of_an_overflowed_gate():
             assert not g.any()
 
 
+@pytest.mark.parametrize("act", ACTS)
+def test_a_gate_below_the_fp32_range(act):
+    """Sums past -3.4e38 are -inf in fp32: every activation is 0 there (and inf above, where U is not 0)."""
+    for t in (1, 20):
+        X = torch.full((t, 64), 2.0 ** 70, dtype=BF16, device="cuda")
+        Wg = torch.full((24, 64), -2.0 ** 70, dtype=BF16, device="cuda")
+        Wg[1::2] *= -1
+        Wu = torch.full((24, 64), 2.0 ** -70, dtype=BF16, device="cuda")
+        H, G, Up = ext.gated_forward(X, Wg, Wu, act)
+        assert torch.isinf(G).all() and not H[:, ::2].any() and torch.isposinf(H[:, 1::2]).all()
+        Wg[2, 5] = float("nan")
+        assert torch.isnan(ext.gated(X, Wg, Wu, act)[:, 2]).all()
+        for dtype in (torch.float32, BF16):              # 4-bit weights: -7 s and 7 s of the greatest scale, X in the range
+            W = torch.full((24, 64), -4.4e5, device="cuda")
+            W[1::2] *= -1
+            w, one = ext.int4_quantize(W, 64, affine=False), ext.int4_quantize(torch.ones(24, 64, device="cuda"), 64, affine=False)
+            for rows in (1, 20):
+                Z = torch.full((rows, 64), 2.0 ** 114, dtype=dtype, device="cuda")
+                h = ext.int4_gated(w, one, Z, act)
+                assert not h[:, ::2].any() and torch.isposinf(h[:, 1::2]).all()
+
+
 @pytest.mark.parametrize("dtype,save", [(F16, F16), (F16, torch.float32), (BF16, BF16), (BF16, torch.float32)])
 @pytest.mark.parametrize("act", ACTS)
 def test_gradients_of_infinite_projections(act, dtype, save):
