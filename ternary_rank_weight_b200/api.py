@@ -665,7 +665,7 @@ def _flat(t: torch.Tensor) -> torch.Tensor:
 
 
 def _check_out(out, shape):
-    if out is not None and (not isinstance(out, torch.Tensor) or out.shape != shape or (out.dim() > 2 and not out.is_contiguous())):
+    if (not isinstance(out, torch.Tensor) or out.shape != shape or (out.dim() > 2 and not out.is_contiguous())):
         raise ValueError(f"out must have shape {shape} (and be contiguous with more than two dimensions)")
 
 
@@ -779,16 +779,18 @@ def _int4_products(ws, X, act: int, out, stream) -> torch.Tensor:
     for w in ws:
         _check_int4(w, dev)
         mats += (w.q.data_ptr(), w.scale.data_ptr(), None if w.offset is None else w.offset.data_ptr())
-    if X.dim() < 1 or X.shape[-1] != w.n:
-        raise ValueError(f"X's last dimension must be {w.n}")
     two = X.dim() == 2
-    shape = (X.shape[0], w.m) if two else (*X.shape[:-1], w.m)
-    _check_out(out, shape)
+    if not two and (X.dim() < 1 or X.shape[-1] != w.n):
+        raise ValueError(f"X's last dimension must be {w.n}")
+    if out is not None:
+        _check_out(out, (*X.shape[:-1], w.m))
     with _guard(stream, dev):
-        X2, x, ldx, nbytes = _operand(_flat(X), w.n, "X", dtype, dev)
+        X2, x, ldx, nbytes = _operand(X if two else _flat(X), w.n, "X", dtype, dev)
         batch = X2.shape[0]
-        Y = _result(None if out is None else out.view(-1, w.m), batch, w.m, X2)
-        if out is not None:
+        if out is None:
+            Y = X2.new_empty((batch, w.m))
+        else:
+            Y = _result(out.view(-1, w.m), batch, w.m, X2)
             _check_apart(Y, X2)
         work = None
         if nbytes and batch > 8:
@@ -800,7 +802,7 @@ def _int4_products(ws, X, act: int, out, stream) -> torch.Tensor:
         else:
             rc = _lib.load().externd_int4_gated(*mats, w.m, w.n, w.group, act, *tail)
     _check(rc, "externd_int4_matvec" if len(ws) == 1 else "externd_int4_gated")
-    return Y if two else Y.view(shape)
+    return Y if two else Y.view((*X.shape[:-1], w.m))
 
 
 def _int4_places(n: int):
@@ -860,7 +862,8 @@ def _gated(X, Wg, Wu, act, save, out, async_status, stream):
     _check_status(async_status, dev)
     two = X.dim() == 2
     shape = (X.shape[0], m) if two else (*X.shape[:-1], m)
-    _check_out(out, shape)
+    if out is not None:
+        _check_out(out, shape)
     if save is not None and save != torch.float32 and save != dtype:
         raise ValueError("the projections can be saved in float32 or in X's type")
     with _guard(stream, dev):
