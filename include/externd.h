@@ -262,13 +262,13 @@ int externd_pack_mask_sign(const uint8_t* T, int64_t rows, int64_t len, uint8_t*
 /* ---------------------------------------------------------------------------
  * 4-bit weights with group scales, and the gated feed-forward block.
  *
- * The uniform 4-bit format is what the pages compare the ternary factors with, and the gated
- * block is where a model's MLP matrices are used.  All pointers are DEVICE pointers of the
+ * 4-bit formats are what the pages compare the ternary factors' storage with (theirs has two levels of
+ * scales; this one, one level), and the gated block is where a model's MLP matrices are used.  All pointers are DEVICE pointers of the
  * current device (EXTERND_EINVAL otherwise).  Matrices are row-major with an explicit leading
  * dimension in ELEMENTS (at least the number of columns); element types are EXTERND_F32,
  * EXTERND_F16 or EXTERND_BF16.  Calls are stream-ordered and asynchronous unless noted; they
  * allocate nothing (the synchronous externd_int4_quantize: 4 bytes, in stream order) and keep
- * nothing between calls, so they can be captured into CUDA graphs.
+ * nothing between calls, so they can be captured into CUDA graphs (all but the synchronous quantiser).
  * Outputs must not overlap inputs.  Sums are held in fp32.  The first call of an entry point on a device may
  * load device code there: make it before any stream capture.  A device-side wait that gave up (2 s; it does
  * not happen unless the device stops) leaves NaN in the results that depended on it.
@@ -309,15 +309,17 @@ size_t externd_int4_row_bytes(int64_t n);
 int externd_int4_quantize(const void* A, int dtype, int64_t m, int64_t n, int64_t lda, int group, uint8_t* q_out,
                           void* scale_out, void* offset_out, int* async_status, void* stream);
 
-/* out (m x n, type dtype) = s (q - 8) + b, rounded once.  offset NULL: b = 0. */
+/* out (m x n, type dtype) = s (q - 8) + b, rounded to fp32 and then to dtype.  offset NULL: b = 0. */
 int externd_int4_dequantize(const uint8_t* q, const void* scale, const void* offset, int64_t m, int64_t n, int group,
                             void* out, int dtype, int64_t ldo, void* stream);
 
 /* Y = X W^T: Y[t] = W X[t] for t < batch (X batch x n, Y batch x m, both of type dtype; batch 0
  * does nothing).  q as externd_int4_quantize lays it out, 16-byte aligned; offset NULL: b = 0.
  * The codes enter the products exactly and each group's sum is scaled in fp32; fp32 inputs are
- * split without loss.  |X| up to 2^115: beyond that, and for infinite entries, a sum may become
- * inf or NaN before it is scaled.  Rows of X do not influence one another.
+ * split without loss (entries below 2^-110 in magnitude may lose up to 2^-133).  |X| up to 2^115: beyond that, and for
+ * infinite entries, a sum may become inf or NaN before it is scaled.  Rows of X do not influence one another.
+ * Any batch is taken; every 64 rows of X unpack the matrix again, so that from about 128 on (a prompt)
+ * externd_int4_dequantize and a dense product are faster.
  *   work       [tmp] NULL (work_bytes 0) for a batch of at most 8, or where the rows of X start on 16-byte
  *                    boundaries; otherwise 256-byte aligned, externd_aligned_bytes(dtype, batch, n) bytes, owned
  *                    by the caller. */

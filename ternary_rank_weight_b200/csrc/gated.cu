@@ -32,7 +32,7 @@ constexpr int ACC = 256;                   // accumulator columns; two accumulat
 constexpr int STG_ROW = 64;                // bytes of a staged row of outputs; its 16-byte pieces swizzled by the row: no bank conflicts
 
 // CG = 2: a pair of CTAs works on one tile of 256 rows, each fetching its 128 rows of A and half of B, so that B
-// crosses shared memory once for two SMs.  4096 tokens through 6912 x 2560: forward 191 us against 208 with CG = 1.
+// crosses shared memory once for two SMs.  4096 tokens through 6912 x 2560: forward 183 us against 207 with CG = 1.
 template <int CG> struct Cfg {
     static constexpr int BM = 128 * CG;                    // tile rows (128 per CTA)
     static constexpr int BBYTES = 256 / CG * BK * 2;       // a CTA's share of at most 256 B rows
@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
 // dG and dU from the saved projections
 // ---------------------------------------------------------------------------------------------------
 
-// Bound by memory: reads dH, G, U and writes dG, dU; 4096 tokens x 6912 with G, U in fp32: 396 MB in 55 us, 7.2 TB/s
-// (gelu: bound by erfc, half that rate).  dG and dU are rounded to the operands' type, which the
+// Bound by memory: reads dH, G, U and writes dG, dU; 4096 tokens x 6912 with G, U in fp32: 396 MB in 54 us, 7.4 TB/s
+// (gelu: bound by erfc, 80 us).  dG and dU are rounded to the operands' type, which the
 // tensor cores need.  Against a step that keeps everything in 32 bits this rounding makes the gradients' error
 // 1.4 times theirs (the output's rounding alone); G and U saved in 16 bits make it 1.8 times, with
 // relu2, which doubles their relative error, 2.5 times.
@@ -657,10 +657,12 @@ int forward_tiles(const Call& c, int width) {
     return launch_gemm<T, FWD, CG>(maps, g, c.stream) == cudaSuccess ? EXTERND_OK : EXTERND_ECUDA;
 }
 
-// Pairs of CTAs or single ones, and how wide the tiles: the fewest rounds, each weighted with its measured time.
-// Narrow tiles save little of it: shared memory writes and reads of both operands bound a round, and a narrower
-// tile still moves all of A.  4096 tokens x 6912 x 2560, us a round: pairs 14.3 / 13.2 / 12.1 at 256 / 192 / 128
-// columns, single CTAs 16.7 / 14.6 / 12.9.
+// Pairs of CTAs or single ones, and how wide the tiles: the fewest weighted rounds.  Narrow tiles save little of a round:
+// shared memory writes and reads of both operands bound it, and a narrower tile still moves all of A.  4096 tokens x 6912 x
+// 2560, us a round: pairs 15.3 / 12.3 / 10.5 at 256 / 192 / 128 columns, single CTAs 17.3 / 14.9 / 13.0.  The weights are not
+// those ratios (1, 0.80, 0.69; 1.13, 0.97, 0.85): calls of one or two rounds, where the choice matters most, have their
+// start and end besides.  Over 120 shapes (32 to 2048 tokens, 2048 to 11008 rows, depths 768 and 2560) the plan they
+// pick takes 2.0 % longer than the best of the six on average (at worst 22 %, at depth 768); the bare ratios' 2.8 % (32 %).
 template <typename T>
 int forward_tiles(const Call& c) {
     constexpr double ROUND[2][3] = {{1.22, 1.03, 0.91}, {1.00, 0.93, 0.85}};
@@ -778,8 +780,11 @@ int backward(const Call& c, const AlignJobs& jobs) {
     float* const part = (float*)(c.work + 2 * plane);
     const cudaError_t e = c.save_dtype == EXTERND_F32 ? gate_grad<T, float>(c, dg, du, ldd, jobs) : gate_grad<T, unsigned short>(c, dg, du, ldd, jobs);
     if (e != cudaSuccess) return EXTERND_ECUDA;
-    // as for the forward pass: the stages the busiest worker goes through, weighted with a stage's measured time
-    // (4096 x 6912 x 2560, whole pass: pairs 478 us, single CTAs 560, half as wide 795 with twice the stages)
+    // as for the forward pass: the stages the busiest worker goes through, weighted.  4096 x 6912 x 2560, whole pass: pairs
+    // 455 us, single CTAs 513, half as wide 756 with twice the stages; 1184 tokens: 158, 180, 257.  The second weight leans
+    // further to pairs than these times (1.13, 1.14): over 120 shapes (32 to 4096 tokens, 300 to 6912 rows, depths 300 to
+    // 2560) the plan taken is 2.8 % slower than the best of the three on average, at worst 45 % (32 tokens x 5504 x 768: 30.7 us,
+    // single CTAs 21.1), and with a weight of 1.14 it would be 0.9 % and 20 %.
     struct { int cg, width; double stage; } const shapes[3] = {{2, 256, 1.00}, {1, 256, 1.20}, {1, 128, 0.85}};
     int best_i = 0;
     double best = 1e300;

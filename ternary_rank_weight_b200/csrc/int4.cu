@@ -227,8 +227,8 @@ template <> __device__ __forceinline__ void codes8<__nv_bfloat16>(uint32_t w, ui
 // ---------------------------------------------------------------------------------------------------
 
 // VEC: rows of 16-bit values start on 16-byte boundaries.  Otherwise a warp's 256 values pass through shared memory, so
-// that neighbouring lanes store neighbouring columns (5196 x 3405 bf16: 13 us, 52 without).  2560 x 6912 bf16: 9 us,
-// 4.7 TB/s.
+// that neighbouring lanes store neighbouring columns (5196 x 3405 bf16: 13 us, 52 without).  2560 x 6912: bf16 9.4 us,
+// 4.8 TB/s; fp32 13.9 us, 5.8 TB/s.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) dequantize_kernel(const uint32_t* __restrict__ q, const __half* __restrict__ scale,
                                                          const __half* __restrict__ offset, int64_t m, int64_t n, int lg,
@@ -331,9 +331,11 @@ __device__ __forceinline__ void span_mma(float (&hi)[4], float (&lo)[4], const u
 // from shared memory: the codes would cross it as 16-bit floats, and of a tile's columns 16 at least.)
 // Every lane keeps the codes of its next VEC_DEPTH blocks in flight to shared memory (its own 16 bytes of each row:
 // no barrier, no registers); the scales, whose way from memory is as long, come four blocks ahead through
-// registers; the vectors' entries come from the first-level cache.  Bound by instructions: 163 a block of 128
+// registers; the vectors' entries come from the first-level cache.  163 instructions a block of 128
 // columns and 16 rows, 72 of them to unpack the codes.  8192 x 28672, one fp16 vector: 34 us, 3.5 TB/s (0.54 of
-// the measured copy rate).  Measured and not taken: bulk copies (a warp issues them one lane at a time: 271
+// the measured copy rate); issue slots are 62 % busy, no pipe above 48 %.  Its 512 equal CTAs are four on 68 SMs and
+// three on 80: the last end 1.16 times later than the average, and an SM with three has few warps to hide its waits.
+// Where an SM has one CTA (2560 rows: 160) the blocks' latency is the time.  Measured and not taken: bulk copies (a warp issues them one lane at a time: 271
 // instructions), the entries through the ring too (183), 32 rows a warp (the same time), 6 blocks ahead (slower).
 // The offsets' part b sum(x) takes sum(x) from the lanes that hold x (products with ones would double the work of
 // the warp-level products).
@@ -533,8 +535,11 @@ __global__ void __launch_bounds__(VEC_WARPS * 32) vec4_kernel(Mat4 w0, Mat4 w1, 
 // group's sum of x in every row.  The CTAs' sums meet through distributed shared memory in a fixed order.
 // (Weights scaled before the product would need no accumulator per group, but s (q - 8) + b does not fit 16
 // bits: measured against 64 bits that costs bf16 results 1.4 times the error of their own rounding.)
-// Bound by the latency of its stages: 64 vectors through 4096 x 4096 take 15.5 us, of which 4 until the first stage
-// is full and 3 to add up; the tensor memory's pipe is 18 percent busy.  (The same tile with warp-level products took
+// More than 64 vectors are tiles of 64 side by side, each of which unpacks its rows' codes again: 1537 vectors through
+// 2560 x 6912 take 183 us (298 TFLOP/s), 512 take 81, 128 22.5; dequantising and a dense library product take 47, 27
+// and 21.5.
+// Bound by the latency of its stages: 64 vectors through 4096 x 4096 take 15.4 us, of which 4 until the first stage
+// is full and 3 to add up; the tensor memory's pipe is 19 percent busy.  (The same tile with warp-level products took
 // 43 us: those run at a ninth of this rate.)
 constexpr int TC_EPI = 8, TC_PROD = 8, TC_THREADS = (TC_EPI + 1 + TC_PROD) * 32;
 template <int N> __host__ __device__ constexpr int tc_bufs() { return N == 64 ? 4 : 8; }     // accumulators in flight
@@ -852,8 +857,11 @@ cudaError_t launch_tile4(const Product& p) {
     const cudaError_t e = allow_smem(kernel, smem, done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.m + 128 / NM - 1) / (128 / NM), cols = (p.batch + N - 1) / N, blocks = (p.n + 127) / 128;
-    // shares of the columns: the fewest rounds of CTAs times the blocks of a share, each CTA costing about
-    // nine blocks' time (of 0.8 us) to start, fill its stages and add up
+    // Shares of the columns: the fewest rounds of CTAs times the blocks of a share, each CTA costing about
+    // nine blocks' time (of 0.8 us) to start, fill its stages and add up.  A round is counted as one CTA an SM, whole clusters
+    // or not.  Where the clusters of c CTAs do not fill the GPCs evenly that is too few: 2560 x 6912, 16 vectors, takes
+    // 7 shares (20 clusters) for one round and 22.3 us, where 6 shares take 12.7, 5 13.4, 4 15.1 and 1 35.6 (64 vectors: 29.1,
+    // 16.1, 17.2, 18.3, 45.2).  4096 x 4096, 64 vectors: 4 shares, 15.7 us, against 18.2 with 3 and 28.3 with 5.
     int splits = 1;
     int64_t best = INT64_MAX;
     for (int c = 1; c <= 8 && c <= blocks; ++c) {
@@ -966,7 +974,8 @@ template <typename T>
 cudaError_t run_dequantize(const uint8_t* q, const void* scale, const void* offset, int64_t m, int64_t n, int group, void* out,
                            int64_t ldo, cudaStream_t s) {
     const dim3 grid = row_grid(m, ((n + 127) / 128 + 7) / 8);
-    // fp32 rows always pass through shared memory: 16 bytes a lane, 32 apart, took 12 us where this takes 9
+    // fp32 rows always pass through shared memory: 16 bytes a lane, 32 apart, take 21.0 us for 2560 x 6912 where this
+    // takes 13.9 (8192 x 28672: 245 and 185)
     auto kernel = dequantize_kernel<T, false>;
     if constexpr (sizeof(T) == 2)
         if (row_aligned(out, m, ldo, sizeof(T))) kernel = dequantize_kernel<T, true>;

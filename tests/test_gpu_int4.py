@@ -248,6 +248,20 @@ def test_fp32_vectors_of_huge_and_tiny_range():
     assert torch.all((got - y).abs() <= _sum_bound(w, mag, X) * (1 + 2.0 ** -8) + half_step(F32, y))
 
 
+@pytest.mark.parametrize("t", [4, 20])
+def test_fp32_vectors_near_the_end_of_the_range(t):
+    """The third of an entry's three terms ends at bf16's least subnormal, 2^-133: what lies below it is lost."""
+    w = _random_weights(40, 300, 64, True, seed=10)
+    w.scale.fill_(1.0)
+    W, mag = _values64(w)
+    for e in (100, 112, 120, 126, 132, 140):
+        X = (_vectors(t, 300, 10, F32).double() * 2.0 ** -e).float()
+        y = X.double() @ W.t()
+        got = ext.int4_matvec(w, X).double()
+        lost = 2.0 ** -133 * mag.sum(1)
+        assert torch.all((got - y).abs() <= (_sum_bound(w, mag, X) + lost) * (1 + 2.0 ** -8) + half_step(F32, y))
+
+
 def test_products_repeat_bit_for_bit_on_streams_and_in_graphs():
     w = _random_weights(500, 1300, 128, True, seed=12)
     X = _vectors(24, 1300, 12, F16)
