@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
             const uint64_t t0 = timer_ns();
             while (!mbar_try(drain, 0) && timer_ns() - t0 < WAIT_LIMIT_NS) {}
         }
+        __syncwarp();                                          // lanes that left the loop apart
     } else if (warp >= 4) {
         // ---- epilogue: warp w reads lanes 32 (w % 4) .. + 31 of the accumulator, a row per thread, and every other
         // 32 columns
@@ -403,6 +404,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const __grid_constant_
         }
     }
     if (warp == 1) {
+        __syncwarp();
         fence_after();
         tmem_free<CG>(tmem, 512);
     }

@@ -688,6 +688,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();                                        // lanes that left the loop apart
     } else if (warp == TC_EPI) {
         // ---- products.  (Nothing in the loop needs the whole warp: where a wait runs out, lanes may leave it one by one)
         const bool leader = elect_one();
@@ -794,7 +795,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tile4_kernel(Mat4 w0, Mat4 w1, 
         #pragma unroll
         for (int t = 0; t < W; ++t) red[((warp >> 2) * W + t) * 128 + 32 * (warp & 3) + lane] = bad ? __uint_as_float(0x7fffffffu) : out[t];
     }
-    if (warp == TC_EPI) tmem_free<1>(tmem, COLUMNS);
+    if (warp == TC_EPI) {
+        __syncwarp();
+        tmem_free<1>(tmem, COLUMNS);
+    }
     if (splits > 1) cluster_sync();
     else __syncthreads();
     // each CTA of the cluster adds and stores a share of the rows, four at a time: neighbouring lanes, neighbouring rows,
